@@ -351,6 +351,39 @@ moe_status moe_gate_topk_bwd(const void *x, const void *Wg, const float *logits,
                              size_t ws_bytes, hipStream_t stream);
 
 /*
+ * moe_layer_fwd_few -- the whole layer (gate, top-k, expert FFNs, weighted
+ * sum) for a few tokens, forward only: one step of a serving loop.
+ *   y[t,:] = sum_{j=0..k-1} topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t,:])
+ * with the logits of moe_gate_topk (the same bits) and its choice (NaN logits
+ * rank below all others here), its gate weights (to fp32 rounding) and the FFN of moe_expert_ffn_fwd (the inner
+ * activation rounded to dt, every sum in fp32, y rounded once).  Each
+ * expert that any token chose is read once, whatever the number of tokens;
+ * experts no token chose are not read.  Nothing is kept for a backward.
+ *   x [T,d] dt, Wg [d,E] dt, logit_bias [E] float or NULL, W1 [E,d,f],
+ *   W3 [E,d,f] (SwiGLU only, else NULL), W2 [E,f,d] dt, y [T,d] dt (may not
+ *   overlap an input); logits [T,E] float, topk_idx [T,k] int32, topk_w [T,k]
+ *   float: written when not NULL (in the workspace otherwise).
+ *   ws: at least moe_layer_few_workspace_bytes(T,d,f,E,k,act,dt), 16-byte
+ *   aligned, no initial content needed; calls that may overlap in time need a
+ *   workspace each.
+ *   Limits: T <= 64 and T*k <= 4096, d and f multiples of 64, E <= 1024;
+ *   MOE_ERR_UNSUPPORTED for more tokens or pairs (the workspace query gives 0).
+ *   T = 0 launches nothing.
+ * Sources: ES-MoE review, 三 技术架构 (placement follows the gate; experts
+ * take their tokens without padding); FastMoE review, 제안 방법 (the experts'
+ * linear layers over the tokens each received).
+ */
+size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k,
+                                     moe_act act, moe_dtype dt);
+moe_status moe_layer_fwd_few(const void *x, const void *Wg,
+                             const float *logit_bias, const void *W1,
+                             const void *W3, const void *W2, int T, int d,
+                             int f, int E, int k, int renorm, moe_act act,
+                             moe_dtype dt, float *logits, int32_t *topk_idx,
+                             float *topk_w, void *y, void *ws,
+                             size_t ws_bytes, hipStream_t stream);
+
+/*
  * Kernel timing (benchmark support, off by default).
  * moe_profile_enable(capacity) creates 2*capacity HIP events; from then on
  * every kernel the library launches is bracketed by two of them on its

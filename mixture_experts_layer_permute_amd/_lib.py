@@ -44,6 +44,9 @@ SIGNATURES = {
     "moe_gate_bwd_workspace_bytes": (_Z, [_I, _I, _I]),
     "moe_gate_topk_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I,
                                _P, _P, _Z, _P]),
+    "moe_layer_few_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
+    "moe_layer_fwd_few": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P,
+                               _P, _P, _P, _P, _Z, _P]),
     "moe_mfma_loop": (_I, [_I, _I, _P, _Z, _P]),
     "moe_mfma_loop_random": (_I, [_I, _I, _P, _Z, _P]),
     "moe_lds_probe": (_I, [_I, _I, _I, _P, _Z, _P, _Z, _P]),

@@ -10,7 +10,7 @@ import math
 import torch
 
 from ._lib import MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F32, check, load
-from .ops import _stream
+from .ops import MoEError, _few_check, _need_gpu, _stream
 
 
 def _torch_stream(handle, device):
@@ -670,3 +670,77 @@ class OffloadedMoELayer:
     def step(self, stream=None):
         self.forward(stream)
         self.backward(stream)
+
+
+class FewTokenMoELayer:
+    """The layer's forward for a serving loop: 1 to 64 tokens a step, every
+    buffer allocated once (moe_layer_fwd_few; ES-MoE review, 三 技术架构: the
+    experts take the tokens the gate sends them, without padding).
+
+    The weights are the tensors of MoELayer (bind() keeps them, it copies
+    nothing, so a training step's update is seen by the next forward); the
+    routing is MoELayer's bit for bit.  forward(x) takes up to T tokens and
+    returns y [n,d]; logits, topk_idx and topk_w are of the last forward.
+    They and y are views of the layer's buffers, overwritten by the next
+    forward: two steps in flight at once (two streams, two captured graphs)
+    need a layer each.
+    """
+
+    def __init__(self, T, d, f, E, k, act="gelu", dtype=torch.bfloat16, renorm=1,
+                 device="cuda"):
+        self.T, self.d, self.f, self.E, self.k = T, d, f, E, k
+        self.act = MOE_ACT_SWIGLU if act == "swiglu" else MOE_ACT_GELU
+        self.dtype = dtype
+        self.dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+        self.renorm = renorm
+        self.device = torch.device(device)
+        L = self.lib = load()
+        dev = self.device
+        nb = L.moe_layer_few_workspace_bytes(T, d, f, E, k, self.act, self.dt)
+        if T < 1 or nb == 0:
+            raise MoEError("FewTokenMoELayer: 1 to 64 tokens, T*k <= 4096, d and f multiples "
+                           "of 64, 1 <= k <= E <= 1024")
+        # a smaller step may cut the reduction finer and need more workspace
+        nb = max(L.moe_layer_few_workspace_bytes(t, d, f, E, k, self.act, self.dt)
+                 for t in range(1, T + 1))
+        e = lambda *s, dt=dtype: torch.empty(*s, dtype=dt, device=dev)
+        self._y = e(T, d)
+        self._logits = e(T, E, dt=torch.float32)
+        self._idx = e(T, k, dt=torch.int32)
+        self._w = e(T, k, dt=torch.float32)
+        self.ws = e(nb, dt=torch.uint8)
+        self._views(T)
+
+    def _views(self, n):
+        """y, logits, topk_idx and topk_w of an n-token step."""
+        self._n = n
+        self.y, self.logits = self._y[:n], self._logits[:n]
+        self.topk_idx, self.topk_w = self._idx[:n], self._w[:n]
+
+    def bind(self, Wg, W1, W2, W3=None, logit_bias=None):
+        """Remember the weights (device, contiguous, layer dtype)."""
+        x = self._y[:0]
+        if _few_check(x, Wg, W1, W2, W3, logit_bias, self.act)[1:] != (self.d, self.f, self.E):
+            raise MoEError("FewTokenMoELayer: weights of another layer's sizes")
+        self.Wg, self.W1, self.W2, self.W3, self.bias = Wg, W1, W2, W3, logit_bias
+        return self
+
+    def forward(self, x, stream=None):
+        n = x.shape[0] if x.dim() == 2 else -1
+        if not 0 <= n <= self.T or x.shape[1] != self.d or x.dtype != self.dtype:
+            raise MoEError("FewTokenMoELayer: x [n,%d], n <= %d, of the layer's dtype"
+                           % (self.d, self.T))
+        _need_gpu(x)
+        if x.device != self._y.device:
+            raise MoEError("FewTokenMoELayer: x on another device than the layer")
+        if n != self._n:
+            self._views(n)
+        p = lambda t: None if t is None else t.data_ptr()
+        with torch.cuda.device(x.device):
+            s = _stream(x.device) if stream is None else stream
+            check(self.lib.moe_layer_fwd_few(
+                p(x), p(self.Wg), p(self.bias), p(self.W1), p(self.W3), p(self.W2), n, self.d,
+                self.f, self.E, self.k, self.renorm, self.act, self.dt, p(self._logits),
+                p(self._idx), p(self._w), p(self._y), p(self.ws), self.ws.numel(), s),
+                "moe_layer_fwd_few")
+        return self.y

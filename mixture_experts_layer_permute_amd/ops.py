@@ -285,3 +285,54 @@ def moe_gate_topk_bwd(x, Wg, logits, topk_idx, topk_w, d_topk_w, dx, renorm=1,
                               _stream(dev)),
           "moe_gate_topk_bwd")
     return dWg
+
+
+def _few_check(x, Wg, W1, W2, W3, logit_bias, a):
+    """Shapes, types and devices of a few-token call -> (T, d, f, E)."""
+    ts = [x, Wg, W1, W2] + ([] if W3 is None else [W3])
+    _need_gpu(*ts, logit_bias)
+    if x.dim() != 2 or Wg.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
+        raise MoEError("x [T,d], Wg [d,E], W1 [E,d,f], W2 [E,f,d] expected")
+    T, d = x.shape
+    E, f = Wg.shape[1], W1.shape[2]
+    if (Wg.shape[0] != d or tuple(W1.shape) != (E, d, f) or tuple(W2.shape) != (E, f, d)
+            or (W3 is not None and tuple(W3.shape) != (E, d, f))):
+        raise MoEError("x [T,d], Wg [d,E], W1 and W3 [E,d,f], W2 [E,f,d] do not agree")
+    if (W3 is not None) != (a == MOE_ACT_SWIGLU):
+        raise MoEError("W3 goes with the swiglu activation, and only with it")
+    if any(t.dtype != x.dtype or t.device != x.device for t in ts):
+        raise MoEError("x, Wg and the weights need one dtype and one device")
+    if logit_bias is not None and (tuple(logit_bias.shape) != (E,)
+                                   or logit_bias.dtype != torch.float32
+                                   or logit_bias.device != x.device):
+        raise MoEError("logit_bias: float32 [E] on the inputs' device")
+    return T, d, f, E
+
+
+def moe_layer_fwd_few(x, Wg, W1, W2, W3=None, k=1, act="gelu", logit_bias=None, renorm=1,
+                      out=None, ws=None):
+    """The whole layer for 1 to 64 tokens, forward only.
+    -> (y [T,d], logits [T,E] f32, topk_idx [T,k] i32, topk_w [T,k] f32)."""
+    a = _act(act)
+    T, d, f, E = _few_check(x, Wg, W1, W2, W3, logit_bias, a)
+    dev = x.device
+    L = load()
+    if out is None:
+        out = (torch.empty(T, d, dtype=x.dtype, device=dev),
+               torch.empty(T, E, dtype=torch.float32, device=dev),
+               torch.empty(T, k, dtype=torch.int32, device=dev),
+               torch.empty(T, k, dtype=torch.float32, device=dev))
+    y, logits, topk_idx, topk_w = out
+    for t, shape, dt in ((y, (T, d), x.dtype), (logits, (T, E), torch.float32),
+                         (topk_idx, (T, k), torch.int32), (topk_w, (T, k), torch.float32)):
+        if (tuple(t.shape) != shape or t.dtype != dt or t.device != dev
+                or not t.is_contiguous()):
+            raise MoEError("out: y [T,d], logits [T,E], topk_idx [T,k], topk_w [T,k]")
+    if ws is None:
+        ws = _ws(L.moe_layer_few_workspace_bytes(T, d, f, E, k, a, _dt(x)), dev)
+    with torch.cuda.device(dev):
+        check(L.moe_layer_fwd_few(_p(x), _p(Wg), _p(logit_bias), _p(W1), _p(W3), _p(W2), T, d,
+                                  f, E, k, renorm, a, _dt(x), _p(logits), _p(topk_idx),
+                                  _p(topk_w), _p(y), _p(ws), ws.numel(), _stream(dev)),
+              "moe_layer_fwd_few")
+    return y, logits, topk_idx, topk_w

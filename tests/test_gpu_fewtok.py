@@ -1,0 +1,255 @@
+"""moe_layer_fwd_few and FewTokenMoELayer (the layer for 1 to 64 tokens)
+against the oracle in 64 bits, element by element.
+
+The bound of an element of y is arithmetic, not a fitted tolerance.  With
+u = 2^-24 (half a step of fp32), a sum of n terms in any order is off by at
+most (n + 1) u times the sum of the terms' sizes.  So, per pair:
+  dH <= (d + 2) u |x| |W1|                             pre-activation
+  dA <= slope * dH (+ the second factor's) + 8 u |A|   activation function
+        + r (|A| + the above)                          rounded to the layer's type
+  dO <= dA |W2| + (f + 64) u |A| |W2|                  second product, chunks joined
+and y = sum_j w_j O_j has dy <= sum_j w_j (dO_j + 64 u |O_j|) + r |y|, where r
+is half a step of the type (bf16 2^-8, fp32 2^-24); GeLU's slope is at most
+1.13, SiLU's 1.10, and a gate weight is right to 32 u.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_permute_amd as M
+import oracle
+from moe_inputs import stage
+
+from _gpu import (TDT, TOL, assert_equal_i, banner, dev, host, needs_gpu, rel_err)
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def inputs(T, d, f, E, act, dt, seed=0, bias=None):
+    x = stage.normal(seed, (T, d), 1.0, dt)
+    Wg = stage.normal(seed + 1, (d, E), 1 / np.sqrt(d), dt)
+    W1 = stage.normal(seed + 2, (E, d, f), 1 / np.sqrt(d), dt)
+    W2 = stage.normal(seed + 3, (E, f, d), 1 / np.sqrt(f), dt)
+    W3 = stage.normal(seed + 4, (E, d, f), 1 / np.sqrt(d), dt) if act == "swiglu" else None
+    b = None if bias is None else np.asarray(bias, np.float32)
+    return x, Wg, W1, W2, W3, b
+
+
+def upload(a, dt):
+    x, Wg, W1, W2, W3, b = a
+    g = [dev(v, dt) for v in (x, Wg, W1, W2)] + [None if W3 is None else dev(W3, dt)]
+    return g + [None if b is None else torch.from_numpy(b).cuda()]
+
+
+def reference(a, k, act, renorm, dt):
+    """-> (oracle forward, bound of |y - oracle's y| per element)."""
+    x, Wg, W1, W2, W3, b = a
+    fw = oracle.layer_forward(x, Wg, W1, W2, W3, k=k, act=act, bias=b, renorm=renorm)
+    T, d = x.shape
+    f = W1.shape[2]
+    r = HALF[dt]
+    x64 = np.abs(x.astype(np.float64))
+    bound = r * np.abs(fw["y"])
+    for t in range(T):
+        for j in range(k):
+            e, row, w = fw["idx"][t, j], fw["dest"][t, j], fw["w"][t, j]
+            A = np.abs(fw["A"][row])
+            dH = (d + 2) * U * (x64[t] @ np.abs(W1[e].astype(np.float64)))
+            if act == "swiglu":
+                dH3 = (d + 2) * U * (x64[t] @ np.abs(W3[e].astype(np.float64)))
+                H, H3 = fw["H"][row], np.abs(fw["H3"][row])
+                dA = 1.1 * dH * (H3 + dH3) + np.abs(oracle.silu(H)) * dH3
+            else:
+                dA = 1.13 * dH
+            dA = dA + 8 * U * A
+            dA = dA + r * (A + dA)
+            W2a = np.abs(W2[e].astype(np.float64))
+            bound[t] += w * ((dA + (f + 64) * U * A) @ W2a + 64 * U * (A @ W2a))
+    return fw, bound * 1.001 + 1e-30
+
+
+def compare(got, fw, bound, dt):
+    y, logits, idx, w = got
+    assert_equal_i(logits.cpu().numpy().view(np.uint32), fw["logits"].view(np.uint32), "logits")
+    assert_equal_i(idx, fw["idx"], "topk_idx")
+    assert np.all(np.abs(host(w) - fw["w"]) <= 32 * U * fw["w"] + 1e-30), "topk_w"
+    err = np.abs(host(y) - fw["y"])
+    assert np.all(err <= bound), "y: off by %.2f of its bound" % float((err / bound).max())
+    assert rel_err(host(y), fw["y"]) <= TOL[dt]
+
+
+CASES = [
+    # T, d, f, E, k, act, dtype, renorm: every count of token tiles, strips that
+    # end inside a tile, one step of the reduction and uneven shares of it
+    (1, 64, 64, 1, 1, "gelu", "bf16", 1),
+    (1, 64, 64, 1, 1, "swiglu", "f32", 1),
+    (1, 256, 512, 8, 2, "gelu", "bf16", 1),
+    (2, 192, 320, 5, 3, "swiglu", "bf16", 0),
+    (7, 320, 192, 12, 3, "swiglu", "f32", 0),
+    (15, 128, 448, 3, 2, "gelu", "f32", 1),
+    (16, 128, 256, 2, 1, "gelu", "bf16", 1),
+    (17, 64, 704, 2, 2, "swiglu", "bf16", 1),
+    (31, 256, 64, 4, 2, "gelu", "bf16", 0),
+    (33, 192, 128, 2, 1, "swiglu", "bf16", 1),
+    (33, 128, 192, 2, 2, "swiglu", "f32", 1),
+    (48, 448, 320, 40, 6, "gelu", "bf16", 1),
+    (64, 128, 384, 1, 1, "gelu", "bf16", 1),
+    (64, 320, 128, 4, 4, "swiglu", "bf16", 1),
+    (64, 128, 128, 3, 2, "gelu", "f32", 0),
+    (64, 64, 64, 130, 64, "gelu", "bf16", 1),
+    (3, 64, 128, 1024, 5, "swiglu", "bf16", 0),
+    (64, 64, 64, 1000, 3, "gelu", "f32", 1),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "T%d_d%d_f%d_E%d_k%d_%s_%s_%d" % c)
+def test_against_the_oracle(case):
+    T, d, f, E, k, act, dt, renorm = case
+    banner("few", case)
+    a = inputs(T, d, f, E, act, dt, seed=T + E)
+    fw, bound = reference(a, k, act, renorm, dt)
+    x, Wg, W1, W2, W3, b = upload(a, dt)
+    got = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, k, act, b, renorm)
+    torch.cuda.synchronize()
+    compare(got, fw, bound, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_all_tokens_to_one_expert_others_unread(act, dt):
+    """Every token's only choice is expert 5: 64 rows in one expert, and the
+    other experts' weights are not read (they hold NaN)."""
+    T, d, f, E = 64, 128, 192, 8
+    banner("few one expert", act, dt)
+    a = inputs(T, d, f, E, act, dt, seed=3, bias=[0, 0, 0, 0, 0, 1000, 0, 0])
+    fw, bound = reference(a, 1, act, 1, dt)
+    x, Wg, W1, W2, W3, b = upload(a, dt)
+    for W in (W1, W2, W3):
+        if W is not None:
+            for e in range(E):
+                if e != 5:
+                    W[e] = float("nan")
+    got = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, 1, act, b)
+    torch.cuda.synchronize()
+    compare(got, fw, bound, dt)
+
+
+def test_equal_logits_go_to_the_lower_experts():
+    T, d, f, E, k = 20, 64, 64, 70, 3
+    x, Wg, W1, W2, W3, _ = inputs(T, d, f, E, "gelu", "bf16", seed=9)
+    Wg[:] = 0
+    fw, bound = reference((x, Wg, W1, W2, None, None), k, "gelu", 1, "bf16")
+    g = upload((x, Wg, W1, W2, None, None), "bf16")
+    banner("few ties")
+    got = M.moe_layer_fwd_few(g[0], g[1], g[2], g[3], None, k)
+    torch.cuda.synchronize()
+    assert_equal_i(got[2], np.tile(np.arange(k, dtype=np.int32), (T, 1)), "ties")
+    compare(got, fw, bound, "bf16")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_token_that_is_not_finite_stays_alone(bad, dt):
+    """One token holds NaN or infinity: the others keep their bits, whatever
+    experts the bad one is sent to."""
+    T, d, f, E, k = 19, 128, 256, 4, 2
+    banner("few not finite", bad, dt)
+    a = inputs(T, d, f, E, "swiglu", dt, seed=21)
+    x, Wg, W1, W2, W3, _ = upload(a, dt)
+    good = [v.clone() for v in M.moe_layer_fwd_few(x, Wg, W1, W2, W3, k, "swiglu")]
+    x[6, 17] = bad
+    got = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, k, "swiglu")
+    torch.cuda.synchronize()
+    keep = [t for t in range(T) if t != 6]
+    for g, v in zip(good, got):
+        assert torch.equal(g[keep], v[keep])
+    assert not torch.isfinite(got[0][6].float()).all()
+    idx = got[2][6].tolist()
+    assert len(set(idx)) == k and all(0 <= e < E for e in idx)
+
+
+def test_layer_steps_of_changing_size_on_a_stream_match_the_function():
+    """FewTokenMoELayer over steps of 1 to T tokens on a stream of its own:
+    the function's bits, and rows behind the step's last token left alone."""
+    d, f, E, k = 192, 320, 10, 2
+    banner("few layer steps")
+    a = inputs(40, d, f, E, "swiglu", "bf16", seed=33)
+    x, Wg, W1, W2, W3, _ = upload(a, "bf16")
+    layer = M.FewTokenMoELayer(40, d, f, E, k, "swiglu").bind(Wg, W1, W2, W3)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for n in (40, 1, 17, 0, 33, 2, 40):
+            layer._y.fill_(7)
+            y = layer.forward(x[:n])
+            want = M.moe_layer_fwd_few(x[:n].contiguous(), Wg, W1, W2, W3, k, "swiglu")
+            side.synchronize()
+            assert y.shape == (n, d) and layer.topk_idx.shape == (n, k)
+            for g, v in zip((y, layer.logits, layer.topk_idx, layer.topk_w), want):
+                assert torch.equal(g, v), n
+            assert bool((layer._y[n:] == 7).all()), n
+
+
+def test_two_layers_share_weights_on_two_streams():
+    """Two steps in flight at once over the same weights, a layer each."""
+    d, f, E, k = 256, 512, 8, 2
+    banner("few two streams")
+    a = inputs(24, d, f, E, "gelu", "bf16", seed=40)
+    x, Wg, W1, W2, _, _ = upload(a, "bf16")
+    want = [M.moe_layer_fwd_few(v.contiguous(), Wg, W1, W2, None, k)[0].clone()
+            for v in (x[:11], x[11:])]
+    ls = [M.FewTokenMoELayer(13, d, f, E, k).bind(Wg, W1, W2) for _ in range(2)]
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for l, s, v in zip(ls, ss, (x[:11], x[11:])):
+            with torch.cuda.stream(s):
+                l.forward(v)
+    torch.cuda.synchronize()
+    for l, w in zip(ls, want):
+        assert torch.equal(l.y, w)
+
+
+@pytest.mark.parametrize("T,E,k,dt", [(1, 8, 2, "bf16"), (20, 40, 4, "bf16"), (3, 6, 2, "f32")])
+def test_graph_replays_follow_their_inputs(T, E, k, dt):
+    """A captured step, replayed with other tokens in its input buffer and
+    eager work between the replays: each replay has the eager call's bits."""
+    d, f = 256, 384
+    banner("few graph", T, E, k, dt)
+    a = inputs(T, d, f, E, "swiglu", dt, seed=50)
+    x, Wg, W1, W2, W3, _ = upload(a, dt)
+    layer = M.FewTokenMoELayer(T, d, f, E, k, "swiglu", TDT[dt]).bind(Wg, W1, W2, W3)
+    layer.forward(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.forward(x)
+    for rep in range(4):
+        new = dev(stage.normal(60 + rep, (T, d), 1.0, dt), dt)
+        x.copy_(new)
+        layer._y.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        want = M.moe_layer_fwd_few(new, Wg, W1, W2, W3, k, "swiglu")
+        torch.cuda.synchronize()
+        for q, v in zip((layer.y, layer.logits, layer.topk_idx, layer.topk_w), want):
+            assert torch.equal(q, v), rep
+
+
+def test_agrees_with_the_training_layer():
+    """The same tokens through MoELayer (grouped GEMMs): the same routing bit
+    for bit, outputs within two independent roundings of each."""
+    T, d, f, E, k = 50, 256, 512, 16, 2
+    banner("few against MoELayer")
+    a = inputs(T, d, f, E, "swiglu", "bf16", seed=70)
+    x, Wg, W1, W2, W3, _ = upload(a, "bf16")
+    big = M.MoELayer(T, d, f, E, k, "swiglu").bind(x, Wg, W1, W2, W3)
+    big.forward()
+    few = M.FewTokenMoELayer(T, d, f, E, k, "swiglu").bind(Wg, W1, W2, W3)
+    few.forward(x)
+    torch.cuda.synchronize()
+    assert torch.equal(few.logits, big.logits) and torch.equal(few.topk_idx, big.topk_idx)
+    assert rel_err(host(few.y), host(big.y)) <= TOL["bf16"]
