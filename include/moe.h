@@ -384,6 +384,39 @@ moe_status moe_layer_fwd_few(const void *x, const void *Wg,
                              size_t ws_bytes, hipStream_t stream);
 
 /*
+ * moe_grad_norm, moe_clip_grads -- the global norm of a list of n gradient
+ * tensors and the list scaled to a largest norm, for a training step between
+ * the backward pass and the optimizer.
+ *   norm   = sqrt(sum over all tensors of g^2), summed in fp64, rounded once
+ *   out[i] = grads[i] * (norm > max_norm ? max_norm / norm : 1), rounded once
+ * A norm that is not finite (or above the fp32 range) scales nothing: norm
+ * says so, and out holds the gradients as they were.
+ *   grads, out [n]: host arrays of device pointers; numel [n]: elements of
+ *   each tensor (0: skipped, its pointers may be NULL; at most 2^40); dt [n]:
+ *   each one's moe_dtype (a list may mix them).  The host arrays are read
+ *   during the call only; a captured graph keeps the pointers.  Tensors need
+ *   their element's alignment, no more.  out[i] is grads[i] (in place) or
+ *   overlaps no tensor of the list, and no two out tensors overlap.
+ *   max_norm: host pointer to one float >= 0 (infinity: never scaled), read
+ *   during the call; norm: device pointer to one float.
+ *   ws: at least moe_grad_norm_workspace_bytes(numel, dt, n), 8-byte aligned,
+ *   no initial content needed; calls that may overlap in time need one each.
+ *   n = 0: norm = 0.
+ * The norm is that of one process; the gradients of the layer are exact under
+ * the reordering ("Flattening Every Memory Peak in Long-Context MoE
+ * Training", English abstract), so it is the dense layer's norm.
+ */
+size_t moe_grad_norm_workspace_bytes(const size_t *numel, const int32_t *dt,
+                                     int n);
+moe_status moe_grad_norm(const void *const *grads, const size_t *numel,
+                         const int32_t *dt, int n, float *norm, void *ws,
+                         size_t ws_bytes, hipStream_t stream);
+moe_status moe_clip_grads(const void *const *grads, void *const *out,
+                          const size_t *numel, const int32_t *dt, int n,
+                          const float *max_norm, float *norm, void *ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/*
  * Kernel timing (benchmark support, off by default).
  * moe_profile_enable(capacity) creates 2*capacity HIP events; from then on
  * every kernel the library launches is bracketed by two of them on its

@@ -14,7 +14,7 @@ from .ops import (moe_combine, moe_combine_bwd, moe_expert_ffn_bwd,  # noqa: F40
                   moe_expert_ffn_fwd, moe_expert_ffn_fwd_gather,
                   moe_expert_ffn_fwd_noalloc,
                   moe_expert_ffn_bwd_gather, moe_gate_topk, moe_gate_topk_bwd,
-                  moe_layer_fwd_few,
+                  moe_layer_fwd_few, moe_grad_norm, moe_clip_grads, GradClip,
                   moe_permute, moe_unpermute_grad, moe_init,
                   moe_set_overlap)
 from .layer import (ChunkedMoELayer, FewTokenMoELayer, MoELayer,  # noqa: F401

@@ -47,6 +47,9 @@ SIGNATURES = {
     "moe_layer_few_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
     "moe_layer_fwd_few": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P,
                                _P, _P, _P, _P, _Z, _P]),
+    "moe_grad_norm_workspace_bytes": (_Z, [_P, _P, _I]),
+    "moe_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _Z, _P]),
+    "moe_clip_grads": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _Z, _P]),
     "moe_mfma_loop": (_I, [_I, _I, _P, _Z, _P]),
     "moe_mfma_loop_random": (_I, [_I, _I, _P, _Z, _P]),
     "moe_lds_probe": (_I, [_I, _I, _I, _P, _Z, _P, _Z, _P]),

@@ -1,0 +1,325 @@
+// The global L2 norm of a list of gradient tensors, and the list scaled to a
+// largest norm: what a training step does between the layer's backward pass
+// and its optimizer.
+//
+//   norm = sqrt(sum over all tensors and elements of g^2)
+//   out  = g * min(1, max_norm / norm)
+//
+// Both are streams: the norm reads every gradient once, clipping reads and
+// writes every one once more, so bytes over the HBM rate is the floor and a
+// launch per tensor is what a list of many small tensors must not cost.  The
+// tensors' addresses and sizes travel in the kernel's argument block (128
+// tensors a launch, no copy to the device, so a captured graph holds them);
+// blocks take fixed chunks of the list, whatever tensor they lie in.
+//
+// Squares and sums are taken in fp64: the square of an fp32 value is exact
+// there, no gradient is too large or too small to be squared, and the norm is
+// the correctly rounded one whatever the order.  Partial sums are stored per
+// block and added in block order: no atomics, the same bits every time.
+#include <math.h>
+
+#include "common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTensors = 128;                 // tensors of one launch
+constexpr int kChunkBytes = 64 << 10;         // of one tensor, one block's work item
+constexpr int kNormBlocks = 2048;             // blocks of one launch at most
+constexpr uint64_t kBf16Flag = 1ull << 63;
+
+// One launch's tensors: tensor i covers chunks first[i] .. first[i+1]-1.
+struct GradTable {
+    const void* in[kTensors];
+    void* out[kTensors];
+    uint64_t numel[kTensors];                 // bit 63: bf16
+    uint32_t first[kTensors + 1];
+    int n;
+};
+
+struct Chunk {
+    int t;                                    // tensor
+    bool bf16;
+    uint64_t i0;                              // first element
+    int len;                                  // elements
+};
+__device__ __forceinline__ Chunk chunk_of(const GradTable& g, uint32_t c) {
+    int lo = 0, hi = g.n;                     // largest t with first[t] <= c
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (g.first[mid] <= c) lo = mid; else hi = mid;
+    }
+    Chunk k;
+    k.t = lo;
+    k.bf16 = (g.numel[lo] & kBf16Flag) != 0;
+    const uint64_t n = g.numel[lo] & ~kBf16Flag;
+    const int per = kChunkBytes / (k.bf16 ? 2 : 4);
+    k.i0 = (uint64_t)(c - g.first[lo]) * per;
+    k.len = (int)min((uint64_t)per, n - k.i0);
+    return k;
+}
+
+// 16 bytes at an address aligned to an element only (tensors may be views of
+// a flat buffer).
+typedef unsigned int u32x4_2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32x4_4_t __attribute__((ext_vector_type(4), aligned(4)));
+template <typename T> struct Packed;
+template <> struct Packed<bf16_t> { typedef u32x4_2_t type; };
+template <> struct Packed<float> { typedef u32x4_4_t type; };
+
+__device__ __forceinline__ double sq(double s, float v) {
+    const double d = (double)v;
+    return fma(d, d, s);
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T* __restrict__ p, int len) {
+    typedef typename Packed<T>::type P;
+    constexpr int V = Vec16<T>::N, UN = 4;
+    const int nvec = len / V;
+    double s[2] = {0.0, 0.0};
+    int v = threadIdx.x;
+    for (; v + 256 * (UN - 1) < nvec; v += 256 * UN) {
+        u32x4_t raw[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) raw[u] = *reinterpret_cast<const P*>(p + (v + 256 * u) * V);
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            float o[V];
+            unpack16<T>(raw[u], o);
+#pragma unroll
+            for (int q = 0; q < V; ++q) s[q & 1] = sq(s[q & 1], o[q]);
+        }
+    }
+    for (; v < nvec; v += 256) {
+        float o[V];
+        unpack16<T>(*reinterpret_cast<const P*>(p + v * V), o);
+#pragma unroll
+        for (int q = 0; q < V; ++q) s[q & 1] = sq(s[q & 1], o[q]);
+    }
+    const int i = nvec * V + threadIdx.x;                 // the last len % V elements
+    if (i < len) s[0] = sq(s[0], Elem<T>::ld(p + i));
+    return s[0] + s[1];
+}
+
+// Sum over the block's 256 threads, in a fixed order; every thread gets it.
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
+__global__ __launch_bounds__(256) void grad_squares_kernel(GradTable g,
+                                                           double* __restrict__ partial) {
+    __shared__ double sh[4];
+    double s = 0.0;
+    for (uint32_t c = blockIdx.x; c < g.first[g.n]; c += gridDim.x) {
+        const Chunk k = chunk_of(g, c);
+        s += k.bf16 ? chunk_squares(static_cast<const bf16_t*>(g.in[k.t]) + k.i0, k.len)
+                    : chunk_squares(static_cast<const float*>(g.in[k.t]) + k.i0, k.len);
+    }
+    s = block_sum(s, sh);
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// The norm from all launches' partial sums; every block that calls it gets
+// the same bits.
+__device__ __forceinline__ float norm_of(const double* __restrict__ partial, int np, double* sh) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < np; i += 256) s += partial[i];
+    return (float)sqrt(block_sum(s, sh));
+}
+
+__global__ __launch_bounds__(256) void grad_norm_kernel(const double* __restrict__ partial,
+                                                        int np, float* __restrict__ norm) {
+    __shared__ double sh[4];
+    const float v = norm_of(partial, np, sh);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, float c) {
+    typedef typename Packed<T>::type P;
+    constexpr int V = Vec16<T>::N, UN = 4;
+    const int nvec = len / V;
+    auto scaled = [&](u32x4_t raw) {
+        float a[V];
+        unpack16<T>(raw, a);
+#pragma unroll
+        for (int q = 0; q < V; ++q) a[q] *= c;
+        return pack16<T>(a);
+    };
+    int v = threadIdx.x;
+    for (; v + 256 * (UN - 1) < nvec; v += 256 * UN) {
+        u32x4_t raw[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) raw[u] = *reinterpret_cast<const P*>(p + (v + 256 * u) * V);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            *reinterpret_cast<P*>(o + (v + 256 * u) * V) = scaled(raw[u]);
+    }
+    for (; v < nvec; v += 256)
+        *reinterpret_cast<P*>(o + v * V) = scaled(*reinterpret_cast<const P*>(p + v * V));
+    const int i = nvec * V + threadIdx.x;
+    if (i < len) Elem<T>::st(o + i, Elem<T>::ld(p + i) * c);
+}
+
+// out = g * (norm > max_norm ? max_norm / norm : 1), one rounding.  A norm
+// that is not finite scales nothing: the step is the caller's to drop, and
+// zeros or NaN in place of the gradients would hide why.  In place a factor
+// of 1 leaves nothing to do.
+__global__ __launch_bounds__(256) void grad_scale_kernel(GradTable g,
+                                                         const double* __restrict__ partial,
+                                                         int np, float max_norm,
+                                                         float* __restrict__ norm) {
+    __shared__ double sh[4];
+    const float v = norm_of(partial, np, sh);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+    const float c = v > max_norm && v < INFINITY ? max_norm / v : 1.0f;
+    for (uint32_t q = blockIdx.x; q < g.first[g.n]; q += gridDim.x) {
+        const Chunk k = chunk_of(g, q);
+        if (c == 1.0f && g.in[k.t] == g.out[k.t]) continue;
+        if (k.bf16)
+            chunk_scale(static_cast<const bf16_t*>(g.in[k.t]) + k.i0,
+                        static_cast<bf16_t*>(g.out[k.t]) + k.i0, k.len, c);
+        else
+            chunk_scale(static_cast<const float*>(g.in[k.t]) + k.i0,
+                        static_cast<float*>(g.out[k.t]) + k.i0, k.len, c);
+    }
+}
+
+// ------------------------------------------------------------------- host
+constexpr size_t kMaxNumel = (size_t)1 << 40;          // chunks of a launch stay in 32 bits
+
+bool list_ok(const void* const* grads, void* const* out, const size_t* numel, const int32_t* dt,
+             int n, bool clip) {
+    if (n < 0 || (n > 0 && (!grads || !numel || !dt || (clip && !out)))) return false;
+    for (int i = 0; i < n; ++i) {
+        if (dt[i] != MOE_F32 && dt[i] != MOE_BF16) return false;
+        if (numel[i] > kMaxNumel) return false;
+        if (numel[i] == 0) continue;
+        const uintptr_t mask = dt[i] == MOE_BF16 ? 1 : 3;
+        if (!grads[i] || (reinterpret_cast<uintptr_t>(grads[i]) & mask)) return false;
+        if (clip && (!out[i] || (reinterpret_cast<uintptr_t>(out[i]) & mask))) return false;
+    }
+    return true;
+}
+
+uint64_t chunks_of(size_t numel, int dt) {
+    const size_t per = kChunkBytes / (dt == MOE_BF16 ? 2 : 4);
+    return (numel + per - 1) / per;
+}
+
+// Calls f(table, blocks) for each launch of the list, in order; stops early
+// when f returns false.  out may be NULL.
+template <class F>
+void for_launches(const void* const* grads, void* const* out, const size_t* numel,
+                  const int32_t* dt, int n, F&& f) {
+    GradTable g;
+    g.n = 0;
+    g.first[0] = 0;
+    auto flush = [&]() {
+        if (g.n == 0) return true;
+        const bool ok = f(g, (int)min((uint32_t)kNormBlocks, g.first[g.n]));
+        g.n = 0;
+        return ok;
+    };
+    for (int i = 0; i < n; ++i) {
+        if (numel[i] == 0) continue;
+        const uint64_t c = chunks_of(numel[i], dt[i]);
+        // a launch's chunk numbers, and a block's next one, stay below 2^32
+        if (g.n == kTensors || (g.n > 0 && g.first[g.n] + c >= (1ull << 31)))
+            if (!flush()) return;
+        if (grads) g.in[g.n] = grads[i];
+        g.out[g.n] = out ? out[i] : nullptr;
+        g.numel[g.n] = numel[i] | (dt[i] == MOE_BF16 ? kBf16Flag : 0);
+        g.first[g.n + 1] = g.first[g.n] + (uint32_t)c;
+        ++g.n;
+    }
+    flush();
+}
+
+int partials_of(const size_t* numel, const int32_t* dt, int n) {
+    int np = 0;
+    for_launches(nullptr, nullptr, numel, dt, n, [&](const GradTable&, int blocks) {
+        np += blocks;
+        return true;
+    });
+    return np;
+}
+
+moe_status run_squares(const void* const* grads, const size_t* numel, const int32_t* dt, int n,
+                       double* partial, hipStream_t s) {
+    int at = 0;
+    moe_status st = MOE_OK;
+    for_launches(grads, nullptr, numel, dt, n, [&](const GradTable& g, int blocks) {
+        MOE_LAUNCH("grad_squares", s, (grad_squares_kernel<<<blocks, 256, 0, s>>>(g, partial + at)));
+        at += blocks;
+        st = launch_status();
+        return st == MOE_OK;
+    });
+    return st;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_grad_norm_workspace_bytes(const size_t* numel, const int32_t* dt, int n) {
+    if (n < 0 || (n > 0 && (!numel || !dt))) return 0;
+    for (int i = 0; i < n; ++i)
+        if ((dt[i] != MOE_F32 && dt[i] != MOE_BF16) || numel[i] > kMaxNumel) return 0;
+    return align_up(sizeof(double) * ((size_t)partials_of(numel, dt, n) + 1), 256);
+}
+
+moe_status moe_grad_norm(const void* const* grads, const size_t* numel, const int32_t* dt, int n,
+                         float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
+    MOE_CHECK_ARG(list_ok(grads, nullptr, numel, dt, n, false) && norm);
+    const int np = partials_of(numel, dt, n);
+    if (!ws || ws_bytes < sizeof(double) * (size_t)np) return MOE_ERR_WORKSPACE;
+    MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(ws) & 7u) == 0);
+    MOE_CHECK_DEVICE();
+    double* partial = static_cast<double*>(ws);
+    const moe_status st = run_squares(grads, numel, dt, n, partial, stream);
+    if (st != MOE_OK) return st;
+    MOE_LAUNCH("grad_norm", stream,
+               (grad_norm_kernel<<<1, 256, 0, stream>>>(partial, np, norm)));
+    return launch_status();
+}
+
+moe_status moe_clip_grads(const void* const* grads, void* const* out, const size_t* numel,
+                          const int32_t* dt, int n, const float* max_norm, float* norm, void* ws,
+                          size_t ws_bytes, hipStream_t stream) {
+    MOE_CHECK_ARG(list_ok(grads, out, numel, dt, n, true) && norm && max_norm);
+    const float mx = *max_norm;
+    MOE_CHECK_ARG(mx >= 0.0f);                            // NaN too is refused
+    const int np = partials_of(numel, dt, n);
+    if (!ws || ws_bytes < sizeof(double) * (size_t)np) return MOE_ERR_WORKSPACE;
+    MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(ws) & 7u) == 0);
+    MOE_CHECK_DEVICE();
+    double* partial = static_cast<double*>(ws);
+    moe_status st = run_squares(grads, numel, dt, n, partial, stream);
+    if (st != MOE_OK) return st;
+    if (np == 0) {
+        MOE_LAUNCH("grad_norm", stream,
+                   (grad_norm_kernel<<<1, 256, 0, stream>>>(partial, 0, norm)));
+        return launch_status();
+    }
+    bool first = true;
+    for_launches(grads, out, numel, dt, n, [&](const GradTable& g, int blocks) {
+        MOE_LAUNCH("grad_scale", stream,
+                   (grad_scale_kernel<<<blocks, 256, 0, stream>>>(g, partial, np, mx,
+                                                                  first ? norm : nullptr)));
+        first = false;
+        st = launch_status();
+        return st == MOE_OK;
+    });
+    return st;
+}
+
+}  // extern "C"

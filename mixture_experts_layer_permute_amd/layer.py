@@ -10,7 +10,7 @@ import math
 import torch
 
 from ._lib import MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F32, check, load
-from .ops import MoEError, _few_check, _need_gpu, _stream
+from .ops import GradClip, MoEError, _few_check, _need_gpu, _stream
 
 
 def _torch_stream(handle, device):
@@ -25,6 +25,16 @@ def _torch_stream(handle, device):
     if handle == dflt.cuda_stream:
         return dflt
     return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _weight_grads(layer):
+    return [g for g in (layer.dWg, layer.dW1, layer.dW3, layer.dW2) if g is not None]
+
+
+def _clip_grads(layer, max_norm, stream):
+    if getattr(layer, "_clip", None) is None:
+        layer._clip = GradClip(_weight_grads(layer))     # the buffers never move
+    return layer._clip.clip(max_norm, stream)
 
 
 class MoELayer:
@@ -179,6 +189,17 @@ class MoELayer:
         """One forward + backward pass."""
         self._run(self._fwd, stream)
         self.backward(stream)
+
+    def weight_grads(self):
+        """The weight gradients of the last backward: dWg, dW1, dW3 (SwiGLU), dW2."""
+        return _weight_grads(self)
+
+    def clip_grads(self, max_norm, stream=None):
+        """Scale the weight gradients to the global norm max_norm if theirs is
+        larger, in place, on the step's stream -> the norm before, [1] float32
+        (a model of several layers clips them together: GradClip over all
+        their weight_grads())."""
+        return _clip_grads(self, max_norm, stream)
 
     def stage_calls(self):
         """[(name, callable)] of every step of one layer step, in order, on one
@@ -349,6 +370,14 @@ class ChunkedMoELayer:
     def step(self, stream=None):
         self.forward(stream)
         self.backward(stream)
+
+    def weight_grads(self):
+        """The weight gradients of the last backward: dWg, dW1, dW3 (SwiGLU), dW2."""
+        return _weight_grads(self)
+
+    def clip_grads(self, max_norm, stream=None):
+        """MoELayer.clip_grads: in place, -> the norm before, [1] float32."""
+        return _clip_grads(self, max_norm, stream)
 
 
 def offload_groups(E, G, pinned):

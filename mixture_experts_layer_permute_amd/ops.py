@@ -4,6 +4,8 @@ Shapes and meanings are those of include/moe.h.  Outputs not passed in are
 allocated with torch on the inputs' device; workspaces likewise.  All calls
 are asynchronous on torch's current HIP stream.
 """
+import ctypes
+
 import torch
 
 from ._lib import (MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F32, MoEError,
@@ -336,3 +338,92 @@ def moe_layer_fwd_few(x, Wg, W1, W2, W3=None, k=1, act="gelu", logit_bias=None, 
                                   _p(topk_w), _p(y), _p(ws), ws.numel(), _stream(dev)),
               "moe_layer_fwd_few")
     return y, logits, topk_idx, topk_w
+
+
+class GradClip:
+    """The global norm of a list of gradients and clipping to a largest norm
+    (moe_grad_norm, moe_clip_grads), the list's addresses and the workspace
+    kept from step to step.
+
+    grads: float32 or bfloat16 device tensors, contiguous, of one device (a
+    list may mix the types; views of a flat buffer are fine).  out: where
+    clip() writes, tensors like grads; None: in place.  norm() and clip()
+    return the norm as a float32 tensor of one element, overwritten by the
+    next call: two calls in flight at once need a GradClip each.
+    """
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise MoEError("GradClip: as many outputs as gradients")
+        _need_gpu(*self.grads, *self.out)
+        dev = self.device = (self.grads[0].device if self.grads else
+                             torch.device("cuda", torch.cuda.current_device()))
+        for g, o in zip(self.grads, self.out):
+            if g.device != dev or o.device != dev:
+                raise MoEError("GradClip: all tensors on one device")
+            if o.dtype != g.dtype or o.shape != g.shape:
+                raise MoEError("GradClip: an output needs its gradient's shape and dtype")
+        self._disjoint = False         # looked at by the first clip()
+        n = self.n = len(self.grads)
+        ptrs = ctypes.c_void_p * n
+        self._in = ptrs(*[g.data_ptr() for g in self.grads])
+        self._out = ptrs(*[o.data_ptr() for o in self.out])
+        self._numel = (ctypes.c_size_t * n)(*[g.numel() for g in self.grads])
+        self._dts = (ctypes.c_int32 * n)(*[_dt(g) for g in self.grads])
+        L = self.lib = load()
+        self.ws = _ws(L.moe_grad_norm_workspace_bytes(self._numel, self._dts, n), dev)
+        self.result = torch.zeros(1, dtype=torch.float32, device=dev)
+
+    def _no_overlap(self):
+        """Refuse lists whose result would depend on which block comes first:
+        two outputs, or an output and another gradient, that share memory."""
+        span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+        used = []
+        for g, o in zip(self.grads, self.out):
+            if g.numel() == 0:
+                continue
+            used.append(span(o) + (1,))
+            if o.data_ptr() != g.data_ptr():
+                used.append(span(g) + (0,))
+        used.sort()
+        end = written = 0              # ends of all spans and of the outputs so far
+        for a, b, w in used:
+            if a < (end if w else written):
+                raise MoEError("GradClip: tensors overlap")
+            end = max(end, b)
+            written = max(written, b) if w else written
+
+    def norm(self, stream=None):
+        """-> the norm, [1] float32; changes no gradient."""
+        with torch.cuda.device(self.device):
+            s = _stream(self.device) if stream is None else stream
+            check(self.lib.moe_grad_norm(self._in, self._numel, self._dts, self.n,
+                                         _p(self.result), _p(self.ws), self.ws.numel(), s),
+                  "moe_grad_norm")
+        return self.result
+
+    def clip(self, max_norm, stream=None):
+        """out = grads * min(1, max_norm / norm) -> the norm, [1] float32."""
+        if not self._disjoint:
+            self._no_overlap()
+            self._disjoint = True
+        mx = ctypes.c_float(max_norm)
+        with torch.cuda.device(self.device):
+            s = _stream(self.device) if stream is None else stream
+            check(self.lib.moe_clip_grads(self._in, self._out, self._numel, self._dts, self.n,
+                                          ctypes.byref(mx), _p(self.result), _p(self.ws),
+                                          self.ws.numel(), s), "moe_clip_grads")
+        return self.result
+
+
+def moe_grad_norm(grads):
+    """The L2 norm over all elements of a list of gradients -> [1] float32."""
+    return GradClip(grads).norm()
+
+
+def moe_clip_grads(grads, max_norm, out=None):
+    """Scales a list of gradients to the norm max_norm if theirs is larger (in
+    place, or into out) -> the norm before, [1] float32."""
+    return GradClip(grads, out).clip(max_norm)
