@@ -355,8 +355,9 @@ moe_status moe_gate_topk_bwd(const void *x, const void *Wg, const float *logits,
  * sum) for a few tokens, forward only: one step of a serving loop.
  *   y[t,:] = sum_{j=0..k-1} topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t,:])
  * with the logits of moe_gate_topk (the same bits) and its choice (NaN logits
- * rank below all others here), its gate weights (to fp32 rounding) and the FFN of moe_expert_ffn_fwd (the inner
- * activation rounded to dt, every sum in fp32, y rounded once).  Each
+ * rank below all others here), its gate weights (to fp32 rounding) and the FFN of moe_expert_ffn_fwd (for
+ * bf16 the inner activation is kept to 16 significant bits instead of 8; every
+ * sum in fp32, y rounded once).  Each
  * expert that any token chose is read once, whatever the number of tokens;
  * experts no token chose are not read.  Nothing is kept for a backward.
  *   x [T,d] dt, Wg [d,E] dt, logit_bias [E] float or NULL, W1 [E,d,f],
@@ -366,8 +367,8 @@ moe_status moe_gate_topk_bwd(const void *x, const void *Wg, const float *logits,
  *   ws: at least moe_layer_few_workspace_bytes(T,d,f,E,k,act,dt), 16-byte
  *   aligned, no initial content needed; calls that may overlap in time need a
  *   workspace each.
- *   Limits: T <= 64 and T*k <= 4096, d and f multiples of 64, E <= 1024;
- *   MOE_ERR_UNSUPPORTED for more tokens or pairs (the workspace query gives 0).
+ *   Limits: T <= 64 and k <= 64, d and f multiples of 64, E <= 1024;
+ *   MOE_ERR_UNSUPPORTED for more tokens or slots (the workspace query gives 0).
  *   T = 0 launches nothing.
  * Sources: ES-MoE review, 三 技术架构 (placement follows the gate; experts
  * take their tokens without padding); FastMoE review, 제안 방법 (the experts'

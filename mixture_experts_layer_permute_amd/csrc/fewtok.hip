@@ -7,9 +7,9 @@
 // state and its row copies have nothing to give there.
 //
 // Kernels of a call:
-//   few_logits   the gate's logits, one fixed-order fp32 chain per (token,
-//                expert): the same bits as moe_gate_topk
-//   few_topk     top-k and gate weights, one wave per token
+//   few_gate     the gate's logits, one fixed-order fp32 chain per (token,
+//                expert): the same bits as moe_gate_topk; then top-k and gate
+//                weights, one wave per token (few_topk, with over 64 experts)
 //   few_up       per (expert hit, strip of columns): act(x W1[e]) (* x W3[e])
 //   few_down     per (expert hit, strip of columns, chunk of f): h W2[e], fp32
 //   few_combine  y[t] = sum_j w[t,j] sum_chunks partial, in slot and chunk order
@@ -22,8 +22,10 @@
 // so one byte permute per pair of rows transposes in registers.  The tokens
 // are the B operand's columns, 16 at a time, read from L2.
 #include <float.h>
+#include <math.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "common.h"
 
@@ -31,159 +33,263 @@ namespace moe {
 namespace {
 
 constexpr int kFewTokens = 64;          // most tokens of a call
-constexpr int kFewPairs = 4096;         // most (token, slot) pairs of a call
+constexpr int kFewSlots = 64;           // most experts per token
 
-// ------------------------------------------------------------ gate logits
-// Block: 256 threads, 16 tokens x 16 experts, one chain per thread.  The
-// chain's order is fixed (increasing feature index, each sum rounded), so its
-// length d sets the time: GK features at a time are staged in LDS as fp32,
-// NPF chunks ahead of the chain in registers.
-constexpr int GK = 128, GTOK = 16, GEXP = 16, GROW = GK + 4;
-
-template <typename T>
-__global__ __launch_bounds__(256) void few_logits_kernel(const T* __restrict__ x,
-                                                         const T* __restrict__ Wg,
-                                                         const float* __restrict__ bias, int Tn,
-                                                         int d, int E,
-                                                         float* __restrict__ logits) {
-#pragma clang fp contract(off)
-    constexpr int V = Vec16<T>::N;
-    constexpr int NPF = 4;
-    constexpr int WV = GK * GEXP / 256;                 // gate elements per thread and chunk
-    constexpr int XV = GTOK * GK / V / 256;             // x vectors per thread and chunk
-    static_assert(XV >= 1, "a vector per thread");
-    __shared__ __attribute__((aligned(16))) float ws[GEXP * GROW];
-    __shared__ __attribute__((aligned(16))) float xs[GTOK * GROW];
-    const int tid = threadIdx.x;
-    const int e0 = blockIdx.x * GEXP, t0 = blockIdx.y * GTOK;
-    const int le = tid % GEXP, lt = tid / GEXP;
-
-    T wr[NPF][WV];
-    u32x4_t xr[NPF][XV];
-    // loads past the matrix read a valid element instead: features past d are
-    // never summed, experts and tokens past the end never stored
-    auto fetch = [&](int c, T (&w)[WV], u32x4_t (&xv)[XV]) {
-        const int k0 = c * GK;
-#pragma unroll
-        for (int q = 0; q < WV; ++q) {
-            const int kk = min(k0 + (tid + 256 * q) / GEXP, d - 1);
-            w[q] = Wg[(long)kk * E + min(e0 + le, E - 1)];
-        }
-#pragma unroll
-        for (int q = 0; q < XV; ++q) {
-            const int i = tid + 256 * q;
-            const int tok = min(t0 + i / (GK / V), Tn - 1);
-            const int k = min(k0 + i % (GK / V) * V, d - V);
-            xv[q] = ld16<false>(x + (long)tok * d + k);
-        }
+// ------------------------------------------------------------------- gate
+// Maximum / minimum over the 64 lanes of a wave, by DPP moves as in
+// wave_incl_scan (a lane without a source keeps its own value); all lanes
+// active, the result in every lane.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    auto step = [&](auto ctrl, auto rows) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(
+            (int)v, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+        v = o > v ? o : v;
     };
-    float acc = 0.0f;
-    const int nc = (d + GK - 1) / GK;
-#pragma unroll
-    for (int c = 0; c < NPF; ++c) fetch(c, wr[c], xr[c]);
-    for (int cb = 0; cb < nc; cb += NPF) {
-#pragma unroll
-        for (int u = 0; u < NPF; ++u) {
-            const int c = cb + u;
-            if (c >= nc) break;
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < WV; ++q)
-                ws[le * GROW + (tid + 256 * q) / GEXP] = Elem<T>::ld(&wr[u][q]);
-#pragma unroll
-            for (int q = 0; q < XV; ++q) {
-                const int i = tid + 256 * q;
-                float o[V];
-                unpack16<T>(xr[u][q], o);
-                float* p = xs + (i / (GK / V)) * GROW + i % (GK / V) * V;
-#pragma unroll
-                for (int v = 0; v < V; v += 4)
-                    *reinterpret_cast<float4*>(p + v) =
-                        make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
-            }
-            __syncthreads();
-            fetch(c + NPF, wr[u], xr[u]);
-            const int kn = min(GK, d - c * GK);         // a multiple of 64
-            const float* wp = ws + le * GROW;
-            const float* xp = xs + lt * GROW;
-#pragma unroll 4
-            for (int k = 0; k < kn; k += 4) {
-                const float4 a = *reinterpret_cast<const float4*>(xp + k);
-                const float4 b = *reinterpret_cast<const float4*>(wp + k);
-                if constexpr (sizeof(T) == 2) {
-                    // the product of two bf16 is exact in fp32: one rounding
-                    acc = __builtin_fmaf(a.x, b.x, acc);
-                    acc = __builtin_fmaf(a.y, b.y, acc);
-                    acc = __builtin_fmaf(a.z, b.z, acc);
-                    acc = __builtin_fmaf(a.w, b.w, acc);
-                } else {
-                    acc = acc + a.x * b.x;
-                    acc = acc + a.y * b.y;
-                    acc = acc + a.z * b.z;
-                    acc = acc + a.w * b.w;
-                }
-            }
-        }
-    }
-    if (e0 + le < E && t0 + lt < Tn) {
-        if (bias) acc = acc + bias[e0 + le];
-        logits[(long)(t0 + lt) * E + e0 + le] = acc;
-    }
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});   // row_shr:1
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});   // row_shr:2
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});   // row_shr:4
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});   // row_shr:8
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});   // row_bcast:15
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});   // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// ------------------------------------------------------------------ top-k
-// One wave per token: k rounds of an arg-max over (value descending, index
-// ascending), then the softmax over the selected logits or over all.  A lane
-// holds experts lane, lane + 64, ...; `live` marks those not taken yet.
+// Top-k and gate weights of one token by one wave: k rounds of an arg-max
+// over (value descending, index ascending), then the softmax over the
+// selected logits (renorm) or over all.  Lane l holds experts l, l + 64, ...
+// (NQ of them); lane j gets the j-th choice and its weight.  k <= 64.
 //
-// The order is taken on one 64-bit key per expert, so that it is total and
-// every lane agrees on the winner whatever the logits hold: the float's bits
-// made monotone (both zeros alike, NaN below everything), then the index
-// downwards.  A key is never 0, which stands for an expert already taken.
-__device__ __forceinline__ uint64_t logit_key(float v, int e) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    const uint32_t m = v != v ? 0u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
-    return ((uint64_t)m << 32) | (uint32_t)(0x7fffffff - e);
-}
-
-__device__ __forceinline__ void wave_topk(const float* __restrict__ lt, int E, int k, int renorm,
-                                          int32_t* __restrict__ idx, float* __restrict__ w) {
+// The order is taken on the float's bits made monotone (both zeros alike, NaN
+// below every number, 0 for an expert that is taken or does not exist), so
+// that it is total and every lane agrees on the winner whatever x holds.
+template <int NQ>
+__device__ __forceinline__ void wave_topk(const float* lt, int E, int k, int renorm, int& idx,
+                                          float& w) {
     const int lane = threadIdx.x & 63;
-    uint32_t live = 0;
-    for (int q = 0; q * 64 + lane < E; ++q) live |= 1u << q;      // E <= 1024
-    float best0 = 0.0f, den = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        uint64_t best = 0;
-        for (int q = 0; q * 64 + lane < E; ++q) {
-            const int e = q * 64 + lane;
-            const uint64_t key = logit_key(lt[e], e);
-            if (((live >> q) & 1u) && key > best) best = key;
-        }
+    float v[NQ];
+    uint32_t key[NQ];
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            const uint64_t o = __shfl_xor((unsigned long long)best, off);
-            best = o > best ? o : best;
+    for (int q = 0; q < NQ; ++q) {
+        const int e = q * 64 + lane;
+        v[q] = e < E ? lt[e] : 0.0f;
+        const uint32_t b = __float_as_uint(v[q] + 0.0f);
+        const uint32_t m = b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+        key[q] = e >= E ? 0u : v[q] != v[q] ? 1u : m;
+    }
+    float first = 0.0f, den = 0.0f;
+    idx = 0;
+    w = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
+        int bq = 0;
+#pragma unroll
+        for (int q = 1; q < NQ; ++q)
+            if (key[q] > best) best = key[q], bq = q;      // the lane's lowest index on a tie
+        const uint32_t top = wave_max_u32(best);
+        // of the lanes that hold it, the one with the lowest expert index
+        const int cand = best == top ? bq * 64 + lane : 0x7fffffff;
+        const int e = NQ == 1 ? __ffsll((unsigned long long)__ballot(best == top)) - 1
+                              : (int)~wave_max_u32(~(uint32_t)cand);
+        const int src = e & 63, sq = e >> 6;
+        float ev = v[0];
+#pragma unroll
+        for (int q = 1; q < NQ; ++q) ev = sq == q ? v[q] : ev;
+        ev = __shfl(ev, src);
+        if (lane == src) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                if (sq == q) key[q] = 0u;
         }
-        const int bi = 0x7fffffff - (int)(uint32_t)best;          // k <= E: always one left
-        const float bv = lt[bi];
-        if ((bi & 63) == lane) live &= ~(1u << (bi >> 6));
-        if (j == 0) best0 = bv;
-        const float ex = expf(bv - best0);
+        if (j == 0) first = ev;
+        const float ex = expf(ev - first);
         den += ex;
-        if (lane == 0) {
-            idx[j] = bi;
-            w[j] = ex;                                             // scaled below
-        }
+        if (lane == j) idx = e, w = ex;
     }
     if (!renorm) {
         den = 0.0f;
-        for (int e = lane; e < E; e += 64) den += expf(lt[e] - best0);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+            if (q * 64 + lane < E) den += expf(v[q] - first);
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1) den += __shfl_xor(den, off);
     }
-    const float inv = 1.0f / den;
-    if (lane == 0)
-        for (int j = 0; j < k; ++j) w[j] *= inv;
+    w /= den;
+}
+
+// Logits of TB = 64 / EB tokens x EB experts per block, one chain per lane of
+// wave 0.
+//
+// A chain's order is fixed (increasing feature index, each product and each
+// sum rounded), so with few tokens its d dependent additions are the kernel's
+// time and all else stays out of their way: wave 0 does nothing but read
+// products from LDS, 32 features ahead of their use, and add.  Waves 1, 2, 3
+// and 5 form the products, half a gate row per thread: they load x and the
+// row NPF chunks of GK features ahead, multiply in fp32 (exactly, for bf16)
+// and store them transposed, one row per chain, in a ring of three chunks:
+// the chunk after the one being added is complete, so the reads ahead cross
+// from chunk to chunk without a wait.
+// Wave 4 does neither: waves go round the four SIMDs, and a second wave on the
+// chain's SIMD would take issue slots from it.  Further waves only meet the
+// barriers.  One token, 16 experts: 3.1 ns per feature (12 us at d 4096)
+// after 3 us to start; additions alone would take 1.9 ns, the rest is the
+// LDS reads, which hold the wave for about 10 clocks each.
+// VE: gate elements per load (16 bytes where a row's length and alignment
+// allow).
+constexpr int GK = 128, GROW = GK + 4;
+struct GateLds {
+    alignas(16) float ps[3][64 * GROW];
+    float lg[64];
+};
+
+// Chunks in flight: eight take 0.3 us each, more than the latency of HBM,
+// where the registers of half a row's loads allow it.
+template <typename T, int EB, int VE>
+constexpr int gate_ahead() {
+    return VE > 1 && EB * sizeof(T) <= 128 ? 8 : 4;
+}
+
+// The logits of tokens t0 .. t0 + TB - 1 and experts e0 .. e0 + EB - 1 into
+// s.lg [TB][EB], and into logits [T, E] when not NULL.
+template <typename T, int EB, int NPF, int VE>
+__device__ __forceinline__ void gate_block(GateLds& s, const T* __restrict__ x,
+                                           const T* __restrict__ Wg,
+                                           const float* __restrict__ bias, int Tn, int d, int E,
+                                           int e0, int t0, float* __restrict__ logits) {
+#pragma clang fp contract(off)
+    constexpr int TB = 64 / EB;
+    constexpr int WL = EB / 2 / VE;                   // loads of half a gate row
+    constexpr int G = 32;                             // features read ahead
+    const int tid = threadIdx.x;
+    // the wave number as a scalar: the roles are a uniform branch, and each
+    // side meets the other's barriers, one per chunk
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nc = (d + GK - 1) / GK;
+
+    if (wv == 4 || wv > 5) {
+        for (int c = 0; c < nc; ++c) __syncthreads();
+    } else if (wv > 0) {
+        const int st = (tid - (wv == 5 ? 128 : 64)) % GK;             // feature of a chunk
+        const int el = (tid - (wv == 5 ? 128 : 64)) / GK * (EB / 2);  // first expert
+        typedef std::conditional_t<VE == 1, T, u32x4_t> wload_t;
+        wload_t wr[NPF][WL];
+        T xr[NPF][TB];
+        // loads past the matrix read a valid element instead: features past d
+        // are never summed, experts and tokens past the end never stored
+        auto fetch = [&](int c, wload_t (&w)[WL], T (&xv)[TB]) {
+            const int kk = min(c * GK + st, d - 1);
+            const T* row = Wg + (long)kk * E;
+#pragma unroll
+            for (int q = 0; q < WL; ++q)
+                w[q] = *reinterpret_cast<const wload_t*>(row + min(e0 + el + q * VE, E - VE));
+#pragma unroll
+            for (int t = 0; t < TB; ++t) xv[t] = x[(long)min(t0 + t, Tn - 1) * d + kk];
+        };
+        auto stash = [&](int b, const wload_t (&w)[WL], const T (&xv)[TB]) {
+            float xf[TB];
+#pragma unroll
+            for (int t = 0; t < TB; ++t) xf[t] = Elem<T>::ld(&xv[t]);
+#pragma unroll
+            for (int q = 0; q < WL; ++q) {
+                float o[VE];
+                if constexpr (VE == 1) {
+                    const T v = w[q];
+                    o[0] = Elem<T>::ld(&v);
+                } else {
+                    unpack16<T>(w[q], o);
+                }
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    if (t > 0 && t0 + t >= Tn) break;
+#pragma unroll
+                    for (int a = 0; a < VE; ++a)
+                        s.ps[b][(t * EB + el + q * VE + a) * GROW + st] = xf[t] * o[a];
+                }
+            }
+        };
+#pragma unroll
+        for (int c = 0; c < NPF; ++c) fetch(c, wr[c], xr[c]);
+        // chunk c goes to LDS while the chains add chunk c - 2, over chunk c - 3
+        int b = 0;
+        for (int cb = 0; cb < nc; cb += NPF) {
+#pragma unroll
+            for (int u = 0; u < NPF; ++u) {
+                const int c = cb + u;
+                if (c >= nc) break;
+                stash(b, wr[u], xr[u]);
+                b = b == 2 ? 0 : b + 1;
+                fetch(c + NPF, wr[u], xr[u]);
+                __syncthreads();
+            }
+        }
+    } else {
+        float acc = 0.0f;
+        float4 pv[2][G / 4];
+        // Reads the next group, at p, then adds group b.  The fences keep the
+        // compiler from moving the reads behind the additions; one wait for the
+        // whole group (all but the G / 4 reads just issued) stands for the one
+        // per read that it would place.
+        static_assert(G / 4 == 8, "the wait below leaves 8 reads in flight");
+        auto group = [&](const float* p, int b, bool add) {
+#pragma unroll
+            for (int q = 0; q < G / 4; ++q)
+                pv[1 - b][q] = *reinterpret_cast<const float4*>(p + 4 * q);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            if (!add) return;
+            __builtin_amdgcn_s_waitcnt(0xc87f);                   // lgkmcnt(8)
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < G / 4; ++q) {
+                acc = acc + pv[b][q].x;
+                acc = acc + pv[b][q].y;
+                acc = acc + pv[b][q].z;
+                acc = acc + pv[b][q].w;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        __syncthreads();                                          // chunk 0 is in LDS
+        group(s.ps[0] + tid * GROW, 1, false);
+        int b = 0;
+        for (int c = 0; c < nc; ++c) {
+            if (c + 1 < nc) __syncthreads();                      // chunk c + 1 is in LDS
+            const float* p = s.ps[b] + tid * GROW;
+            b = b == 2 ? 0 : b + 1;
+            const float* pn = s.ps[b] + tid * GROW;
+            const int kn = min(GK, d - c * GK);                   // a multiple of 2 G
+            for (int k0 = 0; k0 < kn; k0 += 2 * G) {
+                group(p + k0 + G, 0, true);
+                group(k0 + 2 * G < kn ? p + k0 + 2 * G : pn, 1, true);   // (the last: unused)
+            }
+        }
+        const int e = e0 + tid % EB, t = t0 + tid / EB;
+        if (bias) acc = acc + bias[min(e, E - 1)];
+        s.lg[tid] = acc;
+        if (logits && e < E && t < Tn) logits[(long)t * E + e] = acc;
+    }
+    __syncthreads();
+}
+
+template <typename T, int EB, int NPF, int VE>
+__global__ __launch_bounds__(384) void few_gate_kernel(
+    const T* __restrict__ x, const T* __restrict__ Wg, const float* __restrict__ bias, int Tn,
+    int d, int E, int k, int renorm, float* __restrict__ logits, int32_t* __restrict__ topk_idx,
+    float* __restrict__ topk_w) {
+    constexpr int TB = 64 / EB;
+    __shared__ GateLds s;
+    const int t0 = blockIdx.y * TB;
+    gate_block<T, EB, NPF, VE>(s, x, Wg, bias, Tn, d, E, blockIdx.x * EB, t0, logits);
+    if (E > EB) return;                                           // few_topk follows
+    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wv < TB && t0 + wv < Tn) {
+        int e;
+        float w;
+        wave_topk<1>(s.lg + wv * EB, E, k, renorm, e, w);
+        if (lane < k) {
+            topk_idx[(long)(t0 + wv) * k + lane] = e;
+            topk_w[(long)(t0 + wv) * k + lane] = w;
+        }
+    }
 }
 
 __global__ __launch_bounds__(256) void few_topk_kernel(const float* __restrict__ logits, int Tn,
@@ -192,7 +298,41 @@ __global__ __launch_bounds__(256) void few_topk_kernel(const float* __restrict__
                                                        float* __restrict__ w) {
     const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= Tn) return;
-    wave_topk(logits + (long)t * E, E, k, renorm, idx + (long)t * k, w + (long)t * k);
+    int e;
+    float we;
+    wave_topk<16>(logits + (long)t * E, E, k, renorm, e, we);
+    const int lane = threadIdx.x & 63;
+    if (lane < k) {
+        idx[(long)t * k + lane] = e;
+        w[(long)t * k + lane] = we;
+    }
+}
+
+template <typename T, int EB>
+void few_gate_go(const T* x, const T* Wg, const float* bias, int Tn, int d, int E, int k,
+                 int renorm, float* logits, int32_t* idx, float* w, hipStream_t s) {
+    constexpr int VE = 16 / sizeof(T);
+    const dim3 grid(cdiv(E, EB), cdiv(Tn, 64 / EB));
+    if (E % VE == 0 && aligned16(Wg))
+        MOE_LAUNCH("few_gate", s,
+                   (few_gate_kernel<T, EB, gate_ahead<T, EB, VE>(), VE><<<grid, 384, 0, s>>>(
+                       x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w)));
+    else
+        MOE_LAUNCH("few_gate", s,
+                   (few_gate_kernel<T, EB, gate_ahead<T, EB, 1>(), 1><<<grid, 384, 0, s>>>(
+                       x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w)));
+    if (E > EB)
+        MOE_LAUNCH("few_topk", s,
+                   (few_topk_kernel<<<cdiv(Tn, 4), 256, 0, s>>>(logits, Tn, E, k, renorm, idx,
+                                                                w)));
+}
+
+template <typename T>
+void few_gate(const T* x, const T* Wg, const float* bias, int Tn, int d, int E, int k, int renorm,
+              float* logits, int32_t* idx, float* w, hipStream_t s) {
+    if (E <= 16) few_gate_go<T, 16>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
+    else if (E <= 32) few_gate_go<T, 32>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
+    else few_gate_go<T, 64>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
 }
 
 // ------------------------------------------------------- experts' row lists
@@ -260,7 +400,8 @@ template <> struct Core<bf16_t> {
     static constexpr int KSTEP = 32;                  // rows of W per step
     static constexpr int NL = 8;                      // row loads per lane and step
     template <int VW> struct Raw { uint32_t w[NL][VW / 2]; };
-    struct XRaw { u32x4_t v; };
+    // eight k of a token; LO: as the sum of two bf16
+    template <bool LO> struct XRaw { u32x4_t v[LO ? 2 : 1]; };
 
     template <int VW>
     static __device__ __forceinline__ void load(const bf16_t* W, long ldw, int k0, int g,
@@ -282,11 +423,14 @@ template <> struct Core<bf16_t> {
             }
         }
     }
-    static __device__ __forceinline__ void loadx(const bf16_t* xrow, int k0, int g, XRaw& r) {
-        r.v = ld16<false>(xrow + k0 + g * 8);
+    template <bool LO>
+    static __device__ __forceinline__ void loadx(const bf16_t* xrow, long lo, int k0, int g,
+                                                 XRaw<LO>& r) {
+        r.v[0] = ld16<false>(xrow + k0 + g * 8);
+        if constexpr (LO) r.v[1] = ld16<false>(xrow + lo + k0 + g * 8);
     }
-    template <int VW, int NT>
-    static __device__ __forceinline__ void mul(const Raw<VW>& r, const XRaw (&x)[NT], int nt,
+    template <int VW, int NT, bool LO>
+    static __device__ __forceinline__ void mul(const Raw<VW>& r, const XRaw<LO> (&x)[NT],
                                                f32x4 (&acc)[NT][VW]) {
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
@@ -299,10 +443,13 @@ template <> struct Core<bf16_t> {
                                              (j & 1) ? 0x07060302u : 0x05040100u);
             const bf16x8 av = __builtin_bit_cast(bf16x8, a);
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-                if (i < nt)
+            for (int i = 0; i < NT; ++i) {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    av, __builtin_bit_cast(bf16x8, x[i].v[0]), acc[i][j], 0, 0, 0);
+                if constexpr (LO)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        av, __builtin_bit_cast(bf16x8, x[i].v), acc[i][j], 0, 0, 0);
+                        av, __builtin_bit_cast(bf16x8, x[i].v[1]), acc[i][j], 0, 0, 0);
+            }
         }
     }
 };
@@ -311,7 +458,7 @@ template <> struct Core<float> {
     static constexpr int KSTEP = 16;
     static constexpr int NL = 4;
     template <int VW> struct Raw { f32x4 w[NL]; };
-    struct XRaw { f32x4 v; };
+    template <bool LO> struct XRaw { f32x4 v; };
 
     template <int VW>
     static __device__ __forceinline__ void load(const float* W, long ldw, int k0, int g,
@@ -322,11 +469,13 @@ template <> struct Core<float> {
         for (int i = 0; i < NL; ++i)
             r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i * ldw));
     }
-    static __device__ __forceinline__ void loadx(const float* xrow, int k0, int g, XRaw& r) {
+    template <bool LO>
+    static __device__ __forceinline__ void loadx(const float* xrow, long, int k0, int g,
+                                                 XRaw<LO>& r) {
         r.v = *reinterpret_cast<const f32x4*>(xrow + k0 + g * 4);
     }
-    template <int VW, int NT>
-    static __device__ __forceinline__ void mul(const Raw<VW>& r, const XRaw (&x)[NT], int nt,
+    template <int VW, int NT, bool LO>
+    static __device__ __forceinline__ void mul(const Raw<VW>& r, const XRaw<LO> (&x)[NT],
                                                f32x4 (&acc)[NT][VW]) {
 #pragma unroll
         for (int i = 0; i < NL; ++i)
@@ -334,46 +483,40 @@ template <> struct Core<float> {
             for (int j = 0; j < VW; ++j)
 #pragma unroll
                 for (int m = 0; m < NT; ++m)
-                    if (m < nt)
-                        acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(r.w[i][j], x[m].v[i],
-                                                                        acc[m][j], 0, 0, 0);
+                    acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(r.w[i][j], x[m].v[i],
+                                                                    acc[m][j], 0, 0, 0);
     }
 };
 
-template <typename T, int VW, int NT, bool DUAL>
-__device__ __forceinline__ void strip_product(const T* W, const T* W3, long ldw,
-                                              const T* const (&xrow)[NT], int nt, int s0, int s1,
-                                              f32x4 (&acc)[NT][VW],
-                                              f32x4 (&acc3)[DUAL ? NT : 1][DUAL ? VW : 1]) {
+// NB - 1 steps are in flight while one is multiplied.
+template <typename T, int VW, int NT, int NB, bool LO>
+__device__ __forceinline__ void strip_product(const T* W, long ldw, const T* const (&xrow)[NT],
+                                              long lo, int s0, int s1, f32x4 (&acc)[NT][VW]) {
     typedef Core<T> C;
     const int g = (threadIdx.x & 63) >> 4;
-    typename C::template Raw<VW> wa[2], wb[2];
-    typename C::XRaw xa[2][NT];
+    typename C::template Raw<VW> wr[NB];
+    typename C::template XRaw<LO> xr[NB][NT];
     auto fetch = [&](int s, int b) {
-        C::template load<VW>(W, ldw, s * C::KSTEP, g, wa[b]);
-        if constexpr (DUAL) C::template load<VW>(W3, ldw, s * C::KSTEP, g, wb[b]);
+        C::template load<VW>(W, ldw, s * C::KSTEP, g, wr[b]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) C::loadx(xrow[i], s * C::KSTEP, g, xa[b][i]);
+        for (int i = 0; i < NT; ++i) C::template loadx<LO>(xrow[i], lo, s * C::KSTEP, g, xr[b][i]);
     };
-    auto mul = [&](int b) {
-        C::template mul<VW, NT>(wa[b], xa[b], nt, acc);
-        if constexpr (DUAL) C::template mul<VW, NT>(wb[b], xa[b], nt, acc3);
-    };
-    if (s0 >= s1) return;
-    fetch(s0, 0);
+#pragma unroll
+    for (int u = 0; u < NB - 1; ++u)
+        if (s0 + u < s1) fetch(s0 + u, u);
     int s = s0;
-    for (; s + 2 < s1; s += 2) {
-        fetch(s + 1, 1);
-        mul(0);
-        fetch(s + 2, 0);
-        mul(1);
+    for (; s + 2 * NB - 1 <= s1; s += NB) {            // no branch between the loads
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+            fetch(s + u + NB - 1, (u + NB - 1) % NB);
+            C::template mul<VW, NT, LO>(wr[u], xr[u], acc);
+        }
     }
-    if (s + 1 < s1) {
-        fetch(s + 1, 1);
-        mul(0);
-        mul(1);
-    } else {
-        mul(0);
+#pragma unroll
+    for (int u = 0; u < 2 * NB - 2; ++u) {             // the last steps
+        if (s + u >= s1) break;
+        if (s + u + NB - 1 < s1) fetch(s + u + NB - 1, (u + NB - 1) % NB);
+        C::template mul<VW, NT, LO>(wr[u % NB], xr[u % NB], acc);
     }
 }
 
@@ -410,152 +553,306 @@ __device__ __forceinline__ void store4(bf16_t* p, const float* v) {
 }
 
 struct FewArgs {
-    const void* x;              // up: tokens [T, K]; down: h [pairs, K]
+    const void* x;              // up: tokens [T, K]; down: h [pairs, K] (bf16: and h_lo)
     const void *W, *W3;         // [E, K, N]
     const int32_t* idx;         // [pairs]
-    void* out;                  // up: h [pairs, N]; down: partial [KS][pairs][N] fp32
+    void* out;                  // up: h [pairs, N] (bf16: and h_lo); down: partial
+                                // [KS][pairs][N] fp32
     int pairs, k, E, K, N;
 };
+struct RowsLds {
+    uint32_t bits[32];
+    int rows[kFewTokens], res[2];
+};
+
+// The block's expert (the blockIdx.y-th that any pair chose) and its rows, or
+// -1.  With one token the pairs' experts differ: the slot's own, and no search.
+__device__ __forceinline__ int block_expert(const FewArgs& p, const int32_t* idx, RowsLds& r,
+                                            int* n) {
+    const int slot = blockIdx.y;
+    if (p.pairs == p.k) {
+        const int e = idx[slot];
+        // every wave writes the one row and reads what it wrote itself
+        if ((threadIdx.x & 63) == 0) r.rows[0] = slot;
+        __builtin_amdgcn_wave_barrier();
+        *n = 1;
+        return (unsigned)e < (unsigned)p.E ? e : -1;
+    }
+    return expert_rows(idx, p.pairs, p.E, slot, r.bits, r.rows, r.res, n);
+}
 
 // UP: h[p] = act(x[p / k] W[e]) (DUAL: * x W3[e]) for the expert's pairs p.
 // Down (UP = false): partial[ks][p] = h[p] W[e] over the ks-th chunk of K.
 // Grid: strips of 16 * VW columns, experts hit, chunks.  The NW waves of a
-// block take consecutive parts of the chunk; their sums meet in LDS, in order.
-template <typename T, int VW, int NT, int NW, bool UP, bool DUAL>
-__global__ __launch_bounds__(64 * NW, 2) void few_product_kernel(FewArgs p) {
-    constexpr int BN = 16 * VW, LD = BN + 4;
-    constexpr int SLABS = NW * 16 * LD;
-    __shared__ __attribute__((aligned(16))) float red[SLABS * (DUAL ? 2 : 1)];
-    __shared__ uint32_t bits[32];
-    __shared__ int rows[kFewTokens], res[2];
+// block take consecutive parts of the chunk (DUAL: one half of them W, the other
+// W3, which keeps the accumulators of a wave to one product); their sums meet
+// in LDS (red: NW * 16 * (16 VW + 4) floats), in order.
+//
+// h in bf16 is kept as the sum of two (h_lo, the rest that the first rounding
+// left, follows h): the matrix cores wait for memory here anyway, and one
+// rounding of h was the largest part of y's error (0.0024 of |y| against
+// 0.0017 for y's own rounding).
+template <typename T, int VW, int NTM, int NW, bool UP, bool DUAL>
+__device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, const int* rows,
+                                              float* red) {
+    constexpr int KW = DUAL ? NW / 2 : NW;             // waves that share a product's chunk
+    constexpr bool LO = !UP && sizeof(T) == 2;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int n;
-    const int e = expert_rows(p.idx, p.pairs, p.E, blockIdx.y, bits, rows, res, &n);
-    if (e < 0) return;
-    const int nt = (n + 15) >> 4;
-    const int n0 = blockIdx.x * BN;
     const int c = lane & 15;
-    // columns past N (a multiple of 64) read the last ones of the row instead
-    const int col = min(n0 + c * VW, p.N - VW);
-    const T* W = static_cast<const T*>(p.W) + (long)e * p.K * p.N + col;
-    const T* W3 = DUAL ? static_cast<const T*>(p.W3) + (long)e * p.K * p.N + col : nullptr;
-    const T* xrow[NT];
+    const T* We = static_cast<const T*>(DUAL && wv >= KW ? p.W3 : p.W) + (long)e * p.K * p.N;
+    const int steps = p.K / Core<T>::KSTEP;
+    const int units = gridDim.z * KW, u = blockIdx.z * KW + wv % KW;
+    const int s0 = (int)((long)steps * u / units), s1 = (int)((long)steps * (u + 1) / units);
+    // V columns per lane from column n0, NT tiles of 16 rows, NB steps of
+    // registers; again: red may still be read from the call before
+    auto body = [&](auto vc, auto tiles, auto depth, int n0, bool again) {
+        constexpr int V = decltype(vc)::value, NT = decltype(tiles)::value;
+        constexpr int BN = 16 * V, LD = BN + 4;
+        const T* xrow[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int q = rows[min(i * 16 + c, n - 1)];   // rows past n: the last one's again
-        xrow[i] = static_cast<const T*>(p.x) + (long)(UP ? q / p.k : q) * p.K;
-    }
-    f32x4 acc[NT][VW], acc3[DUAL ? NT : 1][DUAL ? VW : 1];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < VW; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (DUAL) {
+        for (int i = 0; i < NT; ++i) {
+            const int q = rows[min(i * 16 + c, n - 1)];  // rows past n: the last one's again
+            xrow[i] = static_cast<const T*>(p.x) + (long)(UP ? q / p.k : q) * p.K;
+        }
+        f32x4 acc[NT][V];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < VW; ++j) acc3[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    const int steps = p.K / Core<T>::KSTEP;
-    const int units = gridDim.z * NW, u = blockIdx.z * NW + wv;
-    strip_product<T, VW, NT, DUAL>(W, W3, p.N, xrow, nt, (int)((long)steps * u / units),
-                                   (int)((long)steps * (u + 1) / units), acc, acc3);
+            for (int j = 0; j < V; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // columns past N (a multiple of 64) read the last ones of the row instead
+        strip_product<T, V, NT, decltype(depth)::value, LO>(
+            We + min(n0 + c * V, p.N - V), p.N, xrow, (long)p.pairs * p.K, s0, s1, acc);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        if (i >= nt) break;
-        if (i > 0) __syncthreads();
-        slab_store<VW>(red + wv * 16 * LD, acc[i]);
-        if constexpr (DUAL) slab_store<VW>(red + SLABS + wv * 16 * LD, acc3[i]);
-        __syncthreads();
-        for (int q = tid; q < 16 * BN / 4; q += 64 * NW) {
-            const int row = q / (BN / 4), cl = q % (BN / 4) * 4;
-            if (i * 16 + row >= n || n0 + cl >= p.N) continue;
-            const float4 s = slab_sum<VW, NW>(red, row, cl);
-            const int pr = rows[i * 16 + row];
-            float v[4] = {s.x, s.y, s.z, s.w};
-            if constexpr (UP) {
-                if constexpr (DUAL) {
-                    const float4 h3 = slab_sum<VW, NW>(red + SLABS, row, cl);
-                    v[0] = silu_f(v[0]) * h3.x;
-                    v[1] = silu_f(v[1]) * h3.y;
-                    v[2] = silu_f(v[2]) * h3.z;
-                    v[3] = silu_f(v[3]) * h3.w;
+        for (int i = 0; i < NT; ++i) {
+            if (i * 16 >= n) break;
+            if (i > 0 || again) __syncthreads();
+            slab_store<V>(red + wv * 16 * LD, acc[i]);
+            __syncthreads();
+            for (int q = tid; q < 16 * BN / 4; q += 64 * NW) {
+                const int row = q / (BN / 4), cl = q % (BN / 4) * 4;
+                if (i * 16 + row >= n || n0 + cl >= p.N) continue;
+                const float4 s = slab_sum<V, KW>(red, row, cl);
+                const int pr = rows[i * 16 + row];
+                float v[4] = {s.x, s.y, s.z, s.w};
+                if constexpr (UP) {
+                    if constexpr (DUAL) {
+                        const float4 h3 = slab_sum<V, KW>(red + KW * 16 * LD, row, cl);
+                        v[0] = silu_f(v[0]) * h3.x;
+                        v[1] = silu_f(v[1]) * h3.y;
+                        v[2] = silu_f(v[2]) * h3.z;
+                        v[3] = silu_f(v[3]) * h3.w;
+                    } else {
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) v[a] = gelu_f(v[a]);
+                    }
+                    T* h = static_cast<T*>(p.out) + (long)pr * p.N + n0 + cl;
+                    store4(h, v);
+                    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            const float hi = bf16_to_f32(f32_to_bf16(v[a]));
+                            v[a] = fabsf(hi) < INFINITY ? v[a] - hi : 0.0f;   // NaN, infinity: hi
+                        }
+                        store4(h + (long)p.pairs * p.N, v);
+                    }
                 } else {
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) v[a] = gelu_f(v[a]);
+                    store4(static_cast<float*>(p.out) +
+                               ((long)blockIdx.z * p.pairs + pr) * p.N + n0 + cl, v);
                 }
-                // h in the layer's type, as moe_expert_ffn_fwd keeps it
-                store4(static_cast<T*>(p.out) + (long)pr * p.N + n0 + cl, v);
+            }
+        }
+    };
+    // The expert's rows in tiles of 16, as many as it has: a wave computes 1,
+    // 2 or 4 of them.  Four tiles of h and h_lo at VW = 8 would not fit the
+    // registers: the strip goes in two halves then.
+    using std::integral_constant;
+    const int n0 = blockIdx.x * 16 * VW;
+    constexpr integral_constant<int, VW> vw{};
+    constexpr integral_constant<int, 2> two{};
+    if constexpr (NTM >= 4) {
+        constexpr integral_constant<int, 4> four{};
+        if (n > 32) {
+            if constexpr (LO && VW == 8) {
+                body(four, four, two, n0, false);
+                return body(four, four, two, n0 + 64, true);
             } else {
-                store4(static_cast<float*>(p.out) +
-                           ((long)blockIdx.z * p.pairs + pr) * p.N + n0 + cl, v);
+                return body(vw, four, two, n0, false);
             }
         }
     }
+    if constexpr (NTM >= 2) {
+        if (n > 16) return body(vw, two, two, n0, false);
+    }
+    body(vw, integral_constant<int, 1>{}, integral_constant<int, VW == 8 ? 2 : 3>{}, n0, false);
 }
 
-// y[t] = sum_j w[t,j] sum_s partial[s][t k + j], rounded once.
+template <typename T, int VW, int NTM, int NW, bool UP, bool DUAL>
+__global__ __launch_bounds__(64 * NW, 2) void few_product_kernel(FewArgs p) {
+    __shared__ __attribute__((aligned(16))) float red[NW * 16 * (16 * VW + 4)];
+    __shared__ RowsLds r;
+    int n;
+    const int e = block_expert(p, p.idx, r, &n);
+    if (e < 0) return;
+    product_block<T, VW, NTM, NW, UP, DUAL>(p, e, n, r.rows, red);
+}
+
+// The gate and the up product in one launch, for a gate that one block of
+// gate_block covers (E <= 16, T <= 4): every block works the same logits and
+// choice out for itself, and the first one stores them.  That costs a read of
+// the gate's matrix from L2 per block and saves a launch and the round trip
+// of the choice through memory.
+struct GateArgs {
+    const void *x, *Wg;
+    const float* bias;
+    int T, d, renorm;
+    float* logits;
+    int32_t* idx;
+    float* w;
+};
+template <typename T, int VE, bool DUAL>
+__global__ __launch_bounds__(512, 2) void few_gate_up_kernel(GateArgs g, FewArgs p) {
+    constexpr int EB = 16, TB = 4, VW = 4, NW = 8;
+    // the product's slabs take the gate's place once the choice is made
+    __shared__ union {
+        GateLds gate;
+        alignas(16) float red[NW * 16 * (16 * VW + 4)];
+    } s;
+    __shared__ RowsLds r;
+    __shared__ int32_t idx[TB * EB];                              // k <= E <= 16
+    const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+    gate_block<T, EB, gate_ahead<T, EB, VE>(), VE>(
+        s.gate, static_cast<const T*>(g.x), static_cast<const T*>(g.Wg), g.bias, g.T, g.d, p.E, 0,
+        0, first ? g.logits : nullptr);
+    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (wv < g.T) {
+        int e;
+        float w;
+        wave_topk<1>(s.gate.lg + wv * EB, p.E, p.k, g.renorm, e, w);
+        if (lane < p.k) {
+            idx[wv * p.k + lane] = e;
+            if (first) {
+                g.idx[wv * p.k + lane] = e;
+                g.w[wv * p.k + lane] = w;
+            }
+        }
+    }
+    __syncthreads();
+    int n;
+    const int e = block_expert(p, idx, r, &n);
+    if (e < 0) return;
+    product_block<T, VW, 1, NW, true, DUAL>(p, e, n, r.rows, s.red);
+}
+
+// y[t] = sum over a token's k slots and ks chunks of w[t,j] partial[s][t k + j],
+// rounded once.  A block takes 128 columns of one token; eight groups of 32
+// threads take every eighth (slot, chunk) each, and meet in LDS, in order.
+constexpr int kCombineCols = 128;
 template <typename T>
 __global__ __launch_bounds__(256) void few_combine_kernel(const float* __restrict__ partial,
                                                           const float* __restrict__ w, int Tn,
                                                           int k, int d, int ks,
                                                           T* __restrict__ y) {
-    const int q = blockIdx.x * 256 + threadIdx.x;
-    const int per = d / 4;
-    if (q >= Tn * per) return;
-    const int t = q / per, c = q % per * 4;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < k; ++j) {
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int z = 0; z < ks; ++z) {
-            const float4 a = *reinterpret_cast<const float4*>(
-                partial + ((long)z * Tn * k + t * k + j) * d + c);
-            s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+    __shared__ __attribute__((aligned(16))) float sums[8][kCombineCols];
+    const int t = blockIdx.y, part = threadIdx.x >> 5;
+    const int c = blockIdx.x * kCombineCols + (threadIdx.x & 31) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < d) {
+        const float* p = partial + (long)t * k * d + c;
+        const int n = k * ks;
+#pragma unroll 4
+        for (int q = part; q < n; q += 8) {
+            const int z = q / k, j = q - z * k;
+            const float4 a =
+                *reinterpret_cast<const float4*>(p + ((long)z * Tn * k + j) * d);
+            const float wj = w[t * k + j];
+            v.x = fmaf(wj, a.x, v.x);
+            v.y = fmaf(wj, a.y, v.y);
+            v.z = fmaf(wj, a.z, v.z);
+            v.w = fmaf(wj, a.w, v.w);
         }
-        const float wj = w[t * k + j];
-        v[0] = fmaf(wj, s.x, v[0]);
-        v[1] = fmaf(wj, s.y, v[1]);
-        v[2] = fmaf(wj, s.z, v[2]);
-        v[3] = fmaf(wj, s.w, v[3]);
     }
-    store4(y + (long)t * d + c, v);
+    *reinterpret_cast<float4*>(&sums[part][(threadIdx.x & 31) * 4]) = v;
+    __syncthreads();
+    if (part > 0 || c >= d) return;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) {
+        const float4 a = *reinterpret_cast<const float4*>(&sums[q][threadIdx.x * 4]);
+        v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+    }
+    const float o[4] = {v.x, v.y, v.z, v.w};
+    store4(y + (long)t * d + c, o);
 }
 
 // ------------------------------------------------------------------- plan
 struct FewPlan {
     int slots;                   // experts hit at most
-    int up_vw, down_vw, up_strips, down_strips, ks;
+    bool fuse_gate;
+    int up_vw, up_nw, up_strips, down_vw, down_nw, down_strips, ks;
     size_t logits, idx, w, h, partial, total;
 };
+
+constexpr double kFewWaves = 600, kChunkWaves = 3000;
+constexpr int kFewChunks = 16;
 
 bool few_sizes_ok(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     return T >= 0 && d >= 64 && d % 64 == 0 && f >= 64 && f % 64 == 0 && E >= 1 && E <= 1024 &&
            k >= 1 && k <= E && (act == MOE_ACT_GELU || act == MOE_ACT_SWIGLU) &&
            (dt == MOE_F32 || dt == MOE_BF16);
 }
-bool few_limits_ok(int T, int k) { return T <= kFewTokens && (long)T * k <= kFewPairs; }
+bool few_limits_ok(int T, int k) { return T <= kFewTokens && k <= kFewSlots; }
 
 FewPlan few_plan(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     FewPlan p;
     const int pairs = T * k;
     p.slots = min(E, pairs);
-    // 16 VW columns a strip.  Two weights at once over more than 16 tokens
-    // would not fit the registers at VW = 8
-    p.up_vw = dt == MOE_BF16 && !(act == MOE_ACT_SWIGLU && T > 16) ? 8 : 4;
-    p.down_vw = dt == MOE_BF16 ? 8 : 4;
+    const int wide = dt == MOE_BF16 ? 8 : 4;
+    // Waves of a product over n columns, from the experts that T tokens hit
+    // when the gate prefers none.
+    const double hit = E * (1.0 - pow(1.0 - (double)k / E, T));
+    auto waves = [&](int n, int vw, int nw) { return cdiv(n, 16 * vw) * hit * nw; };
+    // Strips of 16 wide columns and 4 waves stream best (bf16: 256-byte pieces
+    // of a row; one token of d 4096, f 14336, 8 of 32 experts: 476 us against
+    // 503 with strips of half the width).  Below kFewWaves such waves there is
+    // not enough in flight to cover the latency of HBM, and strips of half the
+    // width with 8 waves are faster (d 4096, f 1536, 8 of 128 experts: 100
+    // against 117 us; d 1024, f 4096, 2 of 8: 22.1 against 22.9).
+    p.up_vw = wide;
+    p.up_nw = 4;
+    // The gate's fusion: what one gate_block covers, in one round of blocks
+    // (two rounds would work the gate out twice).  One token, d 1024, 8
+    // experts: 21.4 us against 23.4 with a launch of its own.
+    p.fuse_gate = E <= 16 && T <= 4 && cdiv(f, 64) * p.slots <= 256;
+    if (p.fuse_gate || waves(f, wide, 4) < kFewWaves) p.up_vw = 4, p.up_nw = 8;
     p.up_strips = cdiv(f, 16 * p.up_vw);
-    p.down_strips = cdiv(d, 16 * p.down_vw);
+    // The down product's reduction f is long and its columns are few: chunks
+    // of it until kChunkWaves waves run, each with at least 8 (narrow strips: 2)
+    // steps to go.  (T 48, d 1024, f 4096, 64 experts: 2 chunks 73 us, one 82;
+    // T 16, f 1024: one 78, 2 chunks of 4 steps 81.)
     const int steps = f / (dt == MOE_BF16 ? 32 : 16);
-    int ks = 1;
-    while (ks < 16 && p.down_strips * p.slots * ks < 512 && steps >= ks * 2 * 4 * 2) ks *= 2;
+    auto chunks = [&](int vw, int nw, int least) {
+        int ks = 1;
+        while (ks < kFewChunks && waves(d, vw, nw) * ks < kChunkWaves &&
+               steps >= ks * 2 * nw * least)
+            ks *= 2;
+        return ks;
+    };
+    p.down_vw = wide;
+    p.down_nw = 4;
+    int ks = chunks(wide, 4, 8);
+    if (waves(d, wide, 4) * ks < kFewWaves) {
+        p.down_vw = 4;
+        p.down_nw = 8;
+        ks = chunks(4, 8, 2);
+    }
+    p.down_strips = cdiv(d, 16 * p.down_vw);
     p.ks = ks;
     const size_t es = dt == MOE_BF16 ? 2 : 4;
     p.logits = 0;
     p.idx = align_up(sizeof(float) * (size_t)T * E, 256);
     p.w = align_up(p.idx + sizeof(int32_t) * pairs, 256);
     p.h = align_up(p.w + sizeof(float) * pairs, 256);
-    p.partial = align_up(p.h + es * pairs * f, 256);
+    p.partial = align_up(p.h + (dt == MOE_BF16 ? 2 : 1) * es * pairs * f, 256);   // h, h_lo
     p.total = align_up(p.partial + sizeof(float) * (size_t)ks * pairs * d, 256);
     return p;
 }
@@ -565,28 +862,56 @@ moe_status few_run(const void* x, const void* Wg, const float* bias, const void*
                    const void* W3, const void* W2, int Tn, int d, int f, int E, int k, int renorm,
                    moe_act act, const FewPlan& p, float* logits, int32_t* idx, float* w, void* y,
                    char* ws, hipStream_t s) {
-    MOE_LAUNCH("few_logits", s,
-               (few_logits_kernel<T><<<dim3(cdiv(E, GEXP), cdiv(Tn, GTOK)), 256, 0, s>>>(
-                   static_cast<const T*>(x), static_cast<const T*>(Wg), bias, Tn, d, E,
-                   logits)));
-    MOE_LAUNCH("few_topk", s,
-               (few_topk_kernel<<<cdiv(Tn, 4), 256, 0, s>>>(logits, Tn, E, k, renorm, idx, w)));
     const int pairs = Tn * k;
     FewArgs u{x, W1, W3, idx, ws + p.h, pairs, k, E, d, f};
     const dim3 gu(p.up_strips, p.slots, 1), gd(p.down_strips, p.slots, p.ks);
-    constexpr int VW = sizeof(T) == 2 ? 8 : 4;
-    constexpr int VWD = NT == 1 ? VW : 4;
-    if (act == MOE_ACT_SWIGLU)
-        MOE_LAUNCH("few_up_swiglu", s,
-                   (few_product_kernel<T, VWD, NT, 4, true, true><<<gu, 256, 0, s>>>(u)));
-    else
-        MOE_LAUNCH("few_up_gelu", s,
-                   (few_product_kernel<T, VW, NT, 4, true, false><<<gu, 256, 0, s>>>(u)));
+    const bool sw = act == MOE_ACT_SWIGLU;
+    if (!p.fuse_gate)
+        few_gate<T>(static_cast<const T*>(x), static_cast<const T*>(Wg), bias, Tn, d, E, k, renorm,
+                    logits, idx, w, s);
+    auto product = [&](const char* name, auto up, auto dual, int vw, int nw, dim3 grid,
+                       const FewArgs& a) {
+        using std::integral_constant;
+        auto go = [&](auto vwc, auto nwc) {
+            constexpr int NWC = decltype(nwc)::value;
+            MOE_LAUNCH(name, s,
+                       (few_product_kernel<T, decltype(vwc)::value, NT, NWC, decltype(up)::value,
+                                           decltype(dual)::value><<<grid, 64 * NWC, 0, s>>>(a)));
+        };
+        auto by_nw = [&](auto vwc) {
+            if (nw == 8) go(vwc, integral_constant<int, 8>{});
+            else go(vwc, integral_constant<int, 4>{});
+        };
+        if constexpr (sizeof(T) == 2)
+            if (vw == 8) return by_nw(integral_constant<int, 8>{});
+        by_nw(integral_constant<int, 4>{});
+    };
+    if (p.fuse_gate) {
+        if constexpr (NT == 1) {
+            const GateArgs g{x, Wg, bias, Tn, d, renorm, logits, idx, w};
+            auto go = [&](auto ve, auto dual) {
+                MOE_LAUNCH("few_gate_up", s,
+                           (few_gate_up_kernel<T, decltype(ve)::value, decltype(dual)::value>
+                            <<<gu, 512, 0, s>>>(g, u)));
+            };
+            constexpr int VE = 16 / sizeof(T);
+            std::integral_constant<int, VE> wide;
+            std::integral_constant<int, 1> one;
+            if (E % VE == 0 && aligned16(Wg)) {
+                if (sw) go(wide, std::true_type{}); else go(wide, std::false_type{});
+            } else {
+                if (sw) go(one, std::true_type{}); else go(one, std::false_type{});
+            }
+        }
+    } else if (sw) {
+        product("few_up_swiglu", std::true_type{}, std::true_type{}, p.up_vw, p.up_nw, gu, u);
+    } else {
+        product("few_up_gelu", std::true_type{}, std::false_type{}, p.up_vw, p.up_nw, gu, u);
+    }
     FewArgs v{ws + p.h, W2, nullptr, idx, ws + p.partial, pairs, k, E, f, d};
-    MOE_LAUNCH("few_down", s,
-               (few_product_kernel<T, VW, NT, 4, false, false><<<gd, 256, 0, s>>>(v)));
+    product("few_down", std::false_type{}, std::false_type{}, p.down_vw, p.down_nw, gd, v);
     MOE_LAUNCH("few_combine", s,
-               (few_combine_kernel<T><<<cdiv((long)Tn * d / 4, 256), 256, 0, s>>>(
+               (few_combine_kernel<T><<<dim3(cdiv(d, kCombineCols), Tn), 256, 0, s>>>(
                    reinterpret_cast<const float*>(ws + p.partial), w, Tn, k, d, p.ks,
                    static_cast<T*>(y))));
     return launch_status();

@@ -10,7 +10,7 @@ import math
 import torch
 
 from ._lib import MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F32, check, load
-from .ops import GradClip, MoEError, _few_check, _need_gpu, _stream
+from .ops import GradClip, MoEError, _few_check, _stream
 
 
 def _torch_stream(handle, device):
@@ -727,7 +727,7 @@ class FewTokenMoELayer:
         dev = self.device
         nb = L.moe_layer_few_workspace_bytes(T, d, f, E, k, self.act, self.dt)
         if T < 1 or nb == 0:
-            raise MoEError("FewTokenMoELayer: 1 to 64 tokens, T*k <= 4096, d and f multiples "
+            raise MoEError("FewTokenMoELayer: 1 to 64 tokens, k <= 64, d and f multiples "
                            "of 64, 1 <= k <= E <= 1024")
         # a smaller step may cut the reduction finer and need more workspace
         nb = max(L.moe_layer_few_workspace_bytes(t, d, f, E, k, self.act, self.dt)
@@ -738,6 +738,7 @@ class FewTokenMoELayer:
         self._idx = e(T, k, dt=torch.int32)
         self._w = e(T, k, dt=torch.float32)
         self.ws = e(nb, dt=torch.uint8)
+        self._index = self._y.device.index
         self._views(T)
 
     def _views(self, n):
@@ -752,24 +753,27 @@ class FewTokenMoELayer:
         if _few_check(x, Wg, W1, W2, W3, logit_bias, self.act)[1:] != (self.d, self.f, self.E):
             raise MoEError("FewTokenMoELayer: weights of another layer's sizes")
         self.Wg, self.W1, self.W2, self.W3, self.bias = Wg, W1, W2, W3, logit_bias
+        p = lambda t: None if t is None else t.data_ptr()
+        # the arguments of moe_layer_fwd_few between x and T, and after T
+        self._weights = (p(Wg), p(logit_bias), p(W1), p(W3), p(W2))
+        self._rest = (self.d, self.f, self.E, self.k, self.renorm, self.act, self.dt,
+                      p(self._logits), p(self._idx), p(self._w), p(self._y), p(self.ws),
+                      self.ws.numel())
         return self
 
     def forward(self, x, stream=None):
-        n = x.shape[0] if x.dim() == 2 else -1
-        if not 0 <= n <= self.T or x.shape[1] != self.d or x.dtype != self.dtype:
-            raise MoEError("FewTokenMoELayer: x [n,%d], n <= %d, of the layer's dtype"
-                           % (self.d, self.T))
-        _need_gpu(x)
-        if x.device != self._y.device:
-            raise MoEError("FewTokenMoELayer: x on another device than the layer")
+        """x [n,d], n <= T -> y [n,d]."""
+        if x.device != self._y.device or x.dtype != self.dtype or not x.is_contiguous():
+            raise MoEError("FewTokenMoELayer: x contiguous, of the layer's dtype and device")
+        n = x.shape[0]
+        if x.dim() != 2 or x.shape[1] != self.d or n > self.T:
+            raise MoEError("FewTokenMoELayer: x [n,%d], n <= %d" % (self.d, self.T))
         if n != self._n:
             self._views(n)
-        p = lambda t: None if t is None else t.data_ptr()
-        with torch.cuda.device(x.device):
-            s = _stream(x.device) if stream is None else stream
-            check(self.lib.moe_layer_fwd_few(
-                p(x), p(self.Wg), p(self.bias), p(self.W1), p(self.W3), p(self.W2), n, self.d,
-                self.f, self.E, self.k, self.renorm, self.act, self.dt, p(self._logits),
-                p(self._idx), p(self._w), p(self._y), p(self.ws), self.ws.numel(), s),
-                "moe_layer_fwd_few")
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self.forward(x, stream)
+        s = _stream(self._index) if stream is None else stream
+        check(self.lib.moe_layer_fwd_few(x.data_ptr(), *self._weights, n, *self._rest, s),
+              "moe_layer_fwd_few")
         return self.y

@@ -375,6 +375,7 @@ class GradClip:
         L = self.lib = load()
         self.ws = _ws(L.moe_grad_norm_workspace_bytes(self._numel, self._dts, n), dev)
         self.result = torch.zeros(1, dtype=torch.float32, device=dev)
+        self._res, self._ws, self._ws_bytes = _p(self.result), _p(self.ws), self.ws.numel()
 
     def _no_overlap(self):
         """Refuse lists whose result would depend on which block comes first:
@@ -395,27 +396,27 @@ class GradClip:
             end = max(end, b)
             written = max(written, b) if w else written
 
+    def _call(self, fn, name, args, stream):
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._call(fn, name, args, stream)
+        s = _stream(self.device) if stream is None else stream
+        check(fn(*args, self._res, self._ws, self._ws_bytes, s), name)
+        return self.result
+
     def norm(self, stream=None):
         """-> the norm, [1] float32; changes no gradient."""
-        with torch.cuda.device(self.device):
-            s = _stream(self.device) if stream is None else stream
-            check(self.lib.moe_grad_norm(self._in, self._numel, self._dts, self.n,
-                                         _p(self.result), _p(self.ws), self.ws.numel(), s),
-                  "moe_grad_norm")
-        return self.result
+        return self._call(self.lib.moe_grad_norm, "moe_grad_norm",
+                          (self._in, self._numel, self._dts, self.n), stream)
 
     def clip(self, max_norm, stream=None):
         """out = grads * min(1, max_norm / norm) -> the norm, [1] float32."""
         if not self._disjoint:
             self._no_overlap()
             self._disjoint = True
-        mx = ctypes.c_float(max_norm)
-        with torch.cuda.device(self.device):
-            s = _stream(self.device) if stream is None else stream
-            check(self.lib.moe_clip_grads(self._in, self._out, self._numel, self._dts, self.n,
-                                          ctypes.byref(mx), _p(self.result), _p(self.ws),
-                                          self.ws.numel(), s), "moe_clip_grads")
-        return self.result
+        return self._call(self.lib.moe_clip_grads, "moe_clip_grads",
+                          (self._in, self._out, self._numel, self._dts, self.n,
+                           ctypes.byref(ctypes.c_float(max_norm))), stream)
 
 
 def moe_grad_norm(grads):
