@@ -336,22 +336,28 @@ void few_gate(const T* x, const T* Wg, const float* bias, int Tn, int d, int E, 
 }
 
 // ------------------------------------------------------- experts' row lists
+struct RowsLds {
+    uint32_t bits[32];
+    int rows[kFewTokens], res[3];
+};
+
 // The rows of the `slot`-th expert (by index) that any token chose, as pair
-// numbers t * k + j in increasing order: at most one per token.  Returns the
+// numbers t * k + j in increasing order (at most one per token) in r.rows, their
+// number in *n and the pairs of the experts before it in *base.  Returns the
 // expert, or -1 when fewer experts were hit.  Every thread of the block takes
-// part; bits: 32 words, rows: kFewTokens ints, res: 2 ints of LDS.
+// part.
 __device__ __forceinline__ int expert_rows(const int32_t* __restrict__ idx, int pairs, int E,
-                                           int slot, uint32_t* bits, int* rows, int* res, int* n) {
+                                           int slot, RowsLds& r, int* n, int* base) {
     const int tid = threadIdx.x, nthr = blockDim.x;
-    if (tid < 32) bits[tid] = 0;
+    if (tid < 32) r.bits[tid] = 0;
     __syncthreads();
     for (int p = tid; p < pairs; p += nthr) {
         const int e = idx[p];
-        if ((unsigned)e < (unsigned)E) atomicOr(&bits[e >> 5], 1u << (e & 31));
+        if ((unsigned)e < (unsigned)E) atomicOr(&r.bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
     if (tid < 64) {
-        uint32_t b = tid < 32 ? bits[tid] : 0u;
+        uint32_t b = tid < 32 ? r.bits[tid] : 0u;
         const int pc = __popc(b);
         const int inc = wave_incl_scan(pc);
         const int exc = inc - pc;
@@ -363,24 +369,27 @@ __device__ __forceinline__ int expert_rows(const int32_t* __restrict__ idx, int 
         }
         const uint64_t who = __ballot(mine);
         e = who ? __shfl(e, __ffsll((unsigned long long)who) - 1) : -1;
-        int cnt = 0;
+        int cnt = 0, before = 0;
         if (e >= 0)
             for (int p0 = 0; p0 < pairs; p0 += 64) {
                 const int p = p0 + tid;
-                const bool hit = p < pairs && idx[p] == e;
-                const uint64_t m = __ballot(hit);
+                const int ep = p < pairs ? idx[p] : E;
+                const uint64_t m = __ballot(ep == e);
                 const int pos = cnt + __popcll(m & ((1ull << tid) - 1));
-                if (hit && pos < kFewTokens) rows[pos] = p;
+                if (ep == e && pos < kFewTokens) r.rows[pos] = p;
                 cnt += __popcll(m);
+                before += __popcll(__ballot(ep < e));
             }
         if (tid == 0) {
-            res[0] = e;
-            res[1] = min(cnt, kFewTokens);
+            r.res[0] = e;
+            r.res[1] = min(cnt, kFewTokens);
+            r.res[2] = before;
         }
     }
     __syncthreads();
-    *n = res[1];
-    return res[0];
+    *n = r.res[1];
+    *base = r.res[2];
+    return r.res[0];
 }
 
 // -------------------------------------------------------------- activation
@@ -424,10 +433,9 @@ template <> struct Core<bf16_t> {
         }
     }
     template <bool LO>
-    static __device__ __forceinline__ void loadx(const bf16_t* xrow, long lo, int k0, int g,
-                                                 XRaw<LO>& r) {
-        r.v[0] = ld16<false>(xrow + k0 + g * 8);
-        if constexpr (LO) r.v[1] = ld16<false>(xrow + lo + k0 + g * 8);
+    static __device__ __forceinline__ void loadx(const bf16_t* x, long lo, int g, XRaw<LO>& r) {
+        r.v[0] = ld16<false>(x + g * 8);
+        if constexpr (LO) r.v[1] = ld16<false>(x + lo + g * 8);
     }
     template <int VW, int NT, bool LO>
     static __device__ __forceinline__ void mul(const Raw<VW>& r, const XRaw<LO> (&x)[NT],
@@ -470,9 +478,8 @@ template <> struct Core<float> {
             r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i * ldw));
     }
     template <bool LO>
-    static __device__ __forceinline__ void loadx(const float* xrow, long, int k0, int g,
-                                                 XRaw<LO>& r) {
-        r.v = *reinterpret_cast<const f32x4*>(xrow + k0 + g * 4);
+    static __device__ __forceinline__ void loadx(const float* x, long, int g, XRaw<LO>& r) {
+        r.v = *reinterpret_cast<const f32x4*>(x + g * 4);
     }
     template <int VW, int NT, bool LO>
     static __device__ __forceinline__ void mul(const Raw<VW>& r, const XRaw<LO> (&x)[NT],
@@ -488,10 +495,11 @@ template <> struct Core<float> {
     }
 };
 
-// NB - 1 steps are in flight while one is multiplied.
+// xrow: each tile's token of this lane, its next step xstep elements on; lo:
+// from a value to its rest.  NB - 1 steps are in flight while one is multiplied.
 template <typename T, int VW, int NT, int NB, bool LO>
 __device__ __forceinline__ void strip_product(const T* W, long ldw, const T* const (&xrow)[NT],
-                                              long lo, int s0, int s1, f32x4 (&acc)[NT][VW]) {
+                                              long xstep, long lo, int s0, int s1, f32x4 (&acc)[NT][VW]) {
     typedef Core<T> C;
     const int g = (threadIdx.x & 63) >> 4;
     typename C::template Raw<VW> wr[NB];
@@ -499,7 +507,7 @@ __device__ __forceinline__ void strip_product(const T* W, long ldw, const T* con
     auto fetch = [&](int s, int b) {
         C::template load<VW>(W, ldw, s * C::KSTEP, g, wr[b]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) C::template loadx<LO>(xrow[i], lo, s * C::KSTEP, g, xr[b][i]);
+        for (int i = 0; i < NT; ++i) C::template loadx<LO>(xrow[i] + s * xstep, lo, g, xr[b][i]);
     };
 #pragma unroll
     for (int u = 0; u < NB - 1; ++u)
@@ -553,22 +561,17 @@ __device__ __forceinline__ void store4(bf16_t* p, const float* v) {
 }
 
 struct FewArgs {
-    const void* x;              // up: tokens [T, K]; down: h [pairs, K] (bf16: and h_lo)
+    const void* x;              // up: tokens [T, K]; down: h (bf16: and h_lo)
     const void *W, *W3;         // [E, K, N]
     const int32_t* idx;         // [pairs]
-    void* out;                  // up: h [pairs, N] (bf16: and h_lo); down: partial
-                                // [KS][pairs][N] fp32
+    void* out;                  // up: h [N / KSTEP][pairs][KSTEP] (bf16: and h_lo);
+                                // down: partial [KS][pairs][N] fp32
     int pairs, k, E, K, N;
 };
-struct RowsLds {
-    uint32_t bits[32];
-    int rows[kFewTokens], res[2];
-};
-
 // The block's expert (the blockIdx.y-th that any pair chose) and its rows, or
 // -1.  With one token the pairs' experts differ: the slot's own, and no search.
 __device__ __forceinline__ int block_expert(const FewArgs& p, const int32_t* idx, RowsLds& r,
-                                            int* n) {
+                                            int* n, int* base) {
     const int slot = blockIdx.y;
     if (p.pairs == p.k) {
         const int e = idx[slot];
@@ -576,68 +579,82 @@ __device__ __forceinline__ int block_expert(const FewArgs& p, const int32_t* idx
         if ((threadIdx.x & 63) == 0) r.rows[0] = slot;
         __builtin_amdgcn_wave_barrier();
         *n = 1;
+        *base = slot;
         return (unsigned)e < (unsigned)p.E ? e : -1;
     }
-    return expert_rows(idx, p.pairs, p.E, slot, r.bits, r.rows, r.res, n);
+    return expert_rows(idx, p.pairs, p.E, slot, r, n, base);
 }
 
-// UP: h[p] = act(x[p / k] W[e]) (DUAL: * x W3[e]) for the expert's pairs p.
+// UP: h of pair p = act(x[p / k] W[e]) (DUAL: * x W3[e]) for the expert's pairs.
 // Down (UP = false): partial[ks][p] = h[p] W[e] over the ks-th chunk of K.
 // Grid: strips of 16 * VW columns, experts hit, chunks.  The NW waves of a
 // block take consecutive parts of the chunk (DUAL: one half of them W, the other
 // W3, which keeps the accumulators of a wave to one product); their sums meet
 // in LDS (red: NW * 16 * (16 VW + 4) floats), in order.
 //
+// h is laid out for its one reader: the rows in the order of their experts, in
+// blocks of KSTEP columns (64 bytes), so that the 16 tokens' 64 bytes of one
+// step are eight whole cache lines; by token they were 16 half ones, and with
+// few registers' worth of loads in flight the number of lines asked for is what
+// bounds these kernels (T 64, d 4096, f 14336, 32 experts: 768 us against 825).
 // h in bf16 is kept as the sum of two (h_lo, the rest that the first rounding
 // left, follows h): the matrix cores wait for memory here anyway, and one
 // rounding of h was the largest part of y's error (0.0024 of |y| against
 // 0.0017 for y's own rounding).
 template <typename T, int VW, int NTM, int NW, bool UP, bool DUAL>
-__device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, const int* rows,
-                                              float* red) {
+__device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, int base,
+                                              const int* rows, float* red) {
     constexpr int KW = DUAL ? NW / 2 : NW;             // waves that share a product's chunk
     constexpr bool LO = !UP && sizeof(T) == 2;
+    constexpr int KSTEP = Core<T>::KSTEP;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15;
     const T* We = static_cast<const T*>(DUAL && wv >= KW ? p.W3 : p.W) + (long)e * p.K * p.N;
-    const int steps = p.K / Core<T>::KSTEP;
-    const int units = gridDim.z * KW, u = blockIdx.z * KW + wv % KW;
-    const int s0 = (int)((long)steps * u / units), s1 = (int)((long)steps * (u + 1) / units);
-    // V columns per lane from column n0, NT tiles of 16 rows, NB steps of
-    // registers; again: red may still be read from the call before
-    auto body = [&](auto vc, auto tiles, auto depth, int n0, bool again) {
-        constexpr int V = decltype(vc)::value, NT = decltype(tiles)::value;
-        constexpr int BN = 16 * V, LD = BN + 4;
+    const int n0 = blockIdx.x * 16 * VW;
+    // NT tiles of 16 rows per wave, depth steps of registers; halves = 2: half
+    // of the waves take rows 32 and on, and each half splits the chunk
+    auto body = [&](auto tiles, auto depth, auto halves) {
+        constexpr int NT = decltype(tiles)::value, H = decltype(halves)::value;
+        constexpr int BN = 16 * VW, LD = BN + 4;
+        constexpr int PARTS = KW / H;
+        static_assert(H == 1 || !DUAL, "rows or weights are split between the waves");
+        const int half = H == 1 ? 0 : wv / PARTS;
+        const int steps = p.K / KSTEP;
+        const int units = gridDim.z * PARTS, u = blockIdx.z * PARTS + wv % PARTS;
+        const int s0 = (int)((long)steps * u / units), s1 = (int)((long)steps * (u + 1) / units);
         const T* xrow[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const int q = rows[min(i * 16 + c, n - 1)];  // rows past n: the last one's again
-            xrow[i] = static_cast<const T*>(p.x) + (long)(UP ? q / p.k : q) * p.K;
+            // rows past n: the last one's again
+            const int q = min(half * 32 + i * 16 + c, n - 1);
+            xrow[i] = static_cast<const T*>(p.x) +
+                      (UP ? (long)(rows[q] / p.k) * p.K : (long)(base + q) * KSTEP);
         }
-        f32x4 acc[NT][V];
+        f32x4 acc[NT][VW];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < VW; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // columns past N (a multiple of 64) read the last ones of the row instead
-        strip_product<T, V, NT, decltype(depth)::value, LO>(
-            We + min(n0 + c * V, p.N - V), p.N, xrow, (long)p.pairs * p.K, s0, s1, acc);
+        strip_product<T, VW, NT, decltype(depth)::value, LO>(
+            We + min(n0 + c * VW, p.N - VW), p.N, xrow, UP ? KSTEP : (long)p.pairs * KSTEP,
+            (long)p.pairs * p.K, s0, s1, acc);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             if (i * 16 >= n) break;
-            if (i > 0 || again) __syncthreads();
-            slab_store<V>(red + wv * 16 * LD, acc[i]);
+            if (i > 0) __syncthreads();
+            slab_store<VW>(red + wv * 16 * LD, acc[i]);
             __syncthreads();
-            for (int q = tid; q < 16 * BN / 4; q += 64 * NW) {
-                const int row = q / (BN / 4), cl = q % (BN / 4) * 4;
-                if (i * 16 + row >= n || n0 + cl >= p.N) continue;
-                const float4 s = slab_sum<V, KW>(red, row, cl);
-                const int pr = rows[i * 16 + row];
+            for (int q = tid; q < H * 16 * BN / 4; q += 64 * NW) {
+                const int hq = q / (16 * BN / 4), row = q / (BN / 4) % 16, cl = q % (BN / 4) * 4;
+                const int r = hq * 32 + i * 16 + row;
+                if (r >= n || n0 + cl >= p.N) continue;
+                const float4 s = slab_sum<VW, PARTS>(red + hq * PARTS * 16 * LD, row, cl);
                 float v[4] = {s.x, s.y, s.z, s.w};
                 if constexpr (UP) {
                     if constexpr (DUAL) {
-                        const float4 h3 = slab_sum<V, KW>(red + KW * 16 * LD, row, cl);
+                        const float4 h3 = slab_sum<VW, KW>(red + KW * 16 * LD, row, cl);
                         v[0] = silu_f(v[0]) * h3.x;
                         v[1] = silu_f(v[1]) * h3.y;
                         v[2] = silu_f(v[2]) * h3.z;
@@ -646,7 +663,9 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, co
 #pragma unroll
                         for (int a = 0; a < 4; ++a) v[a] = gelu_f(v[a]);
                     }
-                    T* h = static_cast<T*>(p.out) + (long)pr * p.N + n0 + cl;
+                    const int hc = n0 + cl;
+                    T* h = static_cast<T*>(p.out) +
+                           ((long)(hc / KSTEP) * p.pairs + base + r) * KSTEP + hc % KSTEP;
                     store4(h, v);
                     if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -658,43 +677,39 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, co
                     }
                 } else {
                     store4(static_cast<float*>(p.out) +
-                               ((long)blockIdx.z * p.pairs + pr) * p.N + n0 + cl, v);
+                               ((long)blockIdx.z * p.pairs + rows[r]) * p.N + n0 + cl, v);
                 }
             }
         }
     };
-    // The expert's rows in tiles of 16, as many as it has: a wave computes 1,
-    // 2 or 4 of them.  Four tiles of h and h_lo at VW = 8 would not fit the
-    // registers: the strip goes in two halves then.
+    // The expert's rows in tiles of 16.  Up: one, two or four of them to a wave.
+    // Down: a wave with two operands per token has registers for two; rows past
+    // 32 are the other half of the waves', which read the strip a second time,
+    // from the caches, at about the same time (in blocks of their own they were
+    // 19% more misses of the L2).
     using std::integral_constant;
-    const int n0 = blockIdx.x * 16 * VW;
-    constexpr integral_constant<int, VW> vw{};
+    constexpr integral_constant<int, 1> one{};
     constexpr integral_constant<int, 2> two{};
     if constexpr (NTM >= 4) {
-        constexpr integral_constant<int, 4> four{};
         if (n > 32) {
-            if constexpr (LO && VW == 8) {
-                body(four, four, two, n0, false);
-                return body(four, four, two, n0 + 64, true);
-            } else {
-                return body(vw, four, two, n0, false);
-            }
+            if constexpr (LO) return body(two, two, two);
+            else return body(integral_constant<int, 4>{}, two, one);
         }
     }
     if constexpr (NTM >= 2) {
-        if (n > 16) return body(vw, two, two, n0, false);
+        if (n > 16) return body(two, two, one);
     }
-    body(vw, integral_constant<int, 1>{}, integral_constant<int, VW == 8 ? 2 : 3>{}, n0, false);
+    body(one, integral_constant<int, VW == 8 ? 3 : 4>{}, one);
 }
 
 template <typename T, int VW, int NTM, int NW, bool UP, bool DUAL>
 __global__ __launch_bounds__(64 * NW, 2) void few_product_kernel(FewArgs p) {
     __shared__ __attribute__((aligned(16))) float red[NW * 16 * (16 * VW + 4)];
     __shared__ RowsLds r;
-    int n;
-    const int e = block_expert(p, p.idx, r, &n);
+    int n, base;
+    const int e = block_expert(p, p.idx, r, &n, &base);
     if (e < 0) return;
-    product_block<T, VW, NTM, NW, UP, DUAL>(p, e, n, r.rows, red);
+    product_block<T, VW, NTM, NW, UP, DUAL>(p, e, n, base, r.rows, red);
 }
 
 // The gate and the up product in one launch, for a gate that one block of
@@ -738,10 +753,10 @@ __global__ __launch_bounds__(512, 2) void few_gate_up_kernel(GateArgs g, FewArgs
         }
     }
     __syncthreads();
-    int n;
-    const int e = block_expert(p, idx, r, &n);
+    int n, base;
+    const int e = block_expert(p, idx, r, &n, &base);
     if (e < 0) return;
-    product_block<T, VW, 1, NW, true, DUAL>(p, e, n, r.rows, s.red);
+    product_block<T, VW, 1, NW, true, DUAL>(p, e, n, base, r.rows, s.red);
 }
 
 // y[t] = sum over a token's k slots and ks chunks of w[t,j] partial[s][t k + j],
@@ -792,7 +807,7 @@ struct FewPlan {
     size_t logits, idx, w, h, partial, total;
 };
 
-constexpr double kFewWaves = 600, kChunkWaves = 3000;
+constexpr double kFewWaves = 600, kChunkWaves = 6000;
 constexpr int kFewChunks = 16;
 
 bool few_sizes_ok(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
@@ -827,8 +842,10 @@ FewPlan few_plan(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     p.up_strips = cdiv(f, 16 * p.up_vw);
     // The down product's reduction f is long and its columns are few: chunks
     // of it until kChunkWaves waves run, each with at least 8 (narrow strips: 2)
-    // steps to go.  (T 48, d 1024, f 4096, 64 experts: 2 chunks 73 us, one 82;
-    // T 16, f 1024: one 78, 2 chunks of 4 steps 81.)
+    // steps to go: short blocks, since the experts with the most rows take
+    // longest and may come last.  (T 48, d 1024, f 4096, 64 experts, this product:
+    // 41 us with 6000, 54 with 3000; T 64, d 4096, f 14336, 32 experts: 767 and
+    // 893; T 16, f 1024, whole pass: 78 unsplit, 81 in chunks of 4 steps.)
     const int steps = f / (dt == MOE_BF16 ? 32 : 16);
     auto chunks = [&](int vw, int nw, int least) {
         int ks = 1;
