@@ -24,8 +24,14 @@ namespace moe {
 namespace {
 
 constexpr int kTensors = 128;                 // tensors of one launch
-constexpr int kChunkBytes = 64 << 10;         // of one tensor, one block's work item
-constexpr int kNormBlocks = 2048;             // blocks of one launch at most
+// One block's work item, of one tensor: the blocks at work together then read
+// neighbouring 16 KB pieces.  (Of 16, 32, 64 and 128 KB, 16 was best for small
+// lists, 6.1 against 7.4 us with 64 KB for 1 MB in all, and large ones differed
+// by 1-2%.)
+constexpr int kChunkBytes = 16 << 10;
+// Blocks of one launch at most.  The norm of 5.6 GB: 910 us with 1024, 934 with
+// 2048; scaling 1.07 GB: 380 us with 4096, 384 with 2048, 387 with 1024.
+constexpr int kNormBlocks = 1024, kScaleBlocks = 4096;
 constexpr uint64_t kBf16Flag = 1ull << 63;
 
 // One launch's tensors: tensor i covers chunks first[i] .. first[i+1]-1.
@@ -43,6 +49,7 @@ struct Chunk {
     uint64_t i0;                              // first element
     int len;                                  // elements
 };
+template <bool BACK>                          // a tensor's chunks from its last to its first
 __device__ __forceinline__ Chunk chunk_of(const GradTable& g, uint32_t c) {
     int lo = 0, hi = g.n;                     // largest t with first[t] <= c
     while (hi - lo > 1) {
@@ -54,7 +61,7 @@ __device__ __forceinline__ Chunk chunk_of(const GradTable& g, uint32_t c) {
     k.bf16 = (g.numel[lo] & kBf16Flag) != 0;
     const uint64_t n = g.numel[lo] & ~kBf16Flag;
     const int per = kChunkBytes / (k.bf16 ? 2 : 4);
-    k.i0 = (uint64_t)(c - g.first[lo]) * per;
+    k.i0 = (uint64_t)(BACK ? g.first[lo + 1] - 1 - c : c - g.first[lo]) * per;
     k.len = (int)min((uint64_t)per, n - k.i0);
     return k;
 }
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(256) void grad_squares_kernel(GradTable g,
     __shared__ double sh[4];
     double s = 0.0;
     for (uint32_t c = blockIdx.x; c < g.first[g.n]; c += gridDim.x) {
-        const Chunk k = chunk_of(g, c);
+        const Chunk k = chunk_of<false>(g, c);
         s += k.bf16 ? chunk_squares(static_cast<const bf16_t*>(g.in[k.t]) + k.i0, k.len)
                     : chunk_squares(static_cast<const float*>(g.in[k.t]) + k.i0, k.len);
     }
@@ -158,7 +165,8 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, float c) 
         for (int u = 0; u < UN; ++u) raw[u] = *reinterpret_cast<const P*>(p + (v + 256 * u) * V);
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-            *reinterpret_cast<P*>(o + (v + 256 * u) * V) = scaled(raw[u]);
+            __builtin_nontemporal_store(scaled(raw[u]),
+                                        reinterpret_cast<P*>(o + (v + 256 * u) * V));
     }
     for (; v < nvec; v += 256)
         *reinterpret_cast<P*>(o + v * V) = scaled(*reinterpret_cast<const P*>(p + v * V));
@@ -170,6 +178,12 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, float c) 
 // that is not finite scales nothing: the step is the caller's to drop, and
 // zeros or NaN in place of the gradients would hide why.  In place a factor
 // of 1 leaves nothing to do.
+//
+// The list is taken from its end to its start: what the norm read last is
+// still in the 256 MB cache.  Stores bypass the caches, so that they neither
+// evict it nor leave lines to be written back under the next kernel's reads
+// (345 MB in 200 tensors, norm and scaling: 224 us with plain stores in list
+// order, 210 backwards, 181 with both).
 __global__ __launch_bounds__(256) void grad_scale_kernel(GradTable g,
                                                          const double* __restrict__ partial,
                                                          int np, float max_norm,
@@ -179,7 +193,7 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(GradTable g,
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     const float c = v > max_norm && v < INFINITY ? max_norm / v : 1.0f;
     for (uint32_t q = blockIdx.x; q < g.first[g.n]; q += gridDim.x) {
-        const Chunk k = chunk_of(g, q);
+        const Chunk k = chunk_of<true>(g, q);
         if (c == 1.0f && g.in[k.t] == g.out[k.t]) continue;
         if (k.bf16)
             chunk_scale(static_cast<const bf16_t*>(g.in[k.t]) + k.i0,
@@ -212,21 +226,22 @@ uint64_t chunks_of(size_t numel, int dt) {
     return (numel + per - 1) / per;
 }
 
-// Calls f(table, blocks) for each launch of the list, in order; stops early
-// when f returns false.  out may be NULL.
+// Calls f(table, blocks) for each launch of the list, first tensors first or
+// (back) last ones first; stops early when f returns false.  out may be NULL.
 template <class F>
 void for_launches(const void* const* grads, void* const* out, const size_t* numel,
-                  const int32_t* dt, int n, F&& f) {
+                  const int32_t* dt, int n, int max_blocks, bool back, F&& f) {
     GradTable g;
     g.n = 0;
     g.first[0] = 0;
     auto flush = [&]() {
         if (g.n == 0) return true;
-        const bool ok = f(g, (int)min((uint32_t)kNormBlocks, g.first[g.n]));
+        const bool ok = f(g, (int)min((uint32_t)max_blocks, g.first[g.n]));
         g.n = 0;
         return ok;
     };
-    for (int i = 0; i < n; ++i) {
+    for (int q = 0; q < n; ++q) {
+        const int i = back ? n - 1 - q : q;
         if (numel[i] == 0) continue;
         const uint64_t c = chunks_of(numel[i], dt[i]);
         // a launch's chunk numbers, and a block's next one, stay below 2^32
@@ -243,7 +258,8 @@ void for_launches(const void* const* grads, void* const* out, const size_t* nume
 
 int partials_of(const size_t* numel, const int32_t* dt, int n) {
     int np = 0;
-    for_launches(nullptr, nullptr, numel, dt, n, [&](const GradTable&, int blocks) {
+    for_launches(nullptr, nullptr, numel, dt, n, kNormBlocks, false,
+                 [&](const GradTable&, int blocks) {
         np += blocks;
         return true;
     });
@@ -254,7 +270,8 @@ moe_status run_squares(const void* const* grads, const size_t* numel, const int3
                        double* partial, hipStream_t s) {
     int at = 0;
     moe_status st = MOE_OK;
-    for_launches(grads, nullptr, numel, dt, n, [&](const GradTable& g, int blocks) {
+    for_launches(grads, nullptr, numel, dt, n, kNormBlocks, false,
+                 [&](const GradTable& g, int blocks) {
         MOE_LAUNCH("grad_squares", s, (grad_squares_kernel<<<blocks, 256, 0, s>>>(g, partial + at)));
         at += blocks;
         st = launch_status();
@@ -311,7 +328,8 @@ moe_status moe_clip_grads(const void* const* grads, void* const* out, const size
         return launch_status();
     }
     bool first = true;
-    for_launches(grads, out, numel, dt, n, [&](const GradTable& g, int blocks) {
+    for_launches(grads, out, numel, dt, n, kScaleBlocks, true,
+                 [&](const GradTable& g, int blocks) {
         MOE_LAUNCH("grad_scale", stream,
                    (grad_scale_kernel<<<blocks, 256, 0, stream>>>(g, partial, np, mx,
                                                                   first ? norm : nullptr)));

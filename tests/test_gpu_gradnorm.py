@@ -60,7 +60,8 @@ LISTS = {
     "one bf16": [(BF, (1,))],
     "odd": [(BF, (7,)), (F32, (13, 3)), (BF, (1, 1)), (F32, (0,)), (BF, (2049, 17)), (BF, (0, 4))],
     "chunk edges": [(BF, (32768,)), (BF, (32769,)), (BF, (32767,)), (F32, (16384,)),
-                    (F32, (16385,)), (F32, (16383,))],
+                    (F32, (16385,)), (F32, (16383,)), (BF, (8192,)), (BF, (8193,)),
+                    (F32, (4096,)), (F32, (4097,))],
     "128 tensors": [(F32, (i + 1,)) for i in range(128)],
     "129 tensors": [(BF, (i + 1,)) for i in range(129)],
     "400 tensors": [((BF, F32)[i % 2], (131 * (i % 7), 3)) for i in range(400)],

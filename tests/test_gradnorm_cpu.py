@@ -68,7 +68,7 @@ def test_workspace(lib, base):
     q = lambda numel, dts: lib.moe_grad_norm_workspace_bytes(
         (ctypes.c_size_t * len(numel))(*numel), (ctypes.c_int32 * len(dts))(*dts), len(numel))
     assert q([], []) > 0 and q([0], [0]) > 0 and q([1], [1]) > 0
-    assert q([10 ** 9] * 3, [1, 0, 1]) >= 2048 * 8                   # a partial sum per block
+    assert q([10 ** 9] * 3, [1, 0, 1]) >= 1024 * 8                   # a partial sum per block
     assert q([1] * 400, [0] * 400) >= 400 * 8                        # one chunk per tensor
     assert q([1], [2]) == 0 and q([(1 << 40) + 1], [0]) == 0
     assert lib.moe_grad_norm_workspace_bytes(None, None, 2) == 0
