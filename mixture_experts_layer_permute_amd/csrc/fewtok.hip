@@ -9,7 +9,7 @@
 // Kernels of a call:
 //   few_gate     the gate's logits, one fixed-order fp32 chain per (token,
 //                expert): the same bits as moe_gate_topk; then top-k and gate
-//                weights, one wave per token (few_topk, with over 64 experts)
+//                weights, one wave per token (few_topk, with many experts)
 //   few_up       per (expert hit, strip of columns): act(x W1[e]) (* x W3[e])
 //   few_down     per (expert hit, strip of columns, chunk of f): h W2[e], fp32
 //   few_combine  y[t] = sum_j w[t,j] sum_chunks partial, in slot and chunk order
@@ -134,8 +134,8 @@ __device__ __forceinline__ void wave_topk(const float* lt, int E, int k, int ren
 // barriers.  One token, 16 experts: 3.1 ns per feature (12 us at d 4096)
 // after 3 us to start; additions alone would take 1.9 ns, the rest is the
 // LDS reads, which hold the wave for about 10 clocks each.
-// VE: gate elements per load (16 bytes where a row's length and alignment
-// allow).
+// PACKED: gate rows of any length and alignment, loaded 16 bytes at a time all
+// the same; what a row's last load finds behind it belongs to no expert.
 constexpr int GK = 128, GROW = GK + 4;
 struct GateLds {
     alignas(16) float ps[3][64 * GROW];
@@ -144,20 +144,23 @@ struct GateLds {
 
 // Chunks in flight: eight take 0.3 us each, more than the latency of HBM,
 // where the registers of half a row's loads allow it.
-template <typename T, int EB, int VE>
+template <typename T, int EB>
 constexpr int gate_ahead() {
-    return VE > 1 && EB * sizeof(T) <= 128 ? 8 : 4;
+    return EB * sizeof(T) <= 128 ? 8 : 4;
 }
+
+typedef unsigned int u32x4_2_t __attribute__((ext_vector_type(4), aligned(2)));
 
 // The logits of tokens t0 .. t0 + TB - 1 and experts e0 .. e0 + EB - 1 into
 // s.lg [TB][EB], and into logits [T, E] when not NULL.
-template <typename T, int EB, int NPF, int VE>
+template <typename T, int EB, bool PACKED>
 __device__ __forceinline__ void gate_block(GateLds& s, const T* __restrict__ x,
                                            const T* __restrict__ Wg,
                                            const float* __restrict__ bias, int Tn, int d, int E,
                                            int e0, int t0, float* __restrict__ logits) {
 #pragma clang fp contract(off)
-    constexpr int TB = 64 / EB;
+    constexpr int TB = 64 / EB, NPF = gate_ahead<T, EB>();
+    constexpr int VE = 16 / sizeof(T);
     constexpr int WL = EB / 2 / VE;                   // loads of half a gate row
     constexpr int G = 32;                             // features read ahead
     const int tid = threadIdx.x;
@@ -171,33 +174,48 @@ __device__ __forceinline__ void gate_block(GateLds& s, const T* __restrict__ x,
     } else if (wv > 0) {
         const int st = (tid - (wv == 5 ? 128 : 64)) % GK;             // feature of a chunk
         const int el = (tid - (wv == 5 ? 128 : 64)) / GK * (EB / 2);  // first expert
-        typedef std::conditional_t<VE == 1, T, u32x4_t> wload_t;
-        wload_t wr[NPF][WL];
+        u32x4_t wr[NPF][WL];
         T xr[NPF][TB];
-        // loads past the matrix read a valid element instead: features past d
-        // are never summed, experts and tokens past the end never stored
-        auto fetch = [&](int c, wload_t (&w)[WL], T (&xv)[TB]) {
-            const int kk = min(c * GK + st, d - 1);
-            const T* row = Wg + (long)kk * E;
-#pragma unroll
-            for (int q = 0; q < WL; ++q)
-                w[q] = *reinterpret_cast<const wload_t*>(row + min(e0 + el + q * VE, E - VE));
-#pragma unroll
-            for (int t = 0; t < TB; ++t) xv[t] = x[(long)min(t0 + t, Tn - 1) * d + kk];
+        // Loads past the matrix read a valid element instead: features past d
+        // are never summed, experts and tokens past the end never stored.
+        // place: a load's element offset.  A packed one that would end behind
+        // the last row starts earlier, and its value is shifted down by as much.
+        const long last = (long)d * E - VE;
+        auto place = [&](int c, int q, int& shift) {
+            const long row = (long)min(c * GK + st, d - 1) * E;
+            const int e = e0 + el + q * VE;
+            if constexpr (!PACKED) return row + min(e, E - VE);
+            const long off = row + (e < E ? e : 0);
+            shift = (int)max(off - last, 0l);
+            return off - shift;
         };
-        auto stash = [&](int b, const wload_t (&w)[WL], const T (&xv)[TB]) {
+        auto fetch = [&](int c, u32x4_t (&w)[WL], T (&xv)[TB]) {
+            int shift;
+#pragma unroll
+            for (int q = 0; q < WL; ++q) {
+                const T* p = Wg + place(c, q, shift);
+                if constexpr (PACKED) w[q] = *reinterpret_cast<const u32x4_2_t*>(p);
+                else w[q] = *reinterpret_cast<const u32x4_t*>(p);
+            }
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+                xv[t] = x[(long)min(t0 + t, Tn - 1) * d + min(c * GK + st, d - 1)];
+        };
+        auto stash = [&](int c, int b, const u32x4_t (&w)[WL], const T (&xv)[TB]) {
             float xf[TB];
 #pragma unroll
             for (int t = 0; t < TB; ++t) xf[t] = Elem<T>::ld(&xv[t]);
 #pragma unroll
             for (int q = 0; q < WL; ++q) {
-                float o[VE];
-                if constexpr (VE == 1) {
-                    const T v = w[q];
-                    o[0] = Elem<T>::ld(&v);
-                } else {
-                    unpack16<T>(w[q], o);
+                u32x4_t raw = w[q];
+                if (PACKED && c == nc - 1) {
+                    int shift;
+                    place(c, q, shift);
+                    const unsigned __int128 v = __builtin_bit_cast(unsigned __int128, raw);
+                    raw = __builtin_bit_cast(u32x4_t, v >> (shift * 8 * (int)sizeof(T)));
                 }
+                float o[VE];
+                unpack16<T>(raw, o);
 #pragma unroll
                 for (int t = 0; t < TB; ++t) {
                     if (t > 0 && t0 + t >= Tn) break;
@@ -216,7 +234,7 @@ __device__ __forceinline__ void gate_block(GateLds& s, const T* __restrict__ x,
             for (int u = 0; u < NPF; ++u) {
                 const int c = cb + u;
                 if (c >= nc) break;
-                stash(b, wr[u], xr[u]);
+                stash(c, b, wr[u], xr[u]);
                 b = b == 2 ? 0 : b + 1;
                 fetch(c + NPF, wr[u], xr[u]);
                 __syncthreads();
@@ -270,7 +288,7 @@ __device__ __forceinline__ void gate_block(GateLds& s, const T* __restrict__ x,
     __syncthreads();
 }
 
-template <typename T, int EB, int NPF, int VE>
+template <typename T, int EB, bool PACKED>
 __global__ __launch_bounds__(384) void few_gate_kernel(
     const T* __restrict__ x, const T* __restrict__ Wg, const float* __restrict__ bias, int Tn,
     int d, int E, int k, int renorm, float* __restrict__ logits, int32_t* __restrict__ topk_idx,
@@ -278,7 +296,7 @@ __global__ __launch_bounds__(384) void few_gate_kernel(
     constexpr int TB = 64 / EB;
     __shared__ GateLds s;
     const int t0 = blockIdx.y * TB;
-    gate_block<T, EB, NPF, VE>(s, x, Wg, bias, Tn, d, E, blockIdx.x * EB, t0, logits);
+    gate_block<T, EB, PACKED>(s, x, Wg, bias, Tn, d, E, blockIdx.x * EB, t0, logits);
     if (E > EB) return;                                           // few_topk follows
     const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
     if (wv < TB && t0 + wv < Tn) {
@@ -308,19 +326,23 @@ __global__ __launch_bounds__(256) void few_topk_kernel(const float* __restrict__
     }
 }
 
+template <typename T>
+bool gate_rows_aligned(const void* Wg, int E) {
+    return E % (int)(16 / sizeof(T)) == 0 && aligned16(Wg);
+}
+
 template <typename T, int EB>
 void few_gate_go(const T* x, const T* Wg, const float* bias, int Tn, int d, int E, int k,
                  int renorm, float* logits, int32_t* idx, float* w, hipStream_t s) {
-    constexpr int VE = 16 / sizeof(T);
     const dim3 grid(cdiv(E, EB), cdiv(Tn, 64 / EB));
-    if (E % VE == 0 && aligned16(Wg))
+    if (EB > 32 || gate_rows_aligned<T>(Wg, E))
         MOE_LAUNCH("few_gate", s,
-                   (few_gate_kernel<T, EB, gate_ahead<T, EB, VE>(), VE><<<grid, 384, 0, s>>>(
-                       x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w)));
-    else
+                   (few_gate_kernel<T, EB, false><<<grid, 384, 0, s>>>(x, Wg, bias, Tn, d, E, k,
+                                                                       renorm, logits, idx, w)));
+    else if constexpr (EB <= 32)
         MOE_LAUNCH("few_gate", s,
-                   (few_gate_kernel<T, EB, gate_ahead<T, EB, 1>(), 1><<<grid, 384, 0, s>>>(
-                       x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w)));
+                   (few_gate_kernel<T, EB, true><<<grid, 384, 0, s>>>(x, Wg, bias, Tn, d, E, k,
+                                                                      renorm, logits, idx, w)));
     if (E > EB)
         MOE_LAUNCH("few_topk", s,
                    (few_topk_kernel<<<cdiv(Tn, 4), 256, 0, s>>>(logits, Tn, E, k, renorm, idx,
@@ -330,9 +352,18 @@ void few_gate_go(const T* x, const T* Wg, const float* bias, int Tn, int d, int 
 template <typename T>
 void few_gate(const T* x, const T* Wg, const float* bias, int Tn, int d, int E, int k, int renorm,
               float* logits, int32_t* idx, float* w, hipStream_t s) {
-    if (E <= 16) few_gate_go<T, 16>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
-    else if (E <= 32) few_gate_go<T, 32>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
-    else few_gate_go<T, 64>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
+    // Up to 64 experts go in one block, which then also has the choice to make
+    // (32 in fp32, whose rows are as long, or packed).  More go in blocks of 16,
+    // whose loads are the least in the way of their chains, with the choice in a
+    // launch of its own, about 3 us (one token, d 4096, 128 experts: bf16 18.5 us
+    // against 24.3 in blocks of 64, fp32 19.8 against 34.8; 49 experts, packed:
+    // 24.3 against 35.0).
+    if constexpr (sizeof(T) == 2)
+        if (E > 32 && E <= 64 && gate_rows_aligned<T>(Wg, E))
+            return few_gate_go<T, 64>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
+    if (E > 16 && E <= 32)
+        return few_gate_go<T, 32>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
+    few_gate_go<T, 16>(x, Wg, bias, Tn, d, E, k, renorm, logits, idx, w, s);
 }
 
 // ------------------------------------------------------- experts' row lists
@@ -423,6 +454,9 @@ template <> struct Core<bf16_t> {
                     reinterpret_cast<const u32x4_t*>(p + i * ldw));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) r.w[i][q] = v[q];
+            } else if constexpr (VW == 2) {
+                r.w[i][0] = __builtin_nontemporal_load(
+                    reinterpret_cast<const uint32_t*>(p + i * ldw));
             } else {
                 typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
                 const u32x2_t v = __builtin_nontemporal_load(
@@ -465,17 +499,20 @@ template <> struct Core<bf16_t> {
 template <> struct Core<float> {
     static constexpr int KSTEP = 16;
     static constexpr int NL = 4;
-    template <int VW> struct Raw { f32x4 w[NL]; };
+    template <int VW> struct Raw { float w[NL][VW]; };
     template <bool LO> struct XRaw { f32x4 v; };
 
     template <int VW>
     static __device__ __forceinline__ void load(const float* W, long ldw, int k0, int g,
                                                 Raw<VW>& r) {
-        static_assert(VW == 4, "16 bytes per lane and row");
+        typedef float vec_t __attribute__((ext_vector_type(VW)));
         const float* p = W + (long)(k0 + g * 4) * ldw;
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-            r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + i * ldw));
+        for (int i = 0; i < NL; ++i) {
+            const vec_t v = __builtin_nontemporal_load(reinterpret_cast<const vec_t*>(p + i * ldw));
+#pragma unroll
+            for (int j = 0; j < VW; ++j) r.w[i][j] = v[j];
+        }
     }
     template <bool LO>
     static __device__ __forceinline__ void loadx(const float* x, long, int g, XRaw<LO>& r) {
@@ -535,11 +572,10 @@ __device__ __forceinline__ void slab_store(float* slab, const f32x4 (&acc)[VW]) 
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     float* p = slab + c * LD + g * 4 * VW;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int j = 0; j < VW; j += 4)
-            *reinterpret_cast<float4*>(p + r * VW + j) =
-                make_float4(acc[j][r], acc[j + 1][r], acc[j + 2][r], acc[j + 3][r]);
+    for (int q = 0; q < 4 * VW; q += 4)               // column q of the lane: row q / VW, j q % VW
+        *reinterpret_cast<float4*>(p + q) =
+            make_float4(acc[q % VW][q / VW], acc[(q + 1) % VW][(q + 1) / VW],
+                        acc[(q + 2) % VW][(q + 2) / VW], acc[(q + 3) % VW][(q + 3) / VW]);
 }
 template <int VW, int NW>
 __device__ __forceinline__ float4 slab_sum(const float* slabs, int row, int col) {
@@ -699,7 +735,9 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, in
     if constexpr (NTM >= 2) {
         if (n > 16) return body(two, two, one);
     }
-    body(one, integral_constant<int, VW == 8 ? 3 : 4>{}, one);
+    // (one tile, fp32: three steps deep 151 us against 158 with four, one token
+    // of d 4096, f 14336, 2 of 8 experts; bf16, half-width strips: four)
+    body(one, integral_constant<int, (VW == 8 || sizeof(T) == 4 ? 3 : 4)>{}, one);
 }
 
 template <typename T, int VW, int NTM, int NW, bool UP, bool DUAL>
@@ -725,7 +763,7 @@ struct GateArgs {
     int32_t* idx;
     float* w;
 };
-template <typename T, int VE, bool DUAL>
+template <typename T, bool PACKED, bool DUAL>
 __global__ __launch_bounds__(512, 2) void few_gate_up_kernel(GateArgs g, FewArgs p) {
     constexpr int EB = 16, TB = 4, VW = 4, NW = 8;
     // the product's slabs take the gate's place once the choice is made
@@ -736,7 +774,7 @@ __global__ __launch_bounds__(512, 2) void few_gate_up_kernel(GateArgs g, FewArgs
     __shared__ RowsLds r;
     __shared__ int32_t idx[TB * EB];                              // k <= E <= 16
     const bool first = blockIdx.x == 0 && blockIdx.y == 0;
-    gate_block<T, EB, gate_ahead<T, EB, VE>(), VE>(
+    gate_block<T, EB, PACKED>(
         s.gate, static_cast<const T*>(g.x), static_cast<const T*>(g.Wg), g.bias, g.T, g.d, p.E, 0,
         0, first ? g.logits : nullptr);
     const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -807,7 +845,7 @@ struct FewPlan {
     size_t logits, idx, w, h, partial, total;
 };
 
-constexpr double kFewWaves = 600, kChunkWaves = 6000;
+constexpr double kFewWaves = 600, kChunkWaves = 6000;    // bf16, see few_plan
 constexpr int kFewChunks = 16;
 
 bool few_sizes_ok(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
@@ -832,13 +870,21 @@ FewPlan few_plan(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     // not enough in flight to cover the latency of HBM, and strips of half the
     // width with 8 waves are faster (d 4096, f 1536, 8 of 128 experts: 100
     // against 117 us; d 1024, f 4096, 2 of 8: 22.1 against 22.9).
+    // fp32 has 64-column strips either way and half the bytes per wave and step:
+    // 4 waves a block, or 8 below twice that number (same shape: 76 against 102).
+    const double few = dt == MOE_BF16 ? kFewWaves : 2 * kFewWaves;
     p.up_vw = wide;
     p.up_nw = 4;
     // The gate's fusion: what one gate_block covers, in one round of blocks
     // (two rounds would work the gate out twice).  One token, d 1024, 8
     // experts: 21.4 us against 23.4 with a launch of its own.
     p.fuse_gate = E <= 16 && T <= 4 && cdiv(f, 64) * p.slots <= 256;
-    if (p.fuse_gate || waves(f, wide, 4) < kFewWaves) p.up_vw = 4, p.up_nw = 8;
+    if (p.fuse_gate || waves(f, wide, 4) < few) p.up_vw = 4, p.up_nw = 8;
+    // Too few even of those (small f): half the width again, for twice the
+    // compute units (two tokens, d 2368, f 832, 2 of 48 experts: bf16 15.6 us
+    // against 17.6, fp32 23 against 31; more waves a block gained nothing.  With
+    // 512 waves, bf16, one token, d 4096, f 512, 8 of 64: 19.0 against 18.4).
+    if (!p.fuse_gate && T <= 16 && waves(f, 4, 8) < 0.75 * few) p.up_vw = 2;
     p.up_strips = cdiv(f, 16 * p.up_vw);
     // The down product's reduction f is long and its columns are few: chunks
     // of it until kChunkWaves waves run, each with at least 8 (narrow strips: 2)
@@ -857,7 +903,7 @@ FewPlan few_plan(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     p.down_vw = wide;
     p.down_nw = 4;
     int ks = chunks(wide, 4, 8);
-    if (waves(d, wide, 4) * ks < kFewWaves) {
+    if (waves(d, wide, 4) * ks < few) {
         p.down_vw = 4;
         p.down_nw = 8;
         ks = chunks(4, 8, 2);
@@ -901,23 +947,24 @@ moe_status few_run(const void* x, const void* Wg, const float* bias, const void*
         };
         if constexpr (sizeof(T) == 2)
             if (vw == 8) return by_nw(integral_constant<int, 8>{});
+        if constexpr (decltype(up)::value && NT == 1)
+            if (vw == 2) return go(integral_constant<int, 2>{}, integral_constant<int, 8>{});
         by_nw(integral_constant<int, 4>{});
     };
     if (p.fuse_gate) {
         if constexpr (NT == 1) {
             const GateArgs g{x, Wg, bias, Tn, d, renorm, logits, idx, w};
-            auto go = [&](auto ve, auto dual) {
+            auto go = [&](auto packed, auto dual) {
                 MOE_LAUNCH("few_gate_up", s,
-                           (few_gate_up_kernel<T, decltype(ve)::value, decltype(dual)::value>
+                           (few_gate_up_kernel<T, decltype(packed)::value, decltype(dual)::value>
                             <<<gu, 512, 0, s>>>(g, u)));
             };
-            constexpr int VE = 16 / sizeof(T);
-            std::integral_constant<int, VE> wide;
-            std::integral_constant<int, 1> one;
-            if (E % VE == 0 && aligned16(Wg)) {
-                if (sw) go(wide, std::true_type{}); else go(wide, std::false_type{});
+            if (gate_rows_aligned<T>(Wg, E)) {
+                if (sw) go(std::false_type{}, std::true_type{});
+                else go(std::false_type{}, std::false_type{});
             } else {
-                if (sw) go(one, std::true_type{}); else go(one, std::false_type{});
+                if (sw) go(std::true_type{}, std::true_type{});
+                else go(std::true_type{}, std::false_type{});
             }
         }
     } else if (sw) {
@@ -958,6 +1005,11 @@ moe_status moe_layer_fwd_few(const void* x, const void* Wg, const float* logit_b
     MOE_CHECK_ARG(x && Wg && W1 && W2 && y && (act != MOE_ACT_SWIGLU || W3));
     MOE_CHECK_ARG(aligned16(x) && aligned16(W1) && aligned16(W2) && aligned16(y) &&
                   (act != MOE_ACT_SWIGLU || aligned16(W3)));
+    auto whole = [](const void* q, unsigned bytes) {       // at an element, or NULL
+        return (reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0;
+    };
+    MOE_CHECK_ARG(whole(Wg, dt == MOE_BF16 ? 2 : 4) && whole(logit_bias, 4) && whole(logits, 4) &&
+                  whole(topk_idx, 4) && whole(topk_w, 4));
     const FewPlan p = few_plan(T, d, f, E, k, act, dt);
     if (!ws || ws_bytes < p.total) return MOE_ERR_WORKSPACE;
     MOE_CHECK_ARG((reinterpret_cast<uintptr_t>(ws) & 15u) == 0);

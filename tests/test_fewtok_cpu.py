@@ -46,6 +46,9 @@ def test_unaligned_rows_and_workspace(lib, mem):
     for n in ("x", "W1", "W2", "y", "ws"):
         assert call(lib, mem, **{n: p + 8}) == INV, n
     assert call(lib, mem, act=1, W3=p + 8) == INV
+    for n, off in (("Wg", 1), ("bias", 2), ("logits", 2), ("idx", 2), ("w", 2)):
+        assert call(lib, mem, **{n: p + off}) == INV, n
+    assert call(lib, mem, dt=0, Wg=p + 2) == INV
 
 
 def test_more_tokens_or_pairs_than_a_few(lib, mem):

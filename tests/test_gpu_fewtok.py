@@ -102,6 +102,9 @@ CASES = [
     (64, 128, 128, 3, 2, "gelu", "f32", 0),
     (64, 64, 64, 130, 64, "gelu", "bf16", 1),
     (9, 320, 64, 257, 7, "gelu", "bf16", 0),
+    (2, 2112, 64, 40, 2, "swiglu", "bf16", 1),
+    (5, 2048, 128, 33, 1, "gelu", "f32", 1),
+    (3, 2048, 192, 20, 2, "gelu", "bf16", 0),
     (6, 192, 64, 250, 9, "gelu", "f32", 0),
     (3, 64, 128, 1024, 5, "swiglu", "bf16", 0),
     (64, 64, 64, 1000, 3, "gelu", "f32", 1),
@@ -118,6 +121,28 @@ def test_against_the_oracle(case):
     got = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, k, act, b, renorm)
     torch.cuda.synchronize()
     compare(got, fw, bound, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("E", [1, 2, 3, 7, 9, 13, 16, 20, 35, 49, 64, 71, 119])
+def test_gate_rows_of_any_length_and_alignment(E, dt):
+    """Gate matrices whose rows are no multiple of a load, at any element of a
+    buffer that holds NaN before and behind them: the fixed-order logits' bits
+    and the choice, for d of one chunk and of several, with few and more tokens."""
+    for d, T in ((64, 1), (192, 6), (1088, 3)):
+        banner("few gate", E, dt, d, T)
+        k = min(E, 3)
+        a = inputs(T, d, 64, E, "gelu", dt, seed=E + d)
+        x, Wg, W1, W2, _, _ = upload(a, dt)
+        want = oracle.gate_logits(a[0], a[1])
+        for shift in (0, 1, 3):
+            buf = torch.full((d * E + 16,), float("nan"), dtype=TDT[dt], device="cuda")
+            g = buf[shift:shift + d * E].view(d, E)
+            g.copy_(Wg)
+            y, logits, idx, w = M.moe_layer_fwd_few(x, g, W1, W2, None, k)
+            torch.cuda.synchronize()
+            assert_equal_i(logits.cpu().numpy().view(np.uint32), want.view(np.uint32), "logits")
+            assert_equal_i(idx, oracle.topk_select(want, k), "topk_idx")
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
