@@ -765,9 +765,9 @@ class FewTokenMoELayer:
         """x [n,d], n <= T -> y [n,d]."""
         if x.device != self._y.device or x.dtype != self.dtype or not x.is_contiguous():
             raise MoEError("FewTokenMoELayer: x contiguous, of the layer's dtype and device")
-        n = x.shape[0]
-        if x.dim() != 2 or x.shape[1] != self.d or n > self.T:
+        if x.dim() != 2 or x.shape[1] != self.d or x.shape[0] > self.T:
             raise MoEError("FewTokenMoELayer: x [n,%d], n <= %d" % (self.d, self.T))
+        n = x.shape[0]
         if n != self._n:
             self._views(n)
         if torch.cuda.current_device() != self._index:

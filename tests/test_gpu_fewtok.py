@@ -281,3 +281,93 @@ def test_agrees_with_the_training_layer():
     torch.cuda.synchronize()
     assert torch.equal(few.logits, big.logits) and torch.equal(few.topk_idx, big.topk_idx)
     assert rel_err(host(few.y), host(big.y)) <= TOL["bf16"]
+
+
+def test_masked_experts_are_not_chosen():
+    """Logit biases of minus infinity and of fp32's lowest value: the masked
+    experts (weights NaN) are left out while enough others remain, and with too
+    few others they come last, lower index first, with weight 0."""
+    T, d, f, E, k = 9, 128, 64, 8, 2
+    banner("few masks")
+    low = float(np.finfo(np.float32).min)
+    bias = np.array([0, -np.inf, 0, low, -np.inf, 0, low, -np.inf], np.float32)
+    a = inputs(T, d, f, E, "gelu", "bf16", seed=80, bias=bias)
+    fw, bound = reference(a, k, "gelu", 1, "bf16")
+    x, Wg, W1, W2, _, b = upload(a, "bf16")
+    for e in np.flatnonzero(bias < 0):
+        W1[e] = float("nan")
+    got = M.moe_layer_fwd_few(x, Wg, W1, W2, None, k, "gelu", b)
+    torch.cuda.synchronize()
+    compare(got, fw, bound, "bf16")
+    W1 = dev(a[2], "bf16")
+    got = M.moe_layer_fwd_few(x, Wg, W1, W2, None, 6, "gelu", b)
+    torch.cuda.synchronize()
+    idx, w = got[2].cpu().numpy(), got[3].cpu().numpy()
+    assert all(set(r[:3]) == {0, 2, 5} and list(r[5:]) == [1] for r in idx)
+    assert (w[:, 3:] == 0).all() and np.allclose(w.sum(1), 1, atol=1e-6)
+    assert bool(torch.isfinite(got[0].float()).all())
+
+
+def test_optional_outputs_may_be_left_out():
+    """The C entry point without logits, topk_idx and topk_w: the same y, fused
+    with the gate (one token) and not (20 tokens)."""
+    from mixture_experts_layer_permute_amd import _lib
+    L = _lib.load()
+    d, f, E, k = 128, 192, 8, 2
+    for T in (1, 20):
+        banner("few optional outputs", T)
+        x, Wg, W1, W2, W3, _ = upload(inputs(T, d, f, E, "swiglu", "bf16", seed=90), "bf16")
+        want = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, k, "swiglu")[0]
+        y = torch.empty_like(want)
+        nb = L.moe_layer_few_workspace_bytes(T, d, f, E, k, 1, 1)
+        ws = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
+        p = lambda t: t.data_ptr()
+        assert L.moe_layer_fwd_few(p(x), p(Wg), None, p(W1), p(W3), p(W2), T, d, f, E, k, 1, 1, 1,
+                                   None, None, None, p(y), p(ws), nb,
+                                   torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_an_expert_past_the_32_bit_offsets(dt):
+    """Weight tensors over 2^32 bytes, the last expert chosen by its bias; the
+    others' weights are whatever the memory holds."""
+    T, d, f, E = 3, 1024, 65536, 36 if dt == "bf16" else 18
+    banner("few large", dt)
+    assert E * d * f * (2 if dt == "bf16" else 4) > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=TDT[dt])
+    x, Wg = r(T, d), r(d, E) * d ** -0.5
+    W1 = torch.empty(E, d, f, dtype=TDT[dt], device="cuda")
+    W2 = torch.empty(E, f, d, dtype=TDT[dt], device="cuda")
+    W1[-1] = r(d, f) * d ** -0.5
+    W2[-1] = r(f, d) * f ** -0.5
+    bias = torch.zeros(E, device="cuda")
+    bias[-1] = 1000
+    y, _, idx, _ = M.moe_layer_fwd_few(x, Wg, W1, W2, None, 1, "gelu", bias)
+    torch.cuda.synchronize()
+    assert bool((idx == E - 1).all())
+    h = x.double() @ W1[-1].double()
+    want = (h * torch.special.ndtr(h)) @ W2[-1].double()
+    assert rel_err(host(y), want.cpu().numpy()) <= TOL[dt]
+
+
+def test_refusals_of_the_layer():
+    layer = M.FewTokenMoELayer(4, 64, 128, 4, 2, "swiglu")
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")
+    ok = (z(64, 4), z(4, 64, 128), z(4, 128, 64), z(4, 64, 128))
+    for bad in ((z(64, 5),) + ok[1:], (ok[0], z(4, 64, 64)) + ok[2:], ok[:3],
+                ok[:2] + (z(4, 64, 128),) + ok[3:], (ok[0].float(),) + ok[1:],
+                (ok[0].cpu(),) + ok[1:], ok + (z(4, dt=torch.bfloat16),)):
+        with pytest.raises(M.MoEError):
+            layer.bind(*bad)
+    layer.bind(*ok)
+    for x in (z(5, 64), z(2, 128), z(64), z(2, 64, dt=torch.float32), z(64, 2).t(),
+              torch.zeros(2, 64, dtype=torch.bfloat16)):
+        with pytest.raises(M.MoEError):
+            layer.forward(x)
+    for bad in (dict(T=65), dict(T=0), dict(k=65, E=80), dict(d=96), dict(f=100), dict(k=5)):
+        a = dict(dict(T=4, d=64, f=128, E=4, k=2), **bad)
+        with pytest.raises(M.MoEError):
+            M.FewTokenMoELayer(**a)

@@ -298,3 +298,22 @@ def test_overlapping_tensors_are_refused():
     with pytest.raises(M.MoEError):
         M.moe_grad_norm([flat.view(10, 10).t()])
     assert float(M.moe_grad_norm([a, a])[0]) == 0.0         # only read: any list will do
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_elements_past_the_32_bit_offsets(dt):
+    """A tensor over 2^32 bytes (bf16: over 2^31 elements), zeros but for five
+    elements, the last among them: the exact norm, and those five scaled."""
+    n = 2 ** 31 + 12345 if dt == BF else 2 ** 30 + 12345
+    banner("gradnorm large", dt)
+    t = torch.zeros(n, dtype=dt, device="cuda")
+    at = [0, 7, n // 2 + 3, n - 9, n - 1]
+    for i in at:
+        t[i] = 4.0
+    t[at[2]] = 6.0                                          # 4 * 16 + 36 = 100
+    c = M.GradClip([t])
+    assert float(c.norm()[0]) == 10.0
+    assert float(c.clip(2.5)[0]) == 10.0
+    torch.cuda.synchronize()
+    assert [float(t[i]) for i in at] == [1.0, 1.0, 1.5, 1.0, 1.0]
+    assert int(torch.count_nonzero(t)) == 5
