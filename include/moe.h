@@ -354,12 +354,12 @@ moe_status moe_gate_topk_bwd(const void *x, const void *Wg, const float *logits,
  * moe_layer_fwd_few -- the whole layer (gate, top-k, expert FFNs, weighted
  * sum) for a few tokens, forward only: one step of a serving loop.
  *   y[t,:] = sum_{j=0..k-1} topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t,:])
- * with the logits of moe_gate_topk (the same bits) and its choice (NaN logits
- * rank below all others here), its gate weights (to fp32 rounding) and the FFN of moe_expert_ffn_fwd (for
- * bf16 the inner activation is kept to 16 significant bits instead of 8; every
- * sum in fp32, y rounded once).  Each
- * expert that any token chose is read once, whatever the number of tokens;
- * experts no token chose are not read.  Nothing is kept for a backward.
+ * with the logits of moe_gate_topk (the same bits) and its choice (a NaN logit
+ * ranks below all others here), its gate weights (to fp32 rounding) and the FFN
+ * of moe_expert_ffn_fwd (for bf16 the inner activation is kept to 16 significant
+ * bits instead of 8; every sum in fp32, y rounded once).  Each expert that any
+ * token chose is read once, whatever the number of tokens; experts no token
+ * chose are not read.  Nothing is kept for a backward.
  *   x [T,d] dt, Wg [d,E] dt, logit_bias [E] float or NULL, W1 [E,d,f],
  *   W3 [E,d,f] (SwiGLU only, else NULL), W2 [E,f,d] dt, y [T,d] dt (may not
  *   overlap an input); logits [T,E] float, topk_idx [T,k] int32, topk_w [T,k]
@@ -389,7 +389,8 @@ moe_status moe_layer_fwd_few(const void *x, const void *Wg,
  * tensors and the list scaled to a largest norm, for a training step between
  * the backward pass and the optimizer.
  *   norm   = sqrt(sum over all tensors of g^2), summed in fp64, rounded once
- *   out[i] = grads[i] * (norm > max_norm ? max_norm / norm : 1), rounded once
+ *   out[i] = grads[i] * (norm > max_norm ? max_norm / norm : 1), the factor
+ *            in fp32, the product rounded once
  * A norm that is not finite (or above the fp32 range) scales nothing: norm
  * says so, and out holds the gradients as they were.
  *   grads, out [n]: host arrays of device pointers; numel [n]: elements of

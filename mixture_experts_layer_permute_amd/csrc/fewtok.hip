@@ -941,15 +941,12 @@ moe_status few_run(const void* x, const void* Wg, const float* bias, const void*
                        (few_product_kernel<T, decltype(vwc)::value, NT, NWC, decltype(up)::value,
                                            decltype(dual)::value><<<grid, 64 * NWC, 0, s>>>(a)));
         };
-        auto by_nw = [&](auto vwc) {
-            if (nw == 8) go(vwc, integral_constant<int, 8>{});
-            else go(vwc, integral_constant<int, 4>{});
-        };
-        if constexpr (sizeof(T) == 2)
-            if (vw == 8) return by_nw(integral_constant<int, 8>{});
+        // few_plan's: the type's wide strips with 4 waves, narrower ones with 8
+        constexpr integral_constant<int, sizeof(T) == 2 ? 8 : 4> wide{};
+        if (nw == 4) return go(wide, integral_constant<int, 4>{});
         if constexpr (decltype(up)::value && NT == 1)
             if (vw == 2) return go(integral_constant<int, 2>{}, integral_constant<int, 8>{});
-        by_nw(integral_constant<int, 4>{});
+        go(integral_constant<int, 4>{}, integral_constant<int, 8>{});
     };
     if (p.fuse_gate) {
         if constexpr (NT == 1) {

@@ -10,7 +10,7 @@ import math
 import torch
 
 from ._lib import MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F32, check, load
-from .ops import GradClip, MoEError, _few_check, _stream
+from .ops import GradClip, MoEError, _act, _dt, _few_check, _stream
 
 
 def _torch_stream(handle, device):
@@ -712,15 +712,16 @@ class FewTokenMoELayer:
     returns y [n,d]; logits, topk_idx and topk_w are of the last forward.
     They and y are views of the layer's buffers, overwritten by the next
     forward: two steps in flight at once (two streams, two captured graphs)
-    need a layer each.
+    need a layer each.  stream: a HIP stream handle, the current stream if None;
+    x has to be ready on it.
     """
 
     def __init__(self, T, d, f, E, k, act="gelu", dtype=torch.bfloat16, renorm=1,
                  device="cuda"):
         self.T, self.d, self.f, self.E, self.k = T, d, f, E, k
-        self.act = MOE_ACT_SWIGLU if act == "swiglu" else MOE_ACT_GELU
+        self.act = _act(act)
         self.dtype = dtype
-        self.dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F32
+        self.dt = _dt(torch.empty(0, dtype=dtype))
         self.renorm = renorm
         self.device = torch.device(device)
         L = self.lib = load()
@@ -739,6 +740,7 @@ class FewTokenMoELayer:
         self._w = e(T, k, dt=torch.float32)
         self.ws = e(nb, dt=torch.uint8)
         self._index = self._y.device.index
+        self._weights = None
         self._views(T)
 
     def _views(self, n):
@@ -767,6 +769,8 @@ class FewTokenMoELayer:
             raise MoEError("FewTokenMoELayer: x contiguous, of the layer's dtype and device")
         if x.dim() != 2 or x.shape[1] != self.d or x.shape[0] > self.T:
             raise MoEError("FewTokenMoELayer: x [n,%d], n <= %d" % (self.d, self.T))
+        if self._weights is None:
+            raise MoEError("FewTokenMoELayer: bind() the weights first")
         n = x.shape[0]
         if n != self._n:
             self._views(n)

@@ -332,6 +332,8 @@ def moe_layer_fwd_few(x, Wg, W1, W2, W3=None, k=1, act="gelu", logit_bias=None, 
             raise MoEError("out: y [T,d], logits [T,E], topk_idx [T,k], topk_w [T,k]")
     if ws is None:
         ws = _ws(L.moe_layer_few_workspace_bytes(T, d, f, E, k, a, _dt(x)), dev)
+    elif ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise MoEError("ws: contiguous uint8 on the inputs' device")
     with torch.cuda.device(dev):
         check(L.moe_layer_fwd_few(_p(x), _p(Wg), _p(logit_bias), _p(W1), _p(W3), _p(W2), T, d,
                                   f, E, k, renorm, a, _dt(x), _p(logits), _p(topk_idx),
@@ -374,7 +376,7 @@ class GradClip:
         self._dts = (ctypes.c_int32 * n)(*[_dt(g) for g in self.grads])
         L = self.lib = load()
         self.ws = _ws(L.moe_grad_norm_workspace_bytes(self._numel, self._dts, n), dev)
-        self.result = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.result = torch.empty(1, dtype=torch.float32, device=dev)
         self._res, self._ws, self._ws_bytes = _p(self.result), _p(self.ws), self.ws.numel()
 
     def _no_overlap(self):

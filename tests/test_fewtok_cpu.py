@@ -84,3 +84,18 @@ def test_the_binding_takes_device_tensors_only():
     with pytest.raises(M.MoEError):
         M.moe_layer_fwd_few(t, torch.zeros(64, 4), torch.zeros(4, 64, 64),
                             torch.zeros(4, 64, 64), k=2)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=torch.float16), dict(dtype=torch.float64),
+                                dict(act="relu"), dict(T=65), dict(T=0), dict(d=96), dict(k=9)])
+def test_the_layer_takes_the_library_s_types_only(kw):
+    """float16 buffers would be read as float32 ones, past their end."""
+    a = dict(dict(T=4, d=64, f=128, E=8, k=2, device="cpu"), **kw)
+    with pytest.raises(M.MoEError):
+        M.FewTokenMoELayer(**a)
+
+
+def test_the_layer_needs_its_weights_first():
+    layer = M.FewTokenMoELayer(4, 64, 128, 8, 2, device="cpu")
+    with pytest.raises(M.MoEError):
+        layer.forward(torch.zeros(1, 64, dtype=torch.bfloat16))

@@ -371,3 +371,11 @@ def test_refusals_of_the_layer():
         a = dict(dict(T=4, d=64, f=128, E=4, k=2), **bad)
         with pytest.raises(M.MoEError):
             M.FewTokenMoELayer(**a)
+
+
+def test_workspace_of_another_type_or_device():
+    x, Wg, W1, W2, _, _ = upload(inputs(2, 64, 64, 4, "gelu", "bf16", seed=95), "bf16")
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, device="cuda"),
+               torch.empty(16, dtype=torch.uint8, device="cuda")):
+        with pytest.raises(M.MoEError):
+            M.moe_layer_fwd_few(x, Wg, W1, W2, None, 2, "gelu", ws=ws)
