@@ -532,11 +532,12 @@ template <> struct Core<float> {
     }
 };
 
-// xrow: each tile's token of this lane, its next step xstep elements on; lo:
+// x + xoff: each tile's token of this lane, its next step xstep elements on; lo:
 // from a value to its rest.  NB - 1 steps are in flight while one is multiplied.
-template <typename T, int VW, int NT, int NB, bool LO>
-__device__ __forceinline__ void strip_product(const T* W, long ldw, const T* const (&xrow)[NT],
-                                              long xstep, long lo, int s0, int s1, f32x4 (&acc)[NT][VW]) {
+template <typename T, int VW, int NT, int NB, bool LO, typename Off>
+__device__ __forceinline__ void strip_product(const T* W, long ldw, const T* x,
+                                              const Off (&xoff)[NT], long xstep, long lo, int s0,
+                                              int s1, f32x4 (&acc)[NT][VW]) {
     typedef Core<T> C;
     const int g = (threadIdx.x & 63) >> 4;
     typename C::template Raw<VW> wr[NB];
@@ -544,7 +545,8 @@ __device__ __forceinline__ void strip_product(const T* W, long ldw, const T* con
     auto fetch = [&](int s, int b) {
         C::template load<VW>(W, ldw, s * C::KSTEP, g, wr[b]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) C::template loadx<LO>(xrow[i] + s * xstep, lo, g, xr[b][i]);
+        for (int i = 0; i < NT; ++i) 
+            C::template loadx<LO>(x + s * xstep + xoff[i], lo, g, xr[b][i]);
     };
 #pragma unroll
     for (int u = 0; u < NB - 1; ++u)
@@ -563,6 +565,40 @@ __device__ __forceinline__ void strip_product(const T* W, long ldw, const T* con
         if (s + u + NB - 1 < s1) fetch(s + u + NB - 1, (u + NB - 1) % NB);
         C::template mul<VW, NT, LO>(wr[u % NB], xr[u % NB], acc);
     }
+}
+
+// The same for three and four tiles of bf16, whose accumulators leave registers
+// for two steps of W and one of x: x of a step is asked for before W of the next,
+// so that waiting for it leaves those weights in flight.  The order of the loads
+// is the point, so it is held (left to the compiler's scheduling, which spills:
+// 1194 us against 746, the down product of 34 rows for each of 32 experts, d 4096,
+// f 14336).
+template <typename T, int VW, int NT, bool LO, typename Off>
+__device__ __forceinline__ void strip_tall(const T* W, long ldw, const T* x,
+                                           const Off (&xoff)[NT], long xstep, long lo, int s0,
+                                           int s1, f32x4 (&acc)[NT][VW]) {
+    typedef Core<T> C;
+    const int g = (threadIdx.x & 63) >> 4;
+    typename C::template Raw<VW> wr[2];
+    auto loadw = [&](int s, int b) { C::template load<VW>(W, ldw, s * C::KSTEP, g, wr[b]); };
+    auto step = [&](int s, int b, bool more) {
+        typename C::template XRaw<LO> xr[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) C::template loadx<LO>(x + s * xstep + xoff[i], lo, g, xr[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) loadw(s + 1, b ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        C::template mul<VW, NT, LO>(wr[b], xr, acc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (s0 < s1) loadw(s0, 0);
+    int s = s0;
+    for (; s + 3 <= s1; s += 2) {
+        step(s, 0, true);
+        step(s + 1, 1, true);
+    }
+    if (s < s1) step(s, 0, s + 1 < s1);
+    if (s + 1 < s1) step(s + 1, 1, false);
 }
 
 // One wave's accumulators of 16 tokens into its LDS slab [16][BN + 4].
@@ -648,24 +684,20 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, in
     const int c = lane & 15;
     const T* We = static_cast<const T*>(DUAL && wv >= KW ? p.W3 : p.W) + (long)e * p.K * p.N;
     const int n0 = blockIdx.x * 16 * VW;
-    // NT tiles of 16 rows per wave, depth steps of registers; halves = 2: half
-    // of the waves take rows 32 and on, and each half splits the chunk
-    auto body = [&](auto tiles, auto depth, auto halves) {
-        constexpr int NT = decltype(tiles)::value, H = decltype(halves)::value;
+    // NT tiles of 16 rows per wave, depth steps of registers
+    auto body = [&](auto tiles, auto depth) {
+        constexpr int NT = decltype(tiles)::value;
         constexpr int BN = 16 * VW, LD = BN + 4;
-        constexpr int PARTS = KW / H;
-        static_assert(H == 1 || !DUAL, "rows or weights are split between the waves");
-        const int half = H == 1 ? 0 : wv / PARTS;
         const int steps = p.K / KSTEP;
-        const int units = gridDim.z * PARTS, u = blockIdx.z * PARTS + wv % PARTS;
+        const int units = gridDim.z * KW, u = blockIdx.z * KW + wv % KW;
         const int s0 = (int)((long)steps * u / units), s1 = (int)((long)steps * (u + 1) / units);
-        const T* xrow[NT];
+        const T* x = static_cast<const T*>(p.x) + (UP ? 0 : (long)base * KSTEP);
+        std::conditional_t<UP, long, int> xoff[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            // rows past n: the last one's again
-            const int q = min(half * 32 + i * 16 + c, n - 1);
-            xrow[i] = static_cast<const T*>(p.x) +
-                      (UP ? (long)(rows[q] / p.k) * p.K : (long)(base + q) * KSTEP);
+            const int q = min(i * 16 + c, n - 1);          // rows past n: the last one's again
+            if constexpr (UP) xoff[i] = (long)(rows[q] / p.k) * p.K;
+            else xoff[i] = q * KSTEP;
         }
         f32x4 acc[NT][VW];
 #pragma unroll
@@ -673,20 +705,23 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, in
 #pragma unroll
             for (int j = 0; j < VW; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // columns past N (a multiple of 64) read the last ones of the row instead
-        strip_product<T, VW, NT, decltype(depth)::value, LO>(
-            We + min(n0 + c * VW, p.N - VW), p.N, xrow, UP ? KSTEP : (long)p.pairs * KSTEP,
-            (long)p.pairs * p.K, s0, s1, acc);
+        const T* Wn = We + min(n0 + c * VW, p.N - VW);
+        const long xstep = UP ? KSTEP : (long)p.pairs * KSTEP, lo = (long)p.pairs * p.K;
+        if constexpr (sizeof(T) == 2 && NT > 2)
+            strip_tall<T, VW, NT, LO>(Wn, p.N, x, xoff, xstep, lo, s0, s1, acc);
+        else
+            strip_product<T, VW, NT, decltype(depth)::value, LO>(Wn, p.N, x, xoff, xstep, lo, s0,
+                                                                 s1, acc);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             if (i * 16 >= n) break;
             if (i > 0) __syncthreads();
             slab_store<VW>(red + wv * 16 * LD, acc[i]);
             __syncthreads();
-            for (int q = tid; q < H * 16 * BN / 4; q += 64 * NW) {
-                const int hq = q / (16 * BN / 4), row = q / (BN / 4) % 16, cl = q % (BN / 4) * 4;
-                const int r = hq * 32 + i * 16 + row;
+            for (int q = tid; q < 16 * BN / 4; q += 64 * NW) {
+                const int row = q / (BN / 4), cl = q % (BN / 4) * 4, r = i * 16 + row;
                 if (r >= n || n0 + cl >= p.N) continue;
-                const float4 s = slab_sum<VW, PARTS>(red + hq * PARTS * 16 * LD, row, cl);
+                const float4 s = slab_sum<VW, KW>(red, row, cl);
                 float v[4] = {s.x, s.y, s.z, s.w};
                 if constexpr (UP) {
                     if constexpr (DUAL) {
@@ -718,26 +753,20 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, in
             }
         }
     };
-    // The expert's rows in tiles of 16.  Up: one, two or four of them to a wave.
-    // Down: a wave with two operands per token has registers for two; rows past
-    // 32 are the other half of the waves', which read the strip a second time,
-    // from the caches, at about the same time (in blocks of their own they were
-    // 19% more misses of the L2).
+    // The expert's rows in tiles of 16, one to four of them to a wave
     using std::integral_constant;
-    constexpr integral_constant<int, 1> one{};
     constexpr integral_constant<int, 2> two{};
     if constexpr (NTM >= 4) {
-        if (n > 32) {
-            if constexpr (LO) return body(two, two, two);
-            else return body(integral_constant<int, 4>{}, two, one);
-        }
+        if (n > 48) return body(integral_constant<int, 4>{}, two);
+        if (n > 32) return body(integral_constant<int, 3>{}, two);
     }
     if constexpr (NTM >= 2) {
-        if (n > 16) return body(two, two, one);
+        if (n > 16) return body(two, two);
     }
     // (one tile, fp32: three steps deep 151 us against 158 with four, one token
     // of d 4096, f 14336, 2 of 8 experts; bf16, half-width strips: four)
-    body(one, integral_constant<int, (VW == 8 || sizeof(T) == 4 ? 3 : 4)>{}, one);
+    body(integral_constant<int, 1>{},
+         integral_constant<int, (VW == 8 || sizeof(T) == 4 ? 3 : 4)>{});
 }
 
 template <typename T, int VW, int NTM, int NW, bool UP, bool DUAL>
