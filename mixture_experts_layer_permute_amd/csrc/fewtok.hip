@@ -668,7 +668,8 @@ __device__ __forceinline__ int block_expert(const FewArgs& p, const int32_t* idx
 // blocks of KSTEP columns (64 bytes), so that the 16 tokens' 64 bytes of one
 // step are eight whole cache lines; by token they were 16 half ones, and with
 // few registers' worth of loads in flight the number of lines asked for is what
-// bounds these kernels (T 64, d 4096, f 14336, 32 experts: 768 us against 825).
+// bounds these kernels (T 64, d 4096, f 14336, 32 experts, two tiles to a wave: 768
+// us against 825; as it is now, 662, 5.7 TB/s).
 // h in bf16 is kept as the sum of two (h_lo, the rest that the first rounding
 // left, follows h): the matrix cores wait for memory here anyway, and one
 // rounding of h was the largest part of y's error (0.0024 of |y| against
@@ -828,7 +829,10 @@ __global__ __launch_bounds__(512, 2) void few_gate_up_kernel(GateArgs g, FewArgs
 
 // y[t] = sum over a token's k slots and ks chunks of w[t,j] partial[s][t k + j],
 // rounded once.  A block takes 128 columns of one token; eight groups of 32
-// threads take every eighth (slot, chunk) each, and meet in LDS, in order.
+// threads take every eighth (slot, chunk) each, and meet in LDS, in order.  It is
+// a launch and one round trip to memory long (3 to 4.5 us): in the down product
+// its sums would need a wait of blocks for each other, or atomics, whose order
+// changes bits.
 constexpr int kCombineCols = 128;
 template <typename T>
 __global__ __launch_bounds__(256) void few_combine_kernel(const float* __restrict__ partial,
@@ -919,8 +923,9 @@ FewPlan few_plan(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     // of it until kChunkWaves waves run, each with at least 8 (narrow strips: 2)
     // steps to go: short blocks, since the experts with the most rows take
     // longest and may come last.  (T 48, d 1024, f 4096, 64 experts, this product:
-    // 41 us with 6000, 54 with 3000; T 64, d 4096, f 14336, 32 experts: 767 and
-    // 893; T 16, f 1024, whole pass: 78 unsplit, 81 in chunks of 4 steps.)
+    // 31 us with 6000 or 12000, 38 with 3000; T 64, d 4096, f 14336, 32 experts:
+    // 662 with 6000, 668 with 3000, 694 with 12000; T 16, f 1024, whole pass: 78
+    // unsplit, 81 in chunks of 4 steps.)
     const int steps = f / (dt == MOE_BF16 ? 32 : 16);
     auto chunks = [&](int vw, int nw, int least) {
         int ks = 1;
