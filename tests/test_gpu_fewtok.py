@@ -379,3 +379,40 @@ def test_workspace_of_another_type_or_device():
                torch.empty(16, dtype=torch.uint8, device="cuda")):
         with pytest.raises(M.MoEError):
             M.moe_layer_fwd_few(x, Wg, W1, W2, None, 2, "gelu", ws=ws)
+
+
+@pytest.mark.parametrize("T", [17, 33, 48, 49, 64])
+@pytest.mark.parametrize("act,dt", [("gelu", "bf16"), ("swiglu", "bf16"), ("swiglu", "f32")])
+def test_tall_tiles_of_wide_strips(T, act, dt):
+    """Two to four tiles of rows for each of 8 experts, in sizes that give the
+    widest strips, the last one half full: against the products in 64 bits on
+    the device, within the bound above."""
+    banner("few tall", T, act, dt)
+    d, f, E = 1216, 2496, 8
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") * s[-2] ** -0.5).to(TDT[dt])
+    x, Wg, W1, W2 = r(T, d) * T ** 0.5, r(d, E), r(E, d, f), r(E, f, d)
+    W3 = r(E, d, f) if act == "swiglu" else None
+    y, logits, idx, _ = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, E, act)
+    assert torch.equal(logits, M.moe_gate_topk(x, Wg, E)[0])
+    assert bool((idx.sort(1).values == torch.arange(E, device="cuda")).all())
+    w, x64 = logits.double().softmax(1), x.double()
+    want, bound = torch.zeros_like(x64), torch.zeros_like(x64)
+    for e in range(E):
+        W1e, W2e = W1[e].double(), W2[e].double()
+        H, dH = x64 @ W1e, (d + 2) * U * (x64.abs() @ W1e.abs())
+        if act == "swiglu":
+            W3e = W3[e].double()
+            H3, dH3 = x64 @ W3e, (d + 2) * U * (x64.abs() @ W3e.abs())
+            s = H * torch.sigmoid(H)
+            A, dA = s * H3, 1.1 * dH * (H3.abs() + dH3) + s.abs() * dH3
+        else:
+            A, dA = H * torch.special.ndtr(H), 1.13 * dH
+        dA = dA + 8 * U * A.abs()
+        dA = dA + (2.0 ** -16 if dt == "bf16" else 0.0) * (A.abs() + dA)
+        want += w[:, e:e + 1] * (A @ W2e)
+        bound += w[:, e:e + 1] * ((dA + (f + 128) * U * A.abs()) @ W2e.abs())
+    bound = (bound + HALF[dt] * want.abs()) * 1.001 + 1e-30
+    err = (y.double() - want).abs()
+    assert bool((err <= bound).all()), "off by %.2f of its bound" % float((err / bound).max())
+    assert rel_err(host(y), want.cpu().numpy()) <= TOL[dt]
