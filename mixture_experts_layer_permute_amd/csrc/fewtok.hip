@@ -756,7 +756,8 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, in
             }
         }
     };
-    // The expert's rows in tiles of 16, one to four of them to a wave
+    // The expert's rows in tiles of 16, one to four of them to a wave (34 rows for
+    // each of 32 experts, down: three tiles 701 us, four 746)
     using std::integral_constant;
     constexpr integral_constant<int, 2> two{};
     if constexpr (NTM >= 4) {
