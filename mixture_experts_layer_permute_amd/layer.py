@@ -32,8 +32,10 @@ def _weight_grads(layer):
 
 
 def _clip_grads(layer, max_norm, stream):
-    if getattr(layer, "_clip", None) is None:
-        layer._clip = GradClip(_weight_grads(layer))     # the buffers never move
+    grads = _weight_grads(layer)
+    clip = getattr(layer, "_clip", None)
+    if clip is None or any(a is not b for a, b in zip(grads, clip.grads)):
+        layer._clip = GradClip(grads)
     return layer._clip.clip(max_norm, stream)
 
 

@@ -317,3 +317,18 @@ def test_elements_past_the_32_bit_offsets(dt):
     torch.cuda.synchronize()
     assert [float(t[i]) for i in at] == [1.0, 1.0, 1.5, 1.0, 1.0]
     assert int(torch.count_nonzero(t)) == 5
+
+
+@pytest.mark.parametrize("kind", ["whole", "chunked"])
+def test_a_layer_given_other_gradient_tensors_clips_those(kind):
+    banner("clip_grads of other tensors", kind)
+    layer = M.MoELayer(8, 64, 64, 2, 1) if kind == "whole" else \
+        M.ChunkedMoELayer(8, 64, 64, 2, 1, chunk_tokens=4)
+    for _ in range(2):
+        new = tensors([(BF, g.shape) for g in layer.weight_grads()], seed=30 + _)
+        layer.dWg, layer.dW1, layer.dW2 = new
+        keep, want = [g.clone() for g in new], exact_norm(new)
+        norm = layer.clip_grads(want / 2)
+        torch.cuda.synchronize()
+        check_norm(norm, keep)
+        check_clipped(new, keep, want, np.float64(np.float32(want / 2)))
