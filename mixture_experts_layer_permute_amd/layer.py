@@ -31,11 +31,19 @@ def _weight_grads(layer):
     return [g for g in (layer.dWg, layer.dW1, layer.dW3, layer.dW2) if g is not None]
 
 
+def _grad_clip(layer):
+    """The GradClip over a layer's gradient buffers, made with them: memory that
+    torch hands out in the middle of a step may still be in use on its current
+    stream, and the step may run on another one."""
+    return GradClip(_weight_grads(layer)) if layer.dWg.is_cuda else None
+
+
 def _clip_grads(layer, max_norm, stream):
     grads = _weight_grads(layer)
-    clip = getattr(layer, "_clip", None)
-    if clip is None or any(a is not b for a, b in zip(grads, clip.grads)):
-        layer._clip = GradClip(grads)
+    if layer._clip is None or any(a is not b for a, b in zip(grads, layer._clip.grads)):
+        # the caller gave the layer other gradient tensors
+        with torch.cuda.stream(_torch_stream(stream, layer.dWg.device)):
+            layer._clip = GradClip(grads)
     return layer._clip.clip(max_norm, stream)
 
 
@@ -88,6 +96,7 @@ class MoELayer:
         self.ws_ffn_f = ws(L.moe_ffn_workspace_bytes(R, E, d, f, self.act, self.dt, 0))
         self.ws_ffn_b = ws(L.moe_ffn_workspace_bytes(R, E, d, f, self.act, self.dt, 1))
         self.ws_gate = ws(L.moe_gate_bwd_workspace_bytes(T, d, E))
+        self._clip = _grad_clip(self)
 
     def bind(self, x, Wg, W1, W2, W3=None, logit_bias=None, dy=None):
         """Remember the input tensors (device, contiguous, layer dtype)."""
@@ -198,9 +207,9 @@ class MoELayer:
 
     def clip_grads(self, max_norm, stream=None):
         """Scale the weight gradients to the global norm max_norm if theirs is
-        larger, in place, on the step's stream -> the norm before, [1] float32
-        (a model of several layers clips them together: GradClip over all
-        their weight_grads())."""
+        larger, in place, on the step's stream -> the norm before, [1] float32,
+        overwritten by the layer's next clip_grads (a model of several layers
+        clips them together: GradClip over all their weight_grads())."""
         return _clip_grads(self, max_norm, stream)
 
     def stage_calls(self):
@@ -281,6 +290,7 @@ class ChunkedMoELayer:
         self.ws_ffn_b = ws(L.moe_ffn_workspace_bytes(Rc, E, d, f, self.act, self.dt, 1))
         self.ws_gate = ws(L.moe_gate_bwd_workspace_bytes(T, d, E))
         self._resident = -1                    # chunk whose state the buffers hold
+        self._clip = _grad_clip(self)
 
     def bind(self, x, Wg, W1, W2, W3=None, logit_bias=None, dy=None):
         for t in (x, Wg, W1, W2, W3, dy):
@@ -378,7 +388,8 @@ class ChunkedMoELayer:
         return _weight_grads(self)
 
     def clip_grads(self, max_norm, stream=None):
-        """MoELayer.clip_grads: in place, -> the norm before, [1] float32."""
+        """MoELayer.clip_grads: in place, -> the norm before, [1] float32,
+        overwritten by the next call."""
         return _clip_grads(self, max_norm, stream)
 
 

@@ -352,6 +352,10 @@ class GradClip:
     clip() writes, tensors like grads; None: in place.  norm() and clip()
     return the norm as a float32 tensor of one element, overwritten by the
     next call: two calls in flight at once need a GradClip each.
+    The result and the workspace come from torch's current stream when the
+    GradClip is made: make it outside the step (as the layers do), or on the
+    stream it is then called on, and keep it until its work is done.  A tensor
+    given other memory since (t.data = ...) needs a new one.
     """
 
     def __init__(self, grads, out=None):

@@ -332,3 +332,35 @@ def test_a_layer_given_other_gradient_tensors_clips_those(kind):
         torch.cuda.synchronize()
         check_norm(norm, keep)
         check_clipped(new, keep, want, np.float64(np.float32(want / 2)))
+
+
+@pytest.mark.parametrize("kind", ["whole", "chunked"])
+def test_a_layer_s_first_clip_on_a_side_stream(kind):
+    """The step and the layer's first clip_grads on a stream that is not torch's
+    current one, by its handle: nothing is allocated by then (such memory is
+    ordered on the current stream alone), the norm is the gradients' 64-bit one,
+    and the next call overwrites it."""
+    banner("clip_grads on a side stream", kind)
+    cfg = small_variant("moe_s_like", T=300, d=128, f=256, E=4, k=2, act="gelu", dtype="bf16",
+                        zipf_s=None, alpha=0.0)
+    t = device.gen_all(cfg)
+    args = (cfg.T, cfg.d, cfg.f, cfg.E, cfg.k, cfg.act, BF, cfg.renorm)
+    layer = M.MoELayer(*args) if kind == "whole" else M.ChunkedMoELayer(*args, chunk_tokens=128)
+    layer.bind(t["x"], t["Wg"], t["W1"], t["W2"], None, t["bias"], t["dy"])
+    layer.step()
+    torch.cuda.synchronize()
+    raw = [g.clone() for g in layer.weight_grads()]
+    want = exact_norm(raw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    layer.step(side.cuda_stream)
+    made = torch.cuda.memory_stats()["allocation.all.allocated"]
+    norm = layer.clip_grads(want / 2, side.cuda_stream)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == made
+    side.synchronize()
+    check_norm(norm, raw)
+    check_clipped(layer.weight_grads(), raw, want, np.float64(np.float32(want / 2)))
+    again = layer.clip_grads(want, side.cuda_stream)
+    side.synchronize()
+    assert again.data_ptr() == norm.data_ptr()
+    assert abs(float(norm[0]) / (want / 2) - 1) <= 2.0 ** -8 + 8 * U
