@@ -389,8 +389,9 @@ moe_status moe_layer_fwd_few(const void *x, const void *Wg,
  * tensors and the list scaled to a largest norm, for a training step between
  * the backward pass and the optimizer.
  *   norm   = sqrt(sum over all tensors of g^2), summed in fp64, rounded once
- *   out[i] = grads[i] * (norm > max_norm ? max_norm / norm : 1), the factor
- *            in fp32, the product rounded once
+ *   out[i] = grads[i] * (norm > max_norm ? max_norm / norm : 1), factor and
+ *            product in fp32 (in fp64 for a factor below 2^-126, rounded to
+ *            fp32), a bf16 element then rounded to bf16
  * A norm that is not finite (or above the fp32 range) scales nothing: norm
  * says so, and out holds the gradients as they were.
  *   grads, out [n]: host arrays of device pointers; numel [n]: elements of

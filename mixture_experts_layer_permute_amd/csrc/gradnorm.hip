@@ -16,6 +16,7 @@
 // there, no gradient is too large or too small to be squared, and the norm is
 // the correctly rounded one whatever the order.  Partial sums are stored per
 // block and added in block order: no atomics, the same bits every time.
+#include <float.h>
 #include <math.h>
 
 #include "common.h"
@@ -147,16 +148,19 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(const double* __restrict
     if (threadIdx.x == 0) *norm = v;
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, float c) {
+// WIDE: by a factor below fp32's normal range, which has lost bits there (or is
+// 0): factor and product in fp64.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, double c) {
     typedef typename Packed<T>::type P;
     constexpr int V = Vec16<T>::N, UN = 4;
     const int nvec = len / V;
+    auto times = [&](float a) { return WIDE ? (float)((double)a * c) : a * (float)c; };
     auto scaled = [&](u32x4_t raw) {
         float a[V];
         unpack16<T>(raw, a);
 #pragma unroll
-        for (int q = 0; q < V; ++q) a[q] *= c;
+        for (int q = 0; q < V; ++q) a[q] = times(a[q]);
         return pack16<T>(a);
     };
     int v = threadIdx.x;
@@ -172,7 +176,16 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, float c) 
     for (; v < nvec; v += 256)
         *reinterpret_cast<P*>(o + v * V) = scaled(*reinterpret_cast<const P*>(p + v * V));
     const int i = nvec * V + threadIdx.x;
-    if (i < len) Elem<T>::st(o + i, Elem<T>::ld(p + i) * c);
+    if (i < len) Elem<T>::st(o + i, times(Elem<T>::ld(p + i)));
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const GradTable& g, const Chunk& k, float c,
+                                            double wide) {
+    const T* p = static_cast<const T*>(g.in[k.t]) + k.i0;
+    T* o = static_cast<T*>(g.out[k.t]) + k.i0;
+    if (wide > 0.0) chunk_scale<T, true>(p, o, k.len, wide);
+    else chunk_scale<T, false>(p, o, k.len, c);
 }
 
 // out = g * (norm > max_norm ? max_norm / norm : 1), one rounding.  A norm
@@ -193,15 +206,12 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(GradTable g,
     const float v = norm_of(partial, np, sh);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     const float c = v > max_norm && v < INFINITY ? max_norm / v : 1.0f;
+    const double wide = c < FLT_MIN ? (double)max_norm / (double)v : 0.0;
     for (uint32_t q = blockIdx.x; q < g.first[g.n]; q += gridDim.x) {
         const Chunk k = chunk_of<true>(g, q);
         if (c == 1.0f && g.in[k.t] == g.out[k.t]) continue;
-        if (k.bf16)
-            chunk_scale(static_cast<const bf16_t*>(g.in[k.t]) + k.i0,
-                        static_cast<bf16_t*>(g.out[k.t]) + k.i0, k.len, c);
-        else
-            chunk_scale(static_cast<const float*>(g.in[k.t]) + k.i0,
-                        static_cast<float*>(g.out[k.t]) + k.i0, k.len, c);
+        if (k.bf16) chunk_scale<bf16_t>(g, k, c, wide);
+        else chunk_scale<float>(g, k, c, wide);
     }
 }
 

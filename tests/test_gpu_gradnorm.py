@@ -134,6 +134,25 @@ def test_values_whose_squares_leave_fp32(scale):
     check_clipped(out, ts, want, np.float64(np.float32(want / 7)))
 
 
+@pytest.mark.parametrize("mx", [3.0, 1e-3, 1e-6, 1e-20])
+def test_a_factor_below_the_normal_range_of_fp32(mx):
+    """max_norm / norm below 2^-126, where fp32 has few bits or none left while
+    the products are ordinary numbers: the same bound as for any factor."""
+    banner("gradnorm small factor", mx)
+    ts = [t * 1e35 for t in tensors([(F32, (901, 11)), (BF, (30077,)), (F32, (3,))], seed=31)]
+    ts[2].copy_(torch.tensor([3e38, -1e37, 1e30]))
+    want = exact_norm(ts)
+    assert want < 3.4e38 and mx / want < 2.0 ** -126
+    out = [torch.full_like(t, 7) for t in ts]
+    check_norm(M.moe_clip_grads(ts, mx, out), ts)
+    torch.cuda.synchronize()
+    assert abs(float(out[2][0]) / mx) > 0.5
+    check_clipped(out, ts, want, np.float64(np.float32(mx)))
+    M.moe_clip_grads(ts, mx)                                # in place: the same bits
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, o) for t, o in zip(ts, out))
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_norm_that_is_not_finite_scales_nothing(bad):
     banner("gradnorm not finite", bad)
