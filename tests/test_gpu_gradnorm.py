@@ -383,3 +383,62 @@ def test_a_layer_s_first_clip_on_a_side_stream(kind):
     side.synchronize()
     assert again.data_ptr() == norm.data_ptr()
     assert abs(float(norm[0]) / (want / 2) - 1) <= 2.0 ** -8 + 8 * U
+
+
+def test_lists_with_more_partial_sums_than_one_launch_has():
+    """700 tensors, some of many chunks: the norm in a launch of its own before
+    the scaling.  Norm and clipped values within the bounds, the same norm from
+    norm() and clip(), the same bits in place and replayed from a graph."""
+    banner("gradnorm long list")
+    spec = [((BF, F32)[i % 3 == 0], (17_001 + 97 * i if i % 5 else i // 5,)) for i in range(700)]
+    ts = tensors(spec, seed=33)
+    keep, want = [t.clone() for t in ts], exact_norm(ts)
+    out = [torch.full_like(t, 7) for t in ts]
+    c = M.GradClip(ts, out)
+    assert c.ws.numel() > 2 * 1024 * 8
+    n0 = c.norm().clone()
+    check_norm(n0, ts)
+    for mx in (want / 3, want * 3):
+        assert torch.equal(c.clip(mx), n0)
+        torch.cuda.synchronize()
+        check_clipped(out, ts, want, np.float64(np.float32(mx)))
+    c.clip(want / 3)
+    first = [o.clone() for o in out]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.clip(want / 3)
+    for _ in range(3):
+        c.result.fill_(-1)
+        for o in out:
+            o.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.result, n0) and all(torch.equal(a, b) for a, b in zip(out, first))
+    d = M.GradClip(ts)
+    assert torch.equal(d.clip(want / 3), n0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, o) for t, o in zip(ts, first))
+    for t, k in zip(ts, keep):
+        t.copy_(k)
+    ts[699].view(-1)[-1] = float("nan")                     # scales nothing
+    assert bool(torch.isnan(d.clip(1.0)[0]))
+    assert all(torch.equal(t, k) for t, k in zip(ts[:699], keep))
+
+
+def test_time_grows_with_the_list_and_not_with_its_square():
+    """Four times the tensors (1 MB each), in place under the limit: 4 times the
+    time, measured 4.0; 8.2 where every block added all partial sums.  Bound: 6."""
+    banner("gradnorm time of long lists")
+    flat = torch.zeros(5120 << 19, dtype=BF, device="cuda")
+    ts = list(flat.view(5120, 1 << 19))
+    took = {}
+    for n in (1280, 5120):
+        c = M.GradClip(ts[:n])
+        for rep in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            c.clip(1.0)
+            b.record()
+            b.synchronize()
+            took.setdefault(n, []).append(a.elapsed_time(b))
+    assert min(took[5120]) < 6 * min(took[1280]), took
