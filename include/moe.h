@@ -365,8 +365,9 @@ moe_status moe_gate_topk_bwd(const void *x, const void *Wg, const float *logits,
  *   overlap an input); logits [T,E] float, topk_idx [T,k] int32, topk_w [T,k]
  *   float: written when not NULL (in the workspace otherwise).
  *   ws: at least moe_layer_few_workspace_bytes(T,d,f,E,k,act,dt), 16-byte
- *   aligned, no initial content needed; calls that may overlap in time need a
- *   workspace each.
+ *   aligned, no initial content needed (the answer for T covers every smaller
+ *   T of the same layer too); calls that may overlap in time need a workspace
+ *   each.
  *   Limits: T <= 64 and k <= 64, d and f multiples of 64, E <= 1024;
  *   MOE_ERR_UNSUPPORTED for more tokens or slots (the workspace query gives 0).
  *   T = 0 launches nothing.

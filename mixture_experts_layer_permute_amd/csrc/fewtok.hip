@@ -24,6 +24,7 @@
 #include <float.h>
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -1025,7 +1026,10 @@ extern "C" {
 size_t moe_layer_few_workspace_bytes(int T, int d, int f, int E, int k, moe_act act,
                                      moe_dtype dt) {
     if (!few_sizes_ok(T, d, f, E, k, act, dt) || !few_limits_ok(T, k)) return 0;
-    return few_plan(T, d, f, E, k, act, dt).total;
+    // for every smaller step too: fewer tokens may cut the reduction into more chunks
+    size_t most = 0;
+    for (int t = 1; t <= T; ++t) most = std::max(most, few_plan(t, d, f, E, k, act, dt).total);
+    return most;
 }
 
 moe_status moe_layer_fwd_few(const void* x, const void* Wg, const float* logit_bias,

@@ -743,9 +743,6 @@ class FewTokenMoELayer:
         if T < 1 or nb == 0:
             raise MoEError("FewTokenMoELayer: 1 to 64 tokens, k <= 64, d and f multiples "
                            "of 64, 1 <= k <= E <= 1024")
-        # a smaller step may cut the reduction finer and need more workspace
-        nb = max(L.moe_layer_few_workspace_bytes(t, d, f, E, k, self.act, self.dt)
-                 for t in range(1, T + 1))
         e = lambda *s, dt=dtype: torch.empty(*s, dtype=dt, device=dev)
         self._y = e(T, d)
         self._logits = e(T, E, dt=torch.float32)

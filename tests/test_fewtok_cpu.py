@@ -69,6 +69,23 @@ def test_workspace(lib, mem):
         assert lib.moe_layer_few_workspace_bytes(*bad) == 0
 
 
+@pytest.mark.parametrize("layer", [(1024, 4096, 8, 2, 0, 1), (4096, 14336, 32, 8, 1, 1),
+                                   (1088, 1984, 12, 3, 1, 0), (64, 64, 4, 2, 0, 1),
+                                   (2048, 8192, 16, 2, 0, 1), (1024, 4096, 64, 2, 0, 0)])
+def test_the_workspace_of_a_step_covers_every_smaller_step(lib, mem, layer):
+    """A step of fewer tokens may be cut into more chunks; sized once for T, the
+    workspace holds them all: no smaller step is refused for it."""
+    need = [lib.moe_layer_few_workspace_bytes(T, *layer) for T in range(1, 65)]
+    assert need == sorted(need) and need[0] > 0
+    d, f, E, k, act, dt = layer
+    p = ctypes.addressof(mem) + (-ctypes.addressof(mem)) % 16
+    if not torch.cuda.is_available():              # the call's own check, before any launch
+        for T in range(1, 65):
+            got = call(lib, mem, T=T, d=d, f=f, E=E, k=k, act=act, dt=dt, W3=p if act else None,
+                       wsb=need[-1])
+            assert got in (_lib.MOE_ERR_HIP, UNS), T
+
+
 def test_no_tokens_is_a_no_op(lib, mem):
     assert call(lib, mem, T=0, x=None, y=None, ws=None, wsb=0) == 0
 
