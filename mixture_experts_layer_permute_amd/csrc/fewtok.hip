@@ -143,12 +143,8 @@ struct GateLds {
     float lg[64];
 };
 
-// Chunks in flight: eight take 0.3 us each, more than the latency of HBM,
-// where the registers of half a row's loads allow it.
-template <typename T, int EB>
-constexpr int gate_ahead() {
-    return EB * sizeof(T) <= 128 ? 8 : 4;
-}
+// Chunks in flight: eight take 0.3 us each, more than the latency of HBM.
+constexpr int kGateAhead = 8;
 
 typedef unsigned int u32x4_2_t __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -160,7 +156,8 @@ __device__ __forceinline__ void gate_block(GateLds& s, const T* __restrict__ x,
                                            const float* __restrict__ bias, int Tn, int d, int E,
                                            int e0, int t0, float* __restrict__ logits) {
 #pragma clang fp contract(off)
-    constexpr int TB = 64 / EB, NPF = gate_ahead<T, EB>();
+    constexpr int TB = 64 / EB, NPF = kGateAhead;
+    static_assert(EB * sizeof(T) <= 128, "half a gate row of each chunk is held in registers");
     constexpr int VE = 16 / sizeof(T);
     constexpr int WL = EB / 2 / VE;                   // loads of half a gate row
     constexpr int G = 32;                             // features read ahead
