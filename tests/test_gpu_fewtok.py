@@ -416,3 +416,63 @@ def test_tall_tiles_of_wide_strips(T, act, dt):
     err = (y.double() - want).abs()
     assert bool((err <= bound).all()), "off by %.2f of its bound" % float((err / bound).max())
     assert rel_err(host(y), want.cpu().numpy()) <= TOL[dt]
+
+
+def device_reference(x, W1, W2, W3, logits, idx, renorm, dt):
+    """y in 64 bits on the device from the choice idx, and the bound at the top."""
+    T, d = x.shape
+    f = W1.shape[2]
+    z = logits.double()
+    p = (z.gather(1, idx.long()) - (z.gather(1, idx.long()) if renorm else z)
+         .logsumexp(1, keepdim=True)).exp()
+    want = torch.zeros(T, d, dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(want)
+    for e in sorted(set(idx.flatten().tolist())):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        w, xe = p[t, j].unsqueeze(1), x[t].double()
+        W1e, W2e = W1[e].double(), W2[e].double()
+        H, dH = xe @ W1e, (d + 2) * U * (xe.abs() @ W1e.abs())
+        if W3 is not None:
+            W3e = W3[e].double()
+            H3, dH3 = xe @ W3e, (d + 2) * U * (xe.abs() @ W3e.abs())
+            sl = H * torch.sigmoid(H)
+            A, dA = sl * H3, 1.1 * dH * (H3.abs() + dH3) + sl.abs() * dH3
+        else:
+            A, dA = H * torch.special.ndtr(H), 1.13 * dH
+        dA = dA + 8 * U * A.abs()
+        dA = dA + (2.0 ** -16 if dt == "bf16" else 0.0) * (A.abs() + dA)
+        want.index_add_(0, t, w * (A @ W2e))
+        bound.index_add_(0, t, w * ((dA + (f + 128) * U * A.abs()) @ W2e.abs()))
+    return want, (bound + HALF[dt] * want.abs()) * 1.001 + 1e-30
+
+
+@pytest.mark.parametrize("width,T", [(w, T) for w, most in (
+    ("wide", 64), ("8 waves", 64), ("quarter", 16), ("with the gate", 4))
+    for T in (1, 2, 5, 16, 17, 32, 33, 64) if T <= most])
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_every_strip_width(width, T, act, dt):
+    """Sizes that give the up product each width it has, for one, two and four
+    tiles of rows: strips of 16 wide columns with 4 waves (bf16 128 columns,
+    fp32 64), 64 columns with 8 waves, 32 columns (up to 16 tokens), 64 columns
+    behind the gate in one launch (up to 4 tokens); the down product in both
+    widths.  Strips end inside the matrix, skewed routing leaves experts with
+    all tokens and with one."""
+    d, f, E, k = {"wide": (704, 2496, 24, 8), "8 waves": (320, 576, 24, 8),
+                  "quarter": (448, 128, 24, 8), "with the gate": (320, 320, 13, 3)}[width]
+    if width == "8 waves" and T < 5 and dt == "f32":
+        f = 960
+    banner("few widths", T, width, act, dt, d, f, E, k)
+    g = torch.Generator(device="cuda").manual_seed(1000 * T + f)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") * s[-2] ** -0.5).to(TDT[dt])
+    x, Wg, W1, W2 = r(T, d) * T ** 0.5, r(d, E), r(E, d, f), r(E, f, d)
+    W3 = r(E, d, f) if act == "swiglu" else None
+    bias = -1.5 * torch.log(torch.randperm(E, generator=g, device="cuda").float() + 1)
+    for renorm in (1, 0):
+        y, logits, idx, w = M.moe_layer_fwd_few(x, Wg, W1, W2, W3, k, act, bias, renorm)
+        gate = M.moe_gate_topk(x, Wg, k, bias, renorm)
+        assert torch.equal(logits, gate[0]) and torch.equal(idx, gate[1])
+        want, bound = device_reference(x, W1, W2, W3, logits, idx, renorm, dt)
+        err = (y.double() - want).abs()
+        assert bool((err <= bound).all()), "off by %.2f of its bound" % float((err / bound).max())
+        assert rel_err(host(y), want.cpu().numpy()) <= TOL[dt]
