@@ -382,6 +382,7 @@ __device__ __forceinline__ int expert_rows(const int32_t* __restrict__ idx, int 
     __syncthreads();
     for (int p = tid; p < pairs; p += nthr) {
         const int e = idx[p];
+        MOE_DASSERT((unsigned)e < (unsigned)E);
         if ((unsigned)e < (unsigned)E) atomicOr(&r.bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
@@ -409,6 +410,7 @@ __device__ __forceinline__ int expert_rows(const int32_t* __restrict__ idx, int 
                 cnt += __popcll(m);
                 before += __popcll(__ballot(ep < e));
             }
+        MOE_DASSERT(e < 0 || (cnt > 0 && cnt <= kFewTokens && before + cnt <= pairs));
         if (tid == 0) {
             r.res[0] = e;
             r.res[1] = min(cnt, kFewTokens);
@@ -645,6 +647,7 @@ __device__ __forceinline__ int block_expert(const FewArgs& p, const int32_t* idx
     const int slot = blockIdx.z;
     if (p.pairs == p.k) {
         const int e = idx[slot];
+        MOE_DASSERT((unsigned)e < (unsigned)p.E);
         // every wave writes the one row and reads what it wrote itself
         if ((threadIdx.x & 63) == 0) r.rows[0] = slot;
         __builtin_amdgcn_wave_barrier();
@@ -683,6 +686,7 @@ __device__ __forceinline__ void product_block(const FewArgs& p, int e, int n, in
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15;
+    MOE_DASSERT(n > 0 && n <= 16 * NTM && base >= 0 && base + n <= p.pairs);
     const T* We = static_cast<const T*>(DUAL && wv >= KW ? p.W3 : p.W) + (long)e * p.K * p.N;
     const int n0 = blockIdx.x * 16 * VW;
     // NT tiles of 16 rows per wave, depth steps of registers

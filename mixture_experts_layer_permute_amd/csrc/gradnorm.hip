@@ -71,6 +71,7 @@ __device__ __forceinline__ Chunk chunk_of(const GradTable& g, uint32_t c) {
     const uint64_t n = g.numel[lo] & ~kBf16Flag;
     const int per = kChunkBytes / (k.bf16 ? 2 : 4);
     k.i0 = (uint64_t)(BACK ? g.first[lo + 1] - 1 - c : c - g.first[lo]) * per;
+    MOE_DASSERT(g.first[lo] <= c && c < g.first[lo + 1] && k.i0 < n);
     k.len = (int)min((uint64_t)per, n - k.i0);
     return k;
 }

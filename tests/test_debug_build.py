@@ -55,3 +55,16 @@ def test_checks_only_in_the_debug_build(asm):
     for src, kernel in CHECKED.items():
         assert traps_in(asm[(src, True)], kernel) > 0, src
         assert traps_in(asm[(src, False)], kernel) == 0, src
+
+
+# the kernels of the few-token layer and of the gradient clipping
+CHECKED_TOO = {"fewtok.hip": ("few_product_kernel", "few_gate_up_kernel"),
+               "gradnorm.hip": ("grad_squares_kernel", "grad_scale_kernel")}
+
+
+def test_few_token_and_clipping_kernels_are_checked_in_the_debug_build(asm, tmp_path):
+    for src, kernels in CHECKED_TOO.items():
+        normal = device_asm(src, False, str(tmp_path))
+        for k in kernels:
+            assert traps_in(asm[(src, True)], k) > 0, k
+            assert traps_in(normal, k) == 0, k
