@@ -354,8 +354,10 @@ moe_status moe_gate_topk_bwd(const void *x, const void *Wg, const float *logits,
  * moe_layer_fwd_few -- the whole layer (gate, top-k, expert FFNs, weighted
  * sum) for a few tokens, forward only: one step of a serving loop.
  *   y[t,:] = sum_{j=0..k-1} topk_w[t,j] * FFN_{topk_idx[t,j]}(x[t,:])
- * with the logits of moe_gate_topk (the same bits) and its choice (a NaN logit
- * ranks below all others here), its gate weights (to fp32 rounding) and the FFN
+ * with the logits of moe_gate_topk (the same bits, for bf16 as far as each
+ * product x * Wg is zero or a normal fp32 number: every product is rounded here,
+ * where that gate may fuse it with its sum) and its choice (a NaN logit ranks
+ * below all others here), its gate weights (to fp32 rounding) and the FFN
  * of moe_expert_ffn_fwd (for bf16 the inner activation is kept to 16 significant
  * bits instead of 8; every sum in fp32, y rounded once).  Each expert that any
  * token chose is read once, whatever the number of tokens; experts no token
@@ -389,7 +391,8 @@ moe_status moe_layer_fwd_few(const void *x, const void *Wg,
  * moe_grad_norm, moe_clip_grads -- the global norm of a list of n gradient
  * tensors and the list scaled to a largest norm, for a training step between
  * the backward pass and the optimizer.
- *   norm   = sqrt(sum over all tensors of g^2), summed in fp64, rounded once
+ *   norm   = sqrt(sum over all tensors of g^2), summed in fp64 in a fixed
+ *            order, the root rounded to fp32
  *   out[i] = grads[i] * (norm > max_norm ? max_norm / norm : 1), factor and
  *            product in fp32 (in fp64 for a factor below 2^-126, rounded to
  *            fp32), a bf16 element then rounded to bf16

@@ -8,7 +8,8 @@
 //
 // Kernels of a call:
 //   few_gate     the gate's logits, one fixed-order fp32 chain per (token,
-//                expert): the same bits as moe_gate_topk; then top-k and gate
+//                expert): the bits of moe_gate_topk (bf16: while each product
+//                is zero or a normal fp32 number); then top-k and gate
 //                weights, one wave per token (few_topk, with many experts)
 //   few_up       per (expert hit, strip of columns): act(x W1[e]) (* x W3[e])
 //   few_down     per (expert hit, strip of columns, chunk of f): h W2[e], fp32
@@ -835,9 +836,10 @@ __global__ __launch_bounds__(512, 2) void few_gate_up_kernel(GateArgs g, FewArgs
 // y[t] = sum over a token's k slots and ks chunks of w[t,j] partial[s][t k + j],
 // rounded once.  A block takes 128 columns of one token; eight groups of 32
 // threads take every eighth (slot, chunk) each, and meet in LDS, in order.  It is
-// a launch and one round trip to memory long (3 to 4.5 us): in the down product
-// its sums would need a wait of blocks for each other, or atomics, whose order
-// changes bits.
+// a launch and one round trip to memory long (3 to 5 us).  The down product's last
+// block of a strip could take these sums over, in the same order, by a counter per
+// strip; whether making the partial sums visible to a block of another XCD costs
+// less than the launch is not measured.
 constexpr int kCombineCols = 128;
 template <typename T>
 __global__ __launch_bounds__(256) void few_combine_kernel(const float* __restrict__ partial,
@@ -899,7 +901,10 @@ FewPlan few_plan(int T, int d, int f, int E, int k, moe_act act, moe_dtype dt) {
     p.slots = min(E, pairs);
     const int wide = dt == MOE_BF16 ? 8 : 4;
     // Waves of a product over n columns, from the experts that T tokens hit
-    // when the gate prefers none.
+    // when the gate prefers none.  A skewed gate hits fewer, and then fewer waves
+    // run than are aimed at: the choice is not known when the launch is made (T 48,
+    // top-2 of 64 with popularity 1 / rank: 50 expected, 15 to 20 hit, and the down
+    // product runs 1920 waves).
     const double hit = E * (1.0 - pow(1.0 - (double)k / E, T));
     auto waves = [&](int n, int vw, int nw) { return cdiv(n, 16 * vw) * hit * nw; };
     // Strips of 16 wide columns and 4 waves stream best (bf16: 256-byte pieces

@@ -13,9 +13,10 @@
 // blocks take fixed chunks of the list, whatever tensor they lie in.
 //
 // Squares and sums are taken in fp64: the square of an fp32 value is exact
-// there, no gradient is too large or too small to be squared, and the norm is
-// the correctly rounded one whatever the order.  Partial sums are stored per
-// block and added in block order: no atomics, the same bits every time.
+// there and no gradient is too large or too small to be squared.  A sum of n
+// squares is off by at most n 2^-53 of itself, so the norm by that and half a step
+// of fp32.  Partial sums are stored per block and added in block order: no
+// atomics, the same bits every time.
 #include <float.h>
 #include <math.h>
 
@@ -196,8 +197,8 @@ __device__ __forceinline__ void chunk_scale(const GradTable& g, const Chunk& k, 
     else chunk_scale<T, false>(p, o, k.len, c);
 }
 
-// out = g * (norm > max_norm ? max_norm / norm : 1), one rounding.  A norm
-// that is not finite scales nothing: the step is the caller's to drop, and
+// out = g * (norm > max_norm ? max_norm / norm : 1), the product rounded to fp32
+// and a bf16 element then to bf16.  A norm that is not finite scales nothing: the step is the caller's to drop, and
 // zeros or NaN in place of the gradients would hide why.  In place a factor
 // of 1 leaves nothing to do.
 //

@@ -720,8 +720,10 @@ class FewTokenMoELayer:
     experts take the tokens the gate sends them, without padding).
 
     The weights are the tensors of MoELayer (bind() keeps them, it copies
-    nothing, so a training step's update is seen by the next forward); the
-    routing is MoELayer's bit for bit.  forward(x) takes up to T tokens and
+    nothing, so a training step's update in place is seen by the next forward;
+    a tensor given other memory, t.data = ..., needs bind() again); the routing
+    is MoELayer's bit for bit (bf16: while each product x * Wg is zero or a
+    normal float32 number).  forward(x) takes up to T tokens and
     returns y [n,d]; logits, topk_idx and topk_w are of the last forward.
     They and y are views of the layer's buffers, overwritten by the next
     forward: two steps in flight at once (two streams, two captured graphs)
