@@ -728,7 +728,7 @@ class FewTokenMoELayer:
     They and y are views of the layer's buffers, overwritten by the next
     forward: two steps in flight at once (two streams, two captured graphs)
     need a layer each.  stream: a HIP stream handle, the current stream if None;
-    x has to be ready on it.
+    x has to be ready on it, and to be kept until the step is done.
     """
 
     def __init__(self, T, d, f, E, k, act="gelu", dtype=torch.bfloat16, renorm=1,
