@@ -405,7 +405,7 @@ moe_status moe_layer_fwd_few(const void *x, const void *Wg,
  *   their element's alignment, no more.  out[i] is grads[i] (in place) or
  *   overlaps no tensor of the list, and no two out tensors overlap.
  *   max_norm: host pointer to one float >= 0 (infinity: never scaled), read
- *   during the call; norm: device pointer to one float.
+ *   during the call; norm: device pointer to one float outside the tensors.
  *   ws: at least moe_grad_norm_workspace_bytes(numel, dt, n), 8-byte aligned,
  *   no initial content needed; calls that may overlap in time need one each.
  *   n = 0: norm = 0.
