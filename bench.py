@@ -35,8 +35,8 @@ PEAK_HBM_GBS = 8000.0
 # and factors).  Valid only for the kernel sources whose code (comments and
 # blank lines aside, see source_hash) has the SHA-256 prefix TRAFFIC_SRC;
 # null once it changes.
-TRAFFIC_SRC = "0a2b78b8595eaa05"
-TRAFFIC_SOURCES = ("ggemm.hip", "common.h", "permute.hip", "combine.hip")
+TRAFFIC_SRC = "a73256e3e97712f7"
+TRAFFIC_SOURCES = ("ggemm.hip", "mfma_tile.h", "common.h", "permute.hip", "combine.hip")
 TRAFFIC = {
     # profiles/hbm_traffic_long_ctx_swiglu.md
     "long_ctx_swiglu": {
