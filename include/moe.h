@@ -424,6 +424,83 @@ moe_status moe_clip_grads(const void *const *grads, void *const *out,
                           size_t ws_bytes, hipStream_t stream);
 
 /*
+ * moe_head_xent, moe_head_xent_grad -- softmax cross entropy over a vocabulary
+ * head, for the step between the last layer's y and its dy: scores z = x Wv^T,
+ *   lse[t]  = ln sum_v exp z[t,v],  loss[t] = lse[t] - z[t, labels[t]]
+ * and with _grad the gradients of sum_t weight[t] * loss[t]:
+ *   dz[t,v] = weight[t] * (exp(z[t,v] - lse[t]) - [v == labels[t]])
+ *   dx = dz Wv, dWv = dz^T x
+ * The scores are never kept whole: the loss alone keeps a maximum and a sum per
+ * 128 of them, the gradient the scores of as many tokens at a time as the
+ * workspace holds.  A token whose label lies outside [0,V) (padding, a prompt)
+ * has no loss: loss, lse and its row of dx are 0, it adds nothing to dWv, and
+ * its row of x is not read.
+ *   x [T,d] dt, Wv [V,d] dt (row v scores entry v, the layout of an embedding
+ *   table, which it may be), labels [T] int32, weight [T] float or NULL (all
+ *   ones; the mean over n tokens is 1/n each), loss [T] float, lse [T] float or
+ *   NULL, dx [T,d] dt and dWv [V,d] dt (either may be NULL: not wanted; both
+ *   overwritten; they overlap neither each other nor x nor Wv).
+ * Sums are fp32; for bf16 dz is rounded to bf16 for its two products, and dx
+ * and dWv are rounded once.
+ *   ws: 16-byte aligned, no initial content needed; calls that may overlap in
+ *   time need one each.  moe_head_workspace_bytes gives the size for the
+ *   largest pieces of tokens that stay within `limit` bytes (0: 4 GiB), or the
+ *   smallest there is (pieces of 256 tokens) if none does; a call takes any size from
+ *   the smallest on and uses the largest pieces that fit, so more memory is
+ *   fewer pieces.  The answer for T covers every smaller T of the
+ *   same head.  grad: whether for _grad; K: the teacher's slots (below; 0 here).
+ *   Limits: T <= 2^24, V <= 2^20, d a multiple of 64 up to 65536.  T = 0:
+ *   dWv = 0, nothing else is touched.
+ * Sources: "Flattening Every Memory Peak in Long-Context MoE Training",
+ * English abstract (tensors that grow with the tokens are taken in chunks;
+ * loss and gradients stay exact).
+ */
+size_t moe_head_workspace_bytes(int T, int d, int V, int K, moe_dtype dt, int grad,
+                                size_t limit);
+moe_status moe_head_xent(const void *x, const void *Wv, const int32_t *labels,
+                         int T, int d, int V, moe_dtype dt, float *loss,
+                         float *lse, void *ws, size_t ws_bytes,
+                         hipStream_t stream);
+moe_status moe_head_xent_grad(const void *x, const void *Wv,
+                              const int32_t *labels, const float *weight, int T,
+                              int d, int V, moe_dtype dt, float *loss,
+                              float *lse, void *dx, void *dWv, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_head_distill, moe_head_distill_grad -- the divergence of the head's
+ * distribution from a teacher of which K scores a token are kept (its largest,
+ * usually), at the temperature tau:
+ *   q[t,:] = softmax over the token's slots of t_score[t,j] / tau
+ *   kd[t]  = tau^2 sum_j q[t,j] (ln q[t,j] - ln p[t, t_idx[t,j]]),
+ *            p[t,:] = softmax over the whole vocabulary of z[t,:] / tau
+ *   dz[t,v] = t_weight[t] * tau * (p[t,v] - sum_{j: t_idx[t,j] = v} q[t,j])
+ * With labels (else NULL) the cross entropy of the same scores beside it (loss
+ * and lse as above): _grad then gives the gradients of sum_t t_weight[t] *
+ * kd[t] + weight[t] * loss[t], for one set of products.
+ *   t_idx [T,K] int32: a slot outside [0,V) is left out (a teacher that kept
+ *   fewer), as is one whose score is -infinity; a token with no slot has kd 0;
+ *   an entry named by two slots has both.  t_score [T,K] float; K from 1 to
+ *   256; tau: host pointer to one float from 0.001 to 1000, read during the
+ *   call; t_weight [T] float or NULL (all ones); kd [T] float; loss and lse are
+ *   written with labels only.  A token with neither label nor slot is left out as
+ *   above.  Everything else as for moe_head_xent_grad.
+ */
+moe_status moe_head_distill(const void *x, const void *Wv,
+                            const int32_t *t_idx, const float *t_score, int K,
+                            const float *tau, const int32_t *labels, int T,
+                            int d, int V, moe_dtype dt, float *kd, float *loss,
+                            float *lse, void *ws, size_t ws_bytes,
+                            hipStream_t stream);
+moe_status moe_head_distill_grad(const void *x, const void *Wv,
+                                 const int32_t *t_idx, const float *t_score,
+                                 const float *t_weight, int K, const float *tau,
+                                 const int32_t *labels, const float *weight,
+                                 int T, int d, int V, moe_dtype dt, float *kd,
+                                 float *loss, float *lse, void *dx, void *dWv,
+                                 void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * Kernel timing (benchmark support, off by default).
  * moe_profile_enable(capacity) creates 2*capacity HIP events; from then on
  * every kernel the library launches is bracketed by two of them on its

@@ -15,7 +15,9 @@ from .ops import (moe_combine, moe_combine_bwd, moe_expert_ffn_bwd,  # noqa: F40
                   moe_expert_ffn_fwd_noalloc,
                   moe_expert_ffn_bwd_gather, moe_gate_topk, moe_gate_topk_bwd,
                   moe_layer_fwd_few, moe_grad_norm, moe_clip_grads, GradClip,
+                  moe_head_xent, moe_head_xent_grad, moe_head_distill,
+                  moe_head_distill_grad,
                   moe_permute, moe_unpermute_grad, moe_init,
                   moe_set_overlap)
-from .layer import (ChunkedMoELayer, FewTokenMoELayer, MoELayer,  # noqa: F401
-                    OffloadedMoELayer)
+from .layer import (ChunkedMoELayer, FewTokenMoELayer, HeadLoss,  # noqa: F401
+                    MoELayer, OffloadedMoELayer)

@@ -50,6 +50,13 @@ SIGNATURES = {
     "moe_grad_norm_workspace_bytes": (_Z, [_P, _P, _I]),
     "moe_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, _Z, _P]),
     "moe_clip_grads": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _Z, _P]),
+    "moe_head_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I, _Z]),
+    "moe_head_xent": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
+    "moe_head_xent_grad": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_head_distill": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _Z,
+                              _P]),
+    "moe_head_distill_grad": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P,
+                                   _P, _P, _P, _P, _Z, _P]),
     "moe_mfma_loop": (_I, [_I, _I, _P, _Z, _P]),
     "moe_mfma_loop_random": (_I, [_I, _I, _P, _Z, _P]),
     "moe_lds_probe": (_I, [_I, _I, _I, _P, _Z, _P, _Z, _P]),

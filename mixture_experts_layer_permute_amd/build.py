@@ -15,7 +15,7 @@ DEBUG_OUT = os.path.join(HERE, "libmoe_debug_bounds.so")
 DEBUG_FLAGS = ["-DMOE_DEBUG_BOUNDS"]
 
 SOURCES = ["abi.hip", "gate.hip", "permute.hip", "combine.hip", "ggemm.hip", "fewtok.hip",
-           "gradnorm.hip"]
+           "gradnorm.hip", "head.hip"]
 # per-file extra flags: the gate's fp32 logits must not fuse multiply-adds
 EXTRA = {"gate.hip": ["-ffp-contract=off"]}
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

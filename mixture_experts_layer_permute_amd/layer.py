@@ -5,12 +5,13 @@ forward:  moe_gate_topk -> moe_permute -> moe_expert_ffn_fwd -> moe_combine
 backward: moe_combine_bwd -> (moe_gate_topk_bwd on a second stream, writes
           dx) and moe_expert_ffn_bwd -> moe_unpermute_grad (adds to dx)
 """
+import ctypes
 import math
 
 import torch
 
 from ._lib import MOE_ACT_GELU, MOE_ACT_SWIGLU, MOE_BF16, MOE_F32, check, load
-from .ops import GradClip, MoEError, _act, _dt, _few_check, _stream
+from .ops import GradClip, MoEError, _act, _dt, _few_check, _head_check, _head_out, _stream
 
 
 def _torch_stream(handle, device):
@@ -793,3 +794,123 @@ class FewTokenMoELayer:
         check(self.lib.moe_layer_fwd_few(x.data_ptr(), *self._weights, n, *self._rest, s),
               "moe_layer_fwd_few")
         return self.y
+
+
+class HeadLoss:
+    """The loss of a training step over a vocabulary head, every buffer
+    allocated once: cross entropy with a label a token (moe_head_xent), the
+    divergence from a teacher's K top scores (moe_head_distill), or both of the
+    same scores, alone (forward) or with the gradients (step).
+
+    Stands between a layer's y and its dy:
+        head = HeadLoss(T, d, V).bind(Wv, dx=dy)     # dy: the layer's, from bind
+        layer.forward()
+        head.step(layer.y, labels, weight)           # loss, and dy for the layer
+        layer.backward()
+        GradClip(layer.weight_grads() + head.weight_grads()) ...
+
+    bind() keeps the head Wv [V,d] (it copies nothing; a tensor given other
+    memory needs bind() again), and the buffers for the gradients if the caller
+    has some (dx=..., dWv=...; False: that gradient is not wanted).
+    forward and step take up to T tokens and return loss [n] (kd [n] without
+    labels); loss, lse, kd and dx are views of the layer's buffers for the last
+    call, which like dWv the next call overwrites: two calls in flight at once
+    need a HeadLoss each.  stream: a HIP stream handle, the current stream if None; the
+    tensors have to be ready on it, and to be kept until the call is done.
+    limit: the workspace's size in bytes to stay within if possible (None: 4 GiB);
+    a larger one takes more tokens at a time.
+    """
+
+    def __init__(self, T, d, V, dtype=torch.bfloat16, K=0, tau=1.0, grad=True, device="cuda",
+                 limit=None):
+        self.T, self.d, self.V, self.K, self.tau = T, d, V, K, float(tau)
+        self.dtype = dtype
+        self.dt = _dt(torch.empty(0, dtype=dtype))
+        self.grad = bool(grad)
+        self.device = torch.device(device)
+        L = self.lib = load()
+        nb = L.moe_head_workspace_bytes(T, d, V, K, self.dt, int(self.grad), int(limit or 0))
+        if T < 1 or nb == 0:
+            raise MoEError("HeadLoss: 1 to 2^24 tokens, d a multiple of 64 up to 65536, "
+                           "1 to 2^20 entries, at most 256 teacher slots")
+        if not 1e-3 <= self.tau <= 1e3:
+            raise MoEError("HeadLoss: tau from 0.001 to 1000")
+        e = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device=self.device)
+        self._loss, self._lse = e(T), e(T)
+        self._kd = e(T) if K else None
+        self._dx = self.dWv = self.Wv = None
+        self.ws = e(nb, dt=torch.uint8)
+        self._index = self.ws.device.index
+        self._tau = ctypes.c_float(self.tau)
+
+    def bind(self, Wv, dx=None, dWv=None):
+        """Remember the head [V,d] (device, contiguous, the loss's dtype) and the
+        buffers for the gradients (made here if None, left out if False)."""
+        if (tuple(Wv.shape) != (self.V, self.d) or Wv.dtype != self.dtype
+                or Wv.device != self.ws.device or not Wv.is_contiguous()):
+            raise MoEError("HeadLoss: Wv [%d,%d], contiguous, of the loss's dtype and device"
+                           % (self.V, self.d))
+        if not self.grad and (dx is not None or dWv is not None):
+            raise MoEError("HeadLoss: made without gradients")
+        if dx is False and dWv is False:
+            raise MoEError("HeadLoss: one gradient at least, or grad=False")
+        self.Wv = Wv
+        if self.grad:
+            dev = self.ws.device
+            self._dx = None if dx is False else _head_out(dx, (self.T, self.d), self.dtype, dev,
+                                                          "dx")
+            self.dWv = None if dWv is False else _head_out(dWv, (self.V, self.d), self.dtype, dev,
+                                                           "dWv")
+        return self
+
+    def _call(self, x, labels, weight, teacher, grad, stream):
+        if self.Wv is None:
+            raise MoEError("HeadLoss: bind() the head first")
+        if grad and not self.grad:
+            raise MoEError("HeadLoss: made without gradients")
+        n, _, _, K, idx, score, tweight = _head_check(x, self.Wv, labels, weight, teacher, grad)
+        if n > self.T:
+            raise MoEError("HeadLoss: x [n,%d], n <= %d" % (self.d, self.T))
+        if K > self.K:
+            raise MoEError("HeadLoss: made for %d teacher slots" % self.K)
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._call(x, labels, weight, teacher, grad, stream)
+        s = _stream(self._index) if stream is None else stream
+        p = lambda t: None if t is None else t.data_ptr()
+        self.loss = self._loss[:n] if labels is not None else None
+        self.lse = self._lse[:n] if labels is not None else None
+        self.kd = self._kd[:n] if K else None
+        self.dx = self._dx[:n] if grad and self._dx is not None else None
+        size = (n, self.d, self.V, self.dt)
+        end = (p(self.ws), self.ws.numel(), s)
+        L, out = self.lib, (p(self.loss), p(self.lse))
+        g = (p(self.dx), p(self.dWv)) if grad else ()
+        if K:
+            t = (p(idx), p(score)) + ((p(tweight),) if grad else ()) + \
+                (K, ctypes.byref(self._tau), p(labels)) + ((p(weight),) if grad else ())
+            fn = L.moe_head_distill_grad if grad else L.moe_head_distill
+            check(fn(p(x), p(self.Wv), *t, *size, p(self.kd), *out, *g, *end),
+                  "moe_head_distill_grad" if grad else "moe_head_distill")
+        else:
+            t = (p(labels),) + ((p(weight),) if grad else ())
+            fn = L.moe_head_xent_grad if grad else L.moe_head_xent
+            check(fn(p(x), p(self.Wv), *t, *size, *out, *g, *end),
+                  "moe_head_xent_grad" if grad else "moe_head_xent")
+        return self.loss if labels is not None else self.kd
+
+    def forward(self, x, labels=None, teacher=None, stream=None):
+        """x [n,d], labels [n] i32 and/or teacher (indices [n,K] i32, scores [n,K]
+        f32) -> loss [n] (kd [n] without labels)."""
+        if teacher is not None:
+            teacher = tuple(teacher)[:2]                   # its weight is the gradient's
+        return self._call(x, labels, None, teacher, False, stream)
+
+    def step(self, x, labels=None, weight=None, teacher=None, stream=None):
+        """forward, and the gradients of sum_t weight[t] loss[t] + u[t] kd[t]: dx and
+        dWv (weight [n] f32, None: ones; u the teacher's third tensor likewise)."""
+        return self._call(x, labels, weight, teacher, True, stream)
+
+    def weight_grads(self):
+        """The head's gradient of the last step, as a list."""
+        return [] if self.dWv is None else [self.dWv]

@@ -434,3 +434,123 @@ def moe_clip_grads(grads, max_norm, out=None):
     """Scales a list of gradients to the norm max_norm if theirs is larger (in
     place, or into out) -> the norm before, [1] float32."""
     return GradClip(grads, out).clip(max_norm)
+
+
+def _head_check(x, Wv, labels, weight, teacher, grad):
+    """Shapes, types and devices of a head call -> (T, d, V, K, labels, idx, score,
+    teacher's weight)."""
+    idx, score, tweight = (tuple(teacher) + (None,))[:3] if teacher is not None else (None,) * 3
+    _need_gpu(x, Wv, labels, weight, idx, score, tweight)
+    if x.dim() != 2 or Wv.dim() != 2 or x.shape[1] != Wv.shape[1]:
+        raise MoEError("x [T,d] and Wv [V,d] expected")
+    _dt(x)
+    T, d = x.shape
+    if Wv.dtype != x.dtype:
+        raise MoEError("x and Wv need one dtype")
+    K = 0
+    if teacher is not None:
+        if idx is None or score is None or idx.dim() != 2 or idx.shape[1] < 1:
+            raise MoEError("teacher: (indices [T,K], scores [T,K][, weight [T]])")
+        K = idx.shape[1]
+    elif labels is None:
+        raise MoEError("labels or a teacher needed")
+    if not grad and (weight is not None or tweight is not None):
+        raise MoEError("weights go with the gradient")
+    if weight is not None and labels is None:
+        raise MoEError("weight goes with labels")
+    for t, shape, dt, name in ((labels, (T,), torch.int32, "labels: int32 [T]"),
+                               (weight, (T,), torch.float32, "weight: float32 [T]"),
+                               (idx, (T, K), torch.int32, "teacher indices: int32 [T,K]"),
+                               (score, (T, K), torch.float32, "teacher scores: float32 [T,K]"),
+                               (tweight, (T,), torch.float32, "teacher weight: float32 [T]")):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dt):
+            raise MoEError(name + " expected")
+    if any(t is not None and t.device != x.device
+           for t in (Wv, labels, weight, idx, score, tweight)):
+        raise MoEError("all tensors of a head on one device")
+    return T, d, Wv.shape[0], K, idx, score, tweight
+
+
+def _head_out(t, shape, dt, dev, name):
+    if t is None:
+        return torch.empty(shape, dtype=dt, device=dev)
+    if (tuple(t.shape) != tuple(shape) or t.dtype != dt or t.device != dev
+            or not t.is_contiguous()):
+        raise MoEError("out: %s %s, contiguous, %s, on the inputs' device"
+                       % (name, list(shape), dt))
+    return t
+
+
+def _head(x, Wv, labels, weight, teacher, tau, grad, out, ws, limit):
+    T, d, V, K, idx, score, tweight = _head_check(x, Wv, labels, weight, teacher, grad)
+    dev, f32 = x.device, torch.float32
+    out = dict(out or {})
+    known = (["loss", "lse"] if labels is not None else []) + (["kd"] if K else []) + \
+        (["dx", "dWv"] if grad else [])
+    if set(out) - set(known):
+        raise MoEError("out: %s expected" % ", ".join(known))
+    res = {}
+    for name in known:
+        if name in ("dx", "dWv"):
+            if name in out and out[name] is None:          # not wanted
+                res[name] = None
+                continue
+            res[name] = _head_out(out.get(name), (x if name == "dx" else Wv).shape, x.dtype, dev,
+                                  name)
+        else:
+            res[name] = _head_out(out.get(name), (T,), f32, dev, name)
+    L = load()
+    if ws is None:
+        ws = _ws(L.moe_head_workspace_bytes(T, d, V, K, _dt(x), int(grad), limit), dev)
+    elif ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise MoEError("ws: contiguous uint8 on the inputs' device")
+    loss, lse = _p(res.get("loss")), _p(res.get("lse"))
+    tail = (T, d, V, _dt(x))
+    end = (_p(ws), ws.numel())
+    t = ctypes.byref(ctypes.c_float(tau))
+    with torch.cuda.device(dev):
+        s = _stream(dev)
+        if K and grad:
+            check(L.moe_head_distill_grad(_p(x), _p(Wv), _p(idx), _p(score), _p(tweight), K, t,
+                                          _p(labels), _p(weight), *tail, _p(res["kd"]), loss, lse,
+                                          _p(res["dx"]), _p(res["dWv"]), *end, s),
+                  "moe_head_distill_grad")
+        elif K:
+            check(L.moe_head_distill(_p(x), _p(Wv), _p(idx), _p(score), K, t, _p(labels), *tail,
+                                     _p(res["kd"]), loss, lse, *end, s), "moe_head_distill")
+        elif grad:
+            check(L.moe_head_xent_grad(_p(x), _p(Wv), _p(labels), _p(weight), *tail, loss, lse,
+                                       _p(res["dx"]), _p(res["dWv"]), *end, s),
+                  "moe_head_xent_grad")
+        else:
+            check(L.moe_head_xent(_p(x), _p(Wv), _p(labels), *tail, loss, lse, *end, s),
+                  "moe_head_xent")
+    return res
+
+
+def moe_head_xent(x, Wv, labels, out=None, ws=None, limit=0):
+    """Cross entropy of the scores x Wv^T with a label a token (outside [0,V):
+    none, loss and lse 0) -> {"loss" [T] f32, "lse" [T] f32}."""
+    return _head(x, Wv, labels, None, None, 1.0, False, out, ws, limit)
+
+
+def moe_head_xent_grad(x, Wv, labels, weight=None, out=None, ws=None, limit=0):
+    """moe_head_xent and the gradients of sum_t weight[t] loss[t] (weight [T]
+    f32, None: ones) -> {"loss", "lse", "dx" [T,d], "dWv" [V,d]}.  out: buffers by
+    those names; None for dx or dWv leaves that gradient out."""
+    return _head(x, Wv, labels, weight, None, 1.0, True, out, ws, limit)
+
+
+def moe_head_distill(x, Wv, teacher, tau=1.0, labels=None, out=None, ws=None, limit=0):
+    """The divergence from a teacher's top scores: teacher = (indices [T,K] i32,
+    outside [0,V): no slot; scores [T,K] f32) -> {"kd" [T] f32}, with labels
+    {"loss", "lse"} of the same scores too."""
+    return _head(x, Wv, labels, None, teacher, tau, False, out, ws, limit)
+
+
+def moe_head_distill_grad(x, Wv, teacher, tau=1.0, labels=None, weight=None, out=None, ws=None,
+                          limit=0):
+    """moe_head_distill and the gradients of sum_t u[t] kd[t] + weight[t] loss[t],
+    u the teacher's third tensor ([T] f32, left out: ones)
+    -> {"kd", "dx" [T,d], "dWv" [V,d]} and with labels {"loss", "lse"}."""
+    return _head(x, Wv, labels, weight, teacher, tau, True, out, ws, limit)
