@@ -27,6 +27,7 @@
 // Roundings (bf16): dz is rounded once to bf16 as an operand of the matrix
 // cores; every sum is fp32; dx and dWv are rounded once.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "mfma_tile.h"
@@ -35,6 +36,9 @@ namespace moe {
 namespace {
 
 constexpr int kMaxK = 256;              // teacher slots of a token
+#ifndef HEAD_BK
+#define HEAD_BK 64
+#endif
 constexpr int kRowAlign = 256;          // tokens of a piece: whole row tiles
 
 // A wave's lane reads and writes ordered as written: the reads before it have
@@ -77,6 +81,15 @@ __device__ __forceinline__ float wave_sum(float v) {
     v = group_sum<16>(v);
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
+}
+
+// f(0), f(1), ... f(N - 1) with constants.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void unroll(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<N, I + 1>(f);
+    }
 }
 
 // ------------------------------------------------------- tokens with a loss
@@ -218,50 +231,47 @@ __device__ __forceinline__ HeadTile head_tile(const HeadGemm<T>& p) {
     return t;
 }
 
-// Epilogue: each wave stages 16-row slabs of its accumulators (32 x 32
-// fragments of the matrix instructions: column = lane % 32, row by register
-// and lane / 32) in its own part of LDS and hands rows of 8 neighbouring
-// columns to epi.row8(tile, row, col, v).  Every lane takes part in every
-// call; rows and columns past the tile are up to the functor.
-template <int WTM, int WTN, int FM, int FN, class Epi>
-__device__ __forceinline__ void head_epilogue(float* slab, const HeadTile& ti, int wr, int wc,
-                                              const f32x16 (&acc)[FM][FN], const Epi& epi) {
-    constexpr int LDW = WTN + 4;
-    constexpr int LPR = WTN / 8;                   // lanes of a row
-    constexpr int RPP = 64 / LPR;
-    const int lane = threadIdx.x & 63;
-    const int c0 = (lane % LPR) * 8;
-#pragma unroll
-    for (int q = 0; q < 2 * FM; ++q) {
-        const int i = q >> 1, h = q & 1;
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int vv = 0; vv < 8; ++vv) {
-                const int r = (vv >> 2) * 8 + (lane >> 5) * 4 + (vv & 3);
-                slab[r * LDW + j * 32 + (lane & 31)] = acc[i][j][h * 8 + vv];
-            }
-        wave_lds_sync();
-#pragma unroll 1
-        for (int ps = 0; ps < 16 / RPP; ++ps) {
-            const int rl = ps * RPP + lane / LPR;
-            const float* src = &slab[rl * LDW + c0];
-            float v[8];
-            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-            *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(src + 4);
-            epi.template row8<LPR>(ti, wr + i * 32 + h * 16 + rl, wc + c0, v);
-        }
-        wave_lds_sync();
+// Epilogues.  The products are made with the operands swapped, so that a lane's
+// four accumulators of a fragment are four neighbouring columns of one row: the
+// wave hands over row by row (rl: this lane's row in the tile), with the lane's
+// quads v[q] at the columns Lanes::col(q) from cl on.  No LDS, no barrier.
+//  Quads16: 16 x 16 fragments, 8 quads of 128 columns, 4 lanes (16 apart) a row;
+//  Quads32: 32 x 32 fragments, 8 quads of 64 columns, 2 lanes (32 apart) a row.
+struct Quads16 {
+    static constexpr int WIDTH = 128;
+    static __device__ __forceinline__ int col(int q) { return q * 16 + ((threadIdx.x >> 4) & 3) * 4; }
+    static __device__ __forceinline__ bool first() { return (threadIdx.x & 48) == 0; }
+    static __device__ __forceinline__ float max(float v) {
+        v = fmaxf(v, __shfl_xor(v, 16));
+        return fmaxf(v, __shfl_xor(v, 32));
     }
-}
+    static __device__ __forceinline__ float sum(float v) {
+        v += __shfl_xor(v, 16);
+        return v + __shfl_xor(v, 32);
+    }
+};
+struct Quads32 {
+    static constexpr int WIDTH = 64;
+    static __device__ __forceinline__ int col(int q) {
+        return (q >> 2) * 32 + (q & 3) * 8 + ((threadIdx.x >> 5) & 1) * 4;
+    }
+    static __device__ __forceinline__ bool first() { return (threadIdx.x & 32) == 0; }
+    static __device__ __forceinline__ float max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+    static __device__ __forceinline__ float sum(float v) { return v + __shfl_xor(v, 32); }
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
 
 // Scores: per row and 128 (64 in fp32) columns the maximum m and the sums of
 // exp(z - m) and exp((z - m) / tau); the label's score; z itself if kept.
+// exp(z - m) = 2^(z L - m'), L = log2 e, m' = m L rounded: one fused multiply-add
+// before the hardware's 2^x, the same m' wherever the sum is used.
 struct EpiScores {
     int V;
     float2* stat;            // [parts][ldr] (m, sum)
     float* tstat;            // [parts][ldr] sum at the temperature, or NULL
-    float inv_tau;
+    float l2t;               // L / tau
     long ldr;
     const int32_t* labels;   // or NULL
     const int32_t* rows;     // compacted row -> token, or NULL: the row itself
@@ -270,47 +280,61 @@ struct EpiScores {
     float* Z;                // or NULL
     long ldz;                // a multiple of 64
 
-    template <int LPR>
-    __device__ __forceinline__ void row8(const HeadTile& ti, int rl, int cl,
-                                         const float* v) const {
+    template <class Lanes>
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
+                                        f32x4 (&v)[8]) const {
         const int col = ti.n0 + cl;
         const bool in = rl < ti.rows;
         const long r = (long)ti.m0 + rl;
-        float m = -INFINITY;
+        if (Z && in) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) m = fmaxf(m, col + q < V ? v[q] : -INFINITY);
-        m = group_max<LPR>(m);
-        const float ref = m == -INFINITY ? 0.0f : m;   // no column here, or none finite
-        float s = 0.0f, st = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s += col + q < V ? expf(v[q] - ref) : 0.0f;
-        s = group_sum<LPR>(s);
-        if (tstat) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) st += col + q < V ? expf((v[q] - ref) * inv_tau) : 0.0f;
-            st = group_sum<LPR>(st);
-        }
-        if (!in) return;
-        if ((threadIdx.x & (LPR - 1)) == 0) {
-            const long at = (long)(col / (LPR * 8)) * ldr + r;
-            stat[at] = make_float2(m, s);
-            if (tstat) tstat[at] = st;
-        }
-        if (labels) {
-            const int t = rows ? rows[p0 + r] : (int)r;
-            const int y = labels[t] - col;
-            if ((unsigned)y < 8u && col + y < V) {
-                uint32_t z = 0;                    // (not an indexed read: v stays in registers)
-#pragma unroll
-                for (int q = 0; q < 8; ++q) z |= y == q ? __float_as_uint(v[q]) : 0u;
-                zl[r] = __uint_as_float(z);
+            for (int q = 0; q < 8; ++q) {
+                const int c = col + Lanes::col(q);
+                if (c < ldz) *reinterpret_cast<f32x4*>(Z + r * ldz + c) = v[q];
             }
         }
-        if (Z && col < ldz) {
-            float4* q = reinterpret_cast<float4*>(Z + r * ldz + col);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (labels && in) {
+            const int y = labels[rows ? rows[p0 + r] : (int)r] - col;
+            if ((unsigned)y < (unsigned)Lanes::WIDTH && col + y < V) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (y == Lanes::col(q) + u) zl[r] = v[q][u];
+            }
         }
+        if (col + Lanes::WIDTH > V) {                  // the vocabulary's end
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (col + Lanes::col(q) + u >= V) v[q][u] = -INFINITY;
+        }
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            m = fmaxf(fmaxf(m, fmaxf(v[q][0], v[q][1])), fmaxf(v[q][2], v[q][3]));
+        m = Lanes::max(m);
+        const float ref = m == -INFINITY ? 0.0f : m;   // no column here, or none finite
+        const float m2 = ref * kLog2e;
+        float s = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s += exp2_hw(fmaf(v[q][u], kLog2e, -m2));
+        s = Lanes::sum(s);
+        const long at = (long)(col / Lanes::WIDTH) * ldr + r;
+        if (tstat) {
+            const float mt = ref * l2t;
+            float t = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) t += exp2_hw(fmaf(v[q][u], l2t, -mt));
+            t = Lanes::sum(t);
+            if (in && Lanes::first()) tstat[at] = t;
+        }
+        if (in && Lanes::first()) stat[at] = make_float2(m, s);
     }
 };
 
@@ -325,6 +349,38 @@ __device__ __forceinline__ void ld8(const T* p, float* v) {
     if constexpr (sizeof(T) == 4) Vec16<T>::ld(p + 4, v + 4);
 }
 
+// A row's quads to out (row start): bf16 ones in 16-byte stores, two lanes 16
+// apart trading halves of two neighbouring fragments.
+template <class Lanes, typename T>
+__device__ __forceinline__ void store_row(T* out, bool in, int cl, int cols, const f32x4 (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int c = cl + Lanes::col(q);
+            if (in && c < cols) *reinterpret_cast<f32x4*>(out + c) = v[q];
+        }
+    } else {
+        // after the swap of X's odd 16-lane rows with Y's even ones a lane of an
+        // even row holds 8 columns of fragment q, of an odd one of fragment q + 1
+        const int g = (threadIdx.x >> 4) & 3;
+        const int c0 = cl + (g & 1) * 16 + (g >> 1) * 8;
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+            u32x4_t w;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const auto sw = __builtin_amdgcn_permlane16_swap(
+                    pack_bf16x2(v[q][2 * u], v[q][2 * u + 1]),
+                    pack_bf16x2(v[q + 1][2 * u], v[q + 1][2 * u + 1]), false, false);
+                w[u] = sw[0];
+                w[2 + u] = sw[1];
+            }
+            const int c = c0 + q * 16;
+            if (in && c < cols) *reinterpret_cast<u32x4_t*>(out + c) = w;
+        }
+    }
+}
+
 // dx rows, back at their tokens.
 template <typename T>
 struct EpiRows {
@@ -332,11 +388,12 @@ struct EpiRows {
     long ldo;
     const int32_t* rows;
     int p0;
-    template <int LPR>
-    __device__ __forceinline__ void row8(const HeadTile& ti, int rl, int cl,
-                                         const float* v) const {
-        if (rl < ti.rows && cl < ti.cols)
-            st8(out + (long)rows[p0 + ti.m0 + rl] * ldo + ti.n0 + cl, v);
+    template <class Lanes>
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
+                                        const f32x4 (&v)[8]) const {
+        const bool in = rl < ti.rows;
+        store_row<Lanes>(out + (in ? (long)rows[p0 + ti.m0 + rl] : 0) * ldo + ti.n0, in, cl,
+                         ti.cols, v);
     }
 };
 
@@ -344,11 +401,11 @@ struct EpiRows {
 struct EpiPart {
     float* part;
     long ldo, stride;
-    template <int LPR>
-    __device__ __forceinline__ void row8(const HeadTile& ti, int rl, int cl,
-                                         const float* v) const {
-        if (rl < ti.rows && cl < ti.cols)
-            st8(part + ti.split * stride + (long)(ti.m0 + rl) * ldo + ti.n0 + cl, v);
+    template <class Lanes>
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
+                                        const f32x4 (&v)[8]) const {
+        store_row<Lanes>(part + ti.split * stride + (long)(ti.m0 + rl) * ldo + ti.n0,
+                         rl < ti.rows, cl, ti.cols, v);
     }
 };
 
@@ -360,18 +417,20 @@ struct EpiSum {
     long ldo;
     const int32_t* count;
     int p0, piece;
-    template <int LPR>
-    __device__ __forceinline__ void row8(const HeadTile& ti, int rl, int cl, float* v) const {
-        if (rl >= ti.rows || cl >= ti.cols) return;
-        const long at = (long)(ti.m0 + rl) * ldo + ti.n0 + cl;
+    template <class Lanes>
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
+                                        f32x4 (&v)[8]) const {
+        const bool in = rl < ti.rows;
+        const long at = (long)(ti.m0 + rl) * ldo + ti.n0;
         if (p0 > 0) {
-            float a[8];
-            ld8(acc + at, a);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += a[q];
+            for (int q = 0; q < 8; ++q) {
+                const int c = cl + Lanes::col(q);
+                if (in && c < ti.cols) v[q] += *reinterpret_cast<const f32x4*>(acc + at + c);
+            }
         }
-        if (*count <= p0 + piece) st8(out + at, v);
-        else st8(acc + at, v);
+        if (*count <= p0 + piece) store_row<Lanes>(out + at, in, cl, ti.cols, v);
+        else store_row<Lanes>(acc + at, in, cl, ti.cols, v);
     }
 };
 
@@ -382,103 +441,264 @@ __device__ __forceinline__ bool piece_done(const HeadGemm<T>& p) {
     return p.dyn == 2 && p.p0 > 0 && *p.count <= p.p0;
 }
 
-// bf16: BM x BN tiles, WM x WN waves, operands straight from HBM into a ring
-// of NSTG stages of BK steps, fragments double-buffered over the stages (the
-// main loop of the expert products, ggemm_bf16_dma_kernel).
-template <int BM, int BN, int WM, int WN, int NSTG, int BK, int ALAY, int BLAY, class Epi>
-__global__ __launch_bounds__(64 * WM * WN, 2) void head_product_kernel(HeadGemm<bf16_t> p,
-                                                                       Epi epi) {
-    constexpr int NT = 64 * WM * WN;
-    constexpr int WTM = BM / WM, WTN = BN / WN;
-    constexpr int FM = WTM / 32, FN = WTN / 32;
-    constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
-    constexpr int STAGE = A_BYTES + B_BYTES;
-    constexpr int SLAB = 16 * (WTN + 4) * 4;
-    static_assert(NSTG * STAGE <= 160 * 1024 && WM * WN * SLAB <= NSTG * STAGE, "LDS");
-    __shared__ __attribute__((aligned(1024))) uint8_t ringbuf[NSTG * STAGE];
+// One operand of a bf16 product: 256 rows of a stage of BK reduction steps go
+// from HBM straight into LDS (a unit of 256 * BK * 2 bytes, 1 KB a wave and load),
+// and fragments of v_mfma_f32_16x16x32_bf16 come out of it: row = lane % 16,
+// eight reduction steps from 8 * (lane / 16) on.
+//  K-major: rows of BK elements in 16-byte chunks, chunk c of row r at c ^ ((r ^
+//    r/CH) mod CH): the 16 rows of a read lie in distinct banks.
+//  M/N-major: BK rows of 256 elements, read with the transposing LDS read, which
+//    takes 4 reduction steps x 16 columns per 16 lanes; chunk c of step k at c ^
+//    4 (k mod 4) ^ 2 (k/8 mod 2): the four steps of a group and the two groups
+//    of half a wave lie in distinct banks.
+template <int LAY, int BK, int NW>
+struct HeadOperand {
+    static constexpr int ROWS = 256;
+    static constexpr int CH = BK / 8;
+    static constexpr int UNIT = ROWS * BK * 2;
+    static constexpr int NLOAD = UNIT / 1024 / NW;
+    const bf16_t* P;
+    long ld, span;
+    int k_lim;
+    uint32_t off[NLOAD];
+    uint32_t frag[LAY == KMAJ ? BK / 32 : 1];    // this lane's offsets in a unit, see read
+
+    static __device__ __forceinline__ int mn_swz(int k, int c) {
+        return c ^ ((k & 3) << 2) ^ ((k >> 3 & 1) << 1);
+    }
+    // P_: the tile's first row (K-major) or column; rows: valid ones; k_lim: end of
+    // the reduction; w0: the wave's first row in the tile
+    __device__ __forceinline__ void init(const bf16_t* P_, long ld_, int rows, int k_lim_, int w0) {
+        P = P_, ld = ld_, k_lim = k_lim_;
+        span = (long)rows * ld * 2;
+        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+        for (int i = 0; i < NLOAD; ++i) {
+            const int blk = w + NW * i;                    // 1 KB block of the unit
+            if constexpr (LAY == KMAJ) {
+                const int row = blk * (64 / CH) + lane / CH;
+                const int c = (lane % CH) ^ ((row ^ (row / CH)) & (CH - 1));
+                off[i] = (uint32_t)(row * ld * 2 + c * 16);
+            } else {
+                const int k = blk * 2 + lane / 32;
+                const int c = mn_swz(k, lane % 32);
+                off[i] = c * 8 < rows ? (uint32_t)(k * ld * 2 + c * 16) : OOB;
+            }
+        }
+        if constexpr (LAY == KMAJ) {
+            const int row = w0 + (lane & 15);
+#pragma unroll
+            for (int s = 0; s < BK / 32; ++s)
+                frag[s] = row * BK * 2 +
+                          (((s * 4 + (lane >> 4)) ^ ((row ^ (row / CH)) & (CH - 1))) << 4);
+        } else {
+            // step (lane / 16) * 8 + (lane % 16) / 4 of 32, columns 4 (lane % 4) on
+            const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
+            const int c = (w0 >> 3) + ((lane & 3) >> 1);
+            frag[0] = k * ROWS * 2 + (mn_swz(k, c) << 4) + (lane & 1) * 8;
+        }
+    }
+    // The descriptor of the unit at k0, whose loads outside the valid rows, the end
+    // of the reduction or (!some) altogether give zeros and read nothing.
+    __device__ __forceinline__ i32x4_t words(long k0, bool some) const {
+        const bf16_t* base = LAY == KMAJ ? P + k0 : P + k0 * ld;
+        const long n = LAY == KMAJ ? span - k0 * 2 : min((long)BK, k_lim - k0) * ld * 2;
+        return rsrc_words(base, some ? n : 0);
+    }
+    // wlds: the unit's LDS address + 1 KB times the wave, in a scalar register
+    template <int I>
+    __device__ __forceinline__ void load(i32x4_t rs, uint32_t wlds) const {
+        // one wait state between writing m0 and the load that reads it
+        asm volatile(
+            "s_add_u32 m0, %0, %1\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %2, %3, 0 offen lds"
+            :
+            : "s"(wlds), "n"(NW * I * 1024), "v"(off[I]), "s"(rs)
+            : "memory", "m0", "scc");
+    }
+    // Fragment I (rows 16 I on of the wave's) of the 32 steps S of the unit at
+    // LDS address u (aligned to its size, so that the swizzle can be applied to the sum,
+    // which keeps the eight addresses out of registers between the steps).
+    typedef __attribute__((address_space(3))) const u32x4_t lds_u32x4_t;
+    template <int I, int S>
+    __device__ __forceinline__ bf16x8 read(uint32_t u) const {
+        if constexpr (LAY == KMAJ) {
+            // 16 rows further: the swizzle of BK = 64 changes by (2 I) mod 8 chunks
+            constexpr uint32_t X = CH == 8 ? ((I * 2) & 7) << 4 : 0;
+            const u32x4_t v = *reinterpret_cast<lds_u32x4_t*>(((u + frag[S]) ^ X) + I * 16 * BK * 2);
+            return __builtin_bit_cast(bf16x8, v);
+        } else {
+            // 16 columns further: two chunks, under the swizzle
+            const uint32_t o = ((u + frag[0]) ^ (I << 5)) + S * 32 * ROWS * 2;
+            const v4i16_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                reinterpret_cast<lds_v4i16_t*>(o));
+            const v4i16_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                reinterpret_cast<lds_v4i16_t*>(o + 4 * ROWS * 2));
+            typedef short v8i16_t __attribute__((ext_vector_type(8)));
+            const v8i16_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            return __builtin_bit_cast(bf16x8, v);
+        }
+    }
+};
+
+// c += a b, the accumulators kept in the accumulation registers: 64 fragments
+// fill all 256 of them, and the compiler, left to choose, moves some of them to
+// the others and back in every step.
+__device__ __forceinline__ void mfma16(f32x4& c, const bf16x8& a, const bf16x8& b) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+// The wait between the last of them and the first read of their results, which
+// depends on it through the operands.
+__device__ __forceinline__ void mfma_done(f32x4 (&c)[8]) {
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]),
+                   "+a"(c[6]), "+a"(c[7]));
+}
+
+// bf16: 256 x 256 tiles, four waves of 128 x 128 (one a SIMD), operands straight
+// from HBM into a ring of NU units (a unit: one operand's 256 rows of a stage of
+// BK reduction steps; A's and B's take turns, unit u in slot u mod NU).
+//
+// The order of the instructions is the kernel: the matrix pipe takes one
+// 16x16x32 product every 16 cycles, and between two of them a wave issues at
+// most one fragment read or one load.  A step of 32 is 64 products on one set of
+// fragments, with the reads of the next step's set behind every second of the
+// first 32 and the loads spread between them; sched_barrier keeps that order.  One
+// barrier a stage, at the start of its last step: by then every wave has read the
+// whole stage (its two slots are free for the loads that follow) and the next
+// stage, which that step reads from, has landed.
+template <int BK, int NU, int ALAY, int BLAY, class Epi>
+__global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p, Epi epi) {
+    constexpr int UNIT = 256 * BK * 2;
+    constexpr int NS = BK / 32;                        // steps of a stage
+    static_assert(NU * UNIT <= 160 * 1024 && NU >= 5, "LDS");
+    __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[NU * UNIT];
     if (piece_done(p)) return;
-    const HeadTile ti = head_tile<BM, BN>(p);
+    const HeadTile ti = head_tile<256, 256>(p);
     if (!ti.live) return;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int wm = wv / WN, wn = wv % WN;
+    const int wm = wv >> 1, wn = wv & 1;
 
-    DmaOperand<BM, ALAY, NT, BK> opA;
-    DmaOperand<BN, BLAY, NT, BK> opB;
-    opA.init(p.A + (ALAY == KMAJ ? (long)ti.m0 * p.lda : (long)ti.m0), p.lda, ti.rows, ti.k1);
-    opB.init(p.B + (BLAY == KMAJ ? (long)ti.n0 * p.ldb : (long)ti.n0), p.ldb, ti.cols, ti.k1);
-    constexpr int NL = DmaOperand<BM, ALAY, NT, BK>::NLOAD + DmaOperand<BN, BLAY, NT, BK>::NLOAD;
-    static_assert(NL * (NSTG - 1) <= 63, "vmcnt counts at most 63 loads");
+    typedef HeadOperand<ALAY, BK, 4> OpA;
+    typedef HeadOperand<BLAY, BK, 4> OpB;
+    constexpr int NL = OpA::NLOAD;                     // loads of a unit
+    OpA opA;
+    OpB opB;
+    opA.init(p.A + (ALAY == KMAJ ? (long)ti.m0 * p.lda : (long)ti.m0), p.lda, ti.rows, ti.k1,
+             wm * 128);
+    opB.init(p.B + (BLAY == KMAJ ? (long)ti.n0 * p.ldb : (long)ti.n0), p.ldb, ti.cols, ti.k1,
+             wn * 128);
 
-    f32x16 acc[FM][FN];
+    f32x4 acc[8][8];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    bf16x8 af[2][8], bfr[2][8];
 
-    constexpr int KS = BK / 16;
-    static_assert(KS % 2 == 0, "fragment buffer parity assumes an even count");
-    bf16x8 af[2][FM], bfr[2][FN];
-    auto issue = [&](uint8_t* stg, int j) {
-        const long k = (long)ti.k0 + (long)j * BK;
-        opA.dma(k, stg);
-        opB.dma(k, stg + A_BYTES);
-    };
-    auto read_frags = [&](const uint8_t* stg, int ks, int buf) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-            af[buf][i] = dma_frag<BM, ALAY, BK>(stg, wm * WTM + i * 32, ks, lane);
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-            bfr[buf][j] = dma_frag<BN, BLAY, BK>(stg + A_BYTES, wn * WTN + j * 32, ks, lane);
-    };
-    auto mfmas = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[buf][i], bfr[buf][j],
-                                                                   acc[i][j], 0, 0, 0);
-    };
-    auto ring = [&](int q) -> uint8_t* { return ringbuf + q * STAGE; };
     const int nj = (ti.k1 - ti.k0 + BK - 1) / BK;
-    constexpr int NP = ALAY == KMAJ && BLAY == KMAJ ? NSTG : NSTG - 1;
-#pragma unroll
-    for (int q = 0; q < NP; ++q)
-        if (q < nj) issue(ring(q), q);
-    stage_barrier_ahead<NL, NP - 1>(min(nj - 1, NP - 1));   // stage 0 landed
-    if (nj > 0) read_frags(ring(0), 0, 0);
-    int qc = 0;                                        // ring slot of stage j
+    // stages past the end are loaded too, from an empty range: no memory is
+    // read, and the counts of loads in flight stay the same to the end
+    auto rsA = [&](int j) { return opA.words((long)ti.k0 + (long)j * BK, j < nj); };
+    auto rsB = [&](int j) { return opB.words((long)ti.k0 + (long)j * BK, j < nj); };
+    auto wrap = [](int q) { return q >= NU ? q - NU : q; };
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(ringbuf) + wv * 1024);
+    auto slot = [&](int q) { return lds0 + (uint32_t)(q * UNIT); };
+    const uint32_t ring0 = lds_addr(ringbuf);
+    auto unit = [&](int q) { return ring0 + (uint32_t)(q * UNIT); };
+
+    // fragment r of step s of a stage, in the order in which the products take them
+    auto read1 = [&](auto R, auto S, auto BUF, uint32_t ua, uint32_t ub) {
+        constexpr int r = decltype(R)::value, s = decltype(S)::value, buf = decltype(BUF)::value;
+        if constexpr (r == 0) af[buf][0] = opA.template read<0, s>(ua);
+        else if constexpr (r <= 8) bfr[buf][r - 1] = opB.template read<r - 1, s>(ub);
+        else af[buf][r - 8] = opA.template read<r - 8, s>(ua);
+    };
+    // one step: products on set BUF; reads of the set of step S in (ua, ub); loads
+    // L(0..n-1) from product first on, every gap-th
+    auto step = [&](auto BUF, auto S, uint32_t ua, uint32_t ub, auto FIRST, auto GAP,
+                    auto COUNT, auto&& load) {
+        constexpr int buf = decltype(BUF)::value, first = decltype(FIRST)::value,
+                      gap = decltype(GAP)::value, n = decltype(COUNT)::value;
+        static_assert(first + gap * (n - 1) < 64, "loads behind the products");
+        unroll<64>([&](auto Q) {
+            constexpr int q = decltype(Q)::value;
+            mfma16(acc[q / 8][q % 8], bfr[buf][q % 8], af[buf][q / 8]);   // (columns as rows)
+            if constexpr (q % 2 == 0 && q < 32)
+                read1(std::integral_constant<int, q / 2>{}, S, std::integral_constant<int, 1 - buf>{},
+                      ua, ub);
+            if constexpr (q >= first && (q - first) % gap == 0 && (q - first) / gap < n)
+                load(std::integral_constant<int, (q - first) / gap>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    typedef std::integral_constant<int, 0> I0;
+    typedef std::integral_constant<int, 1> I1;
+
+    // units 0 .. NU - 1 but those that the first stage's loads bring
+    constexpr int PRE = NU - (NS == 2 ? 1 : 0);
+    unroll<PRE>([&](auto U) {
+        constexpr int u = decltype(U)::value;
+        const i32x4_t rs = u % 2 ? rsB(u / 2) : rsA(u / 2);
+        unroll<NL>([&](auto I) {
+            if constexpr (u % 2) opB.template load<decltype(I)::value>(rs, slot(u));
+            else opA.template load<decltype(I)::value>(rs, slot(u));
+        });
+    });
+    stage_barrier<NL * (PRE - 2)>();                   // stage 0 landed
+    unroll<16>([&](auto R) { read1(R, I0{}, I0{}, unit(0), unit(1)); });
+    int qa = 0;                                        // slot of A's unit of stage j
+    if constexpr (NS == 2) {
+        // stage j: units 2j, 2j+1; A of stage j+2 is loaded in its first step, B of
+        // stage j+2 right behind its barrier
+        constexpr int G0 = 32 / NL;
+        typedef std::integral_constant<int, G0> GAP;
+        typedef std::integral_constant<int, NL> CNT;
 #pragma unroll 1
-    for (int j = 0; j + 1 < nj; ++j) {
-        const uint8_t* cur = ring(qc);
-        const int qn = qc + 1 == NSTG ? 0 : qc + 1;    // slot of stage j+1
-        const int qf = qc == 0 ? NSTG - 1 : qc - 1;    // slot of stage j-1 = j+NSTG-1
-        // every read of stage j-1 returned before the barrier that opened stage j
-        if ((NP < NSTG || j > 0) && j + NSTG - 1 < nj) issue(ring(qf), j + NSTG - 1);
-#pragma unroll
-        for (int ks = 0; ks + 1 < KS; ++ks) {
-            read_frags(cur, ks + 1, (ks + 1) & 1);
-            mfmas(ks & 1);
+        for (int j = 0; j < nj; ++j) {
+            const uint32_t ua = unit(qa), ub = unit(wrap(qa + 1));
+            const i32x4_t ra = rsA(j + 2);
+            step(I0{}, I1{}, ua, ub, std::integral_constant<int, 33>{}, GAP{}, CNT{}, [&](auto I) {
+                opA.template load<decltype(I)::value>(ra, slot(wrap(qa + 4)));
+            });
+            stage_barrier<NL>();                       // stage j read, stage j+1 landed
+            const i32x4_t rb = rsB(j + 2);
+            const int qn = wrap(qa + 2);
+            step(I1{}, I0{}, unit(qn), unit(wrap(qn + 1)), I1{}, GAP{}, CNT{}, [&](auto I) {
+                opB.template load<decltype(I)::value>(rb, slot(qa));
+            });
+            qa = qn;
         }
-        stage_barrier_ahead<NL, NSTG - 2>(min(nj - 2 - j, NSTG - 2));  // stage j+1 landed
-        read_frags(ring(qn), 0, 0);
-        mfmas((KS - 1) & 1);
-        qc = qn;
-    }
-    if (nj > 0) {
-        const uint8_t* cur = ring(qc);
-#pragma unroll
-        for (int ks = 0; ks + 1 < KS; ++ks) {
-            read_frags(cur, ks + 1, (ks + 1) & 1);
-            mfmas(ks & 1);
+    } else {
+        // stage j is one step, its set of fragments read during stage j-1; loads of stage
+        // j + NU / 2 into its slots
+        auto stage = [&](auto BUF, int j) {
+            stage_barrier<NL * (NU - 4)>();            // stage j read, stage j+1 landed
+            const i32x4_t ra = rsA(j + NU / 2), rb = rsB(j + NU / 2);
+            const int qn = wrap(qa + 2);
+            step(BUF, I0{}, unit(qn), unit(qn + 1), std::integral_constant<int, 33>{},
+                 std::integral_constant<int, 30 / (2 * NL)>{}, std::integral_constant<int, 2 * NL>{},
+                 [&](auto I) {
+                     constexpr int i = decltype(I)::value;
+                     if constexpr (i < NL) opA.template load<i>(ra, slot(qa));
+                     else opB.template load<i - NL>(rb, slot(qa + 1));
+                 });
+            qa = qn;
+        };
+        int j = 0;
+#pragma unroll 1
+        for (; j + 1 < nj; j += 2) {
+            stage(I0{}, j);
+            stage(I1{}, j + 1);
         }
-        mfmas((KS - 1) & 1);
+        if (j < nj) stage(I0{}, j);
     }
-    __syncthreads();
-    head_epilogue<WTM, WTN>(reinterpret_cast<float*>(ringbuf + wv * SLAB), ti, wm * WTM,
-                            wn * WTN, acc, epi);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // (loads of the empty stages)
+    unroll<8>([&](auto I) { mfma_done(acc[I]); });
+    unroll<8>([&](auto I) {
+        epi.template row<Quads16>(ti, wm * 128 + I * 16 + (lane & 15), wn * 128, acc[I]);
+    });
 }
 
 // fp32: 128 x 128 tiles, 4 waves of 64 x 64, v_mfma_f32_32x32x2_f32; tiles
@@ -488,9 +708,7 @@ constexpr int FBM = 128, FBK = 16;
 template <int ALAY, int BLAY, class Epi>
 __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float> p, Epi epi) {
     constexpr int LDT = FBM + 4;
-    constexpr int SLABF = 16 * (64 + 4);
     __shared__ __attribute__((aligned(16))) float lds[2 * 2 * FBK * LDT];
-    static_assert(4 * SLABF <= 4 * FBK * LDT, "epilogue slabs");
     if (piece_done(p)) return;
     const HeadTile ti = head_tile<FBM, FBM>(p);
     if (!ti.live) return;
@@ -566,10 +784,10 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
         for (int kk = 0; kk < FBK; kk += 2) {
             const int o = (kk + (lane >> 5)) * LDT;
             const float a0 = sa[o], a1 = sa[o + 32], b0 = sb[o], b1 = sb[o + 32];
-            acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a0, b0, acc[0][0], 0, 0, 0);
-            acc[0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a0, b1, acc[0][1], 0, 0, 0);
-            acc[1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(a1, b0, acc[1][0], 0, 0, 0);
-            acc[1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(a1, b1, acc[1][1], 0, 0, 0);
+            acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a0, acc[0][0], 0, 0, 0);
+            acc[0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a0, acc[0][1], 0, 0, 0);
+            acc[1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a1, acc[1][0], 0, 0, 0);
+            acc[1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a1, acc[1][1], 0, 0, 0);
         }
         if (more) {                    // the other buffer: read two stages ago
             store(bufA((j + 1) & 1), ALAY, ra);
@@ -577,7 +795,14 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
         }
         __syncthreads();
     }
-    head_epilogue<64, 64>(lds + wv * SLABF, ti, wm * 64, wn * 64, acc, epi);
+    unroll<2>([&](auto I) {
+        f32x4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[q][u] = acc[I][q >> 2][(q & 3) * 4 + u];
+        epi.template row<Quads32>(ti, wm * 64 + I * 32 + (lane & 31), wn * 64, v);
+    });
 }
 
 // out = the parts of a split reduction added in order, for dx (rows != NULL:
@@ -620,35 +845,47 @@ __global__ __launch_bounds__(256) void head_join_kernel(const float* __restrict_
 
 // --------------------------------------------------------- normalisers
 
-// lse (and that at the temperature, relative to the same maximum) of a
-// piece's rows from the parts: 64 rows a block, its 16 waves share the parts.
-// The loss of a labelled row goes to its token.
+// The normaliser of a row in units of log2: 2^(a + b) = sum_v e^z, a = the maximum
+// times L, rounded (the m' of the sums), b = log2 of the sum relative to it.
+struct Norm2 {
+    float a, b;
+};
+// ln of the sum: m + ln 2 (b - (m L - a)), the bracket's m L - a exact in a fused
+// multiply-add, so that the rounding of a does not reach the result.
+__device__ __forceinline__ float norm_ln(Norm2 n, float m, float scale, float l2) {
+    return fmaf(kLn2, n.b - fmaf(m, l2, -n.a), m * scale);
+}
+// p = e^(z - lse) (l2 = L, or L / tau at the temperature)
+__device__ __forceinline__ float norm_p(Norm2 n, float z, float l2) {
+    return exp2_hw(fmaf(z, l2, -n.a) - n.b);
+}
+
+// The normalisers of a piece's rows from the parts: 64 rows a block, its 16
+// waves share the parts.  The loss of a labelled row goes to its token.
 __global__ __launch_bounds__(1024) void head_lse_kernel(
     const float2* __restrict__ stat, const float* __restrict__ tstat, int parts, long ldr,
-    float inv_tau, const float* __restrict__ zl, const int32_t* __restrict__ labels, int V,
+    float l2t, const float* __restrict__ zl, const int32_t* __restrict__ labels, int V,
     const int32_t* __restrict__ rows, const int32_t* __restrict__ count, int fixed, int p0,
-    int piece, float* __restrict__ row_lse, float* __restrict__ row_tlse,
-    float* __restrict__ loss, float* __restrict__ lse) {
+    int piece, Norm2* __restrict__ norm, Norm2* __restrict__ tnorm, float* __restrict__ loss,
+    float* __restrict__ lse) {
     __shared__ float sm[16][64], ss[16][64], st[16][64];
     const int n = piece_rows(count, p0, piece, fixed);
     if (blockIdx.x * 64 >= n) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const long r = (long)blockIdx.x * 64 + lane;
+    // a part's factor relative to the running maximum mx; a part without a column
+    // (m = -inf) adds its sum as it is: 0, or the NaN of a score
+    auto f = [](float m, float mx, float l2) {
+        return m == -INFINITY ? 1.0f : exp2_hw(m * l2 - mx * l2);
+    };
     float m = -INFINITY, s = 0.0f, t = 0.0f;
     if (r < n) {
+#pragma unroll 4
         for (int q = w; q < parts; q += 16) {
             const float2 a = stat[q * ldr + r];
-            if (a.x == -INFINITY) {
-                s += a.y, t += tstat ? tstat[q * ldr + r] : 0.0f;   // no column: 0 (or a NaN)
-                continue;
-            }
             const float mx = fmaxf(m, a.x);
-            const float k0 = m == -INFINITY ? 0.0f : expf(m - mx), k1 = expf(a.x - mx);
-            s = s * k0 + a.y * k1;
-            if (tstat) {
-                const float j0 = m == -INFINITY ? 0.0f : expf((m - mx) * inv_tau);
-                t = t * j0 + tstat[q * ldr + r] * expf((a.x - mx) * inv_tau);
-            }
+            s = s * f(m, mx, kLog2e) + a.y * f(a.x, mx, kLog2e);
+            if (tstat) t = t * f(m, mx, l2t) + tstat[q * ldr + r] * f(a.x, mx, l2t);
             m = mx;
         }
     }
@@ -658,16 +895,16 @@ __global__ __launch_bounds__(1024) void head_lse_kernel(
     for (int q = 1; q < 16; ++q) m = fmaxf(m, sm[q][lane]);
     s = 0.0f, t = 0.0f;
     for (int q = 0; q < 16; ++q) {
-        const float d = sm[q][lane] == -INFINITY ? 0.0f : sm[q][lane] - m;
-        s += ss[q][lane] * expf(d);
-        t += st[q][lane] * expf(d * inv_tau);
+        s += ss[q][lane] * f(sm[q][lane], m, kLog2e);
+        t += st[q][lane] * f(sm[q][lane], m, l2t);
     }
-    const float l = m + logf(s);
-    if (row_lse) row_lse[r] = l;
-    if (row_tlse) row_tlse[r] = m * inv_tau + logf(t);
+    const Norm2 nm = {m * kLog2e, __builtin_amdgcn_logf(s)};
+    if (norm) norm[r] = nm;
+    if (tnorm) tnorm[r] = {m * l2t, __builtin_amdgcn_logf(t)};
     const int tok = rows ? rows[p0 + r] : (int)r;
     if (labels) {
         const bool on = in_vocab(labels[tok], V);
+        const float l = norm_ln(nm, m, 1.0f, kLog2e);
         if (loss) loss[tok] = on ? l - zl[r] : 0.0f;
         if (lse) lse[tok] = on ? l : 0.0f;
     }
@@ -676,52 +913,59 @@ __global__ __launch_bounds__(1024) void head_lse_kernel(
 // ----------------------------------------------------------------- dz
 
 struct HeadDz {
-    float* Z;                // [piece][ldz]; dz takes its place, from each row's start
+    const float* Z;          // [piece][ldz] scores
     long ldz;
+    void* G;                 // [piece][ldg] dz: Z itself (segs = 1), or a buffer of its own
+    long ldg;                // in elements of dz
+    int segs, seg;           // segments of a row, their length (a multiple of 256)
     int V;
     const int32_t* rows;
     const int32_t* count;
     int p0, piece;
-    const float* lse;        // of the row, and at the temperature
-    const float* tlse;
+    const Norm2* norm;       // of the row, and at the temperature
+    const Norm2* tnorm;
     const int32_t* labels;   // or NULL
     const float* weight;     // [T] or NULL: 1
     const int32_t* tidx;     // [T,K] or NULL
     const float* tlogit;
     const float* tweight;    // [T] or NULL: 1
     int K;
-    float tau, inv_tau;
+    float tau, inv_tau, l2t;
     float* kd;               // [T] or NULL
     int grad;
 };
 
-// One wave a row.  The scores at the label and the teacher's slots are read
-// first and their dz is written last (an entry named twice by its first slot,
-// with the slots' q added in order), the rest streams: chunk c of the row's
-// dz is stored after chunk c of z has been read, and lies in front of every
-// chunk still to be read (half the element size; in fp32 at the same place).
+// One wave a row, or a segment of one when the rows are few.  The scores at the
+// label and the teacher's slots are read first and their dz is written last (an
+// entry named twice by its first slot, with the slots' q added in order); the
+// rest streams.  In place: unit c (256 elements) of the row's dz is stored after
+// units 0 .. c of z have come back, and at half the element size lies in front
+// of every unit still to be read (in fp32 in its own place).
 template <typename T>
 __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
-    __shared__ int s_idx[4][kMaxK + 1];
-    __shared__ float s_q[4][kMaxK + 1];
+    __shared__ int s_idx[4][kMaxK];
+    __shared__ float s_q[4][kMaxK];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int n = piece_rows(p.count, p.p0, p.piece, 0);
-    const int r = blockIdx.x * 4 + w;
+    const int item = blockIdx.x * 4 + w;
+    const int r = item / p.segs, part = item - r * p.segs;
     if (r >= n) return;                       // whole waves; no block barrier below
     const int t = p.rows[p.p0 + r];
-    float* z = p.Z + (long)r * p.ldz;
+    const float* z = p.Z + (long)r * p.ldz;
+    const int c0 = part * p.seg, c1 = (int)min(p.ldz, (long)c0 + p.seg);
     int label = p.labels ? p.labels[t] : -1;
     if (!in_vocab(label, p.V)) label = -1;
     const float wce = label >= 0 ? (p.weight ? p.weight[t] : 1.0f) : 0.0f;
-    const float lse = p.lse[r];
+    const Norm2 nm = p.norm[r];
 
-    // the teacher's distribution; slot K is the label
-    constexpr int PL = (kMaxK + 63) / 64;
+    // the teacher's distribution
+    constexpr int PL = kMaxK / 64;
     int idx[PL];
     float q[PL], zt[PL];
-    float wkd = 0.0f, tlse = 0.0f;
+    float wkd = 0.0f;
+    Norm2 tn = {0.0f, 0.0f};
     if (p.tidx) {
-        tlse = p.tlse[r];
+        tn = p.tnorm[r];
         float hi = -INFINITY;
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
@@ -756,11 +1000,12 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
             const int j = lane + 64 * u;
             q[u] *= inv;
             zt[u] = idx[u] >= 0 ? z[idx[u]] : 0.0f;
-            if (q[u] != 0.0f) kd += q[u] * (lq[u] - ltot - (zt[u] * p.inv_tau - tlse));
+            if (q[u] != 0.0f)                 // ln p = ln 2 log2 p
+                kd += q[u] * (lq[u] - ltot - kLn2 * (fmaf(zt[u], p.l2t, -tn.a) - tn.b));
             if (j < p.K) s_idx[w][j] = idx[u], s_q[w][j] = q[u];
         }
         kd = wave_sum(kd);
-        if (lane == 0 && p.kd) p.kd[t] = any ? kd * p.tau * p.tau : 0.0f;
+        if (part == 0 && lane == 0 && p.kd) p.kd[t] = any ? kd * p.tau * p.tau : 0.0f;
         wkd = any ? p.tau * (p.tweight ? p.tweight[t] : 1.0f) : 0.0f;
     }
     if (!p.grad) return;
@@ -768,27 +1013,47 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     wave_lds_sync();
     wave_mem_sync();                          // those reads are back before any store
 
-    T* g = reinterpret_cast<T*>(z);
-    auto dense = [&](float v) {
-        float o = wce != 0.0f ? wce * expf(v - lse) : 0.0f;
-        if (wkd != 0.0f) o += wkd * expf(v * p.inv_tau - tlse);
-        return o;
-    };
-    for (long c = lane * 8; c < p.ldz; c += 512) {
-        float v[8];
-        ld8(z + c, v);
+    T* g = static_cast<T*>(p.G) + (long)r * p.ldg;
+    auto ce = [&](float v) { return wce * norm_p(nm, v, kLog2e); };
+    auto kl = [&](float v) { return wkd * norm_p(tn, v, p.l2t); };
+    auto stream = [&](auto&& dense) {
+        constexpr int U = 4;                  // units in flight
+        for (int c = c0 + lane * 4; c < c1; c += 256 * U) {
+            f32x4 v[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = c + u < p.V ? dense(v[u]) : 0.0f;
-        st8(g + c, v);
-    }
+            for (int u = 0; u < U; ++u)
+                if (c + 256 * u < c1) v[u] = *reinterpret_cast<const f32x4*>(z + c + 256 * u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int cu = c + 256 * u;
+                if (cu >= c1) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[u][e] = cu + e < p.V ? dense(v[u][e]) : 0.0f;
+                if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<f32x4*>(g + cu) = v[u];
+                } else {
+                    *reinterpret_cast<uint2*>(g + cu) =
+                        make_uint2(pack_bf16x2(v[u][0], v[u][1]), pack_bf16x2(v[u][2], v[u][3]));
+                }
+            }
+        }
+    };
+    // a weight of zero leaves its term out (no 0 times infinity)
+    auto at = [&](float v) { return (wce != 0.0f ? ce(v) : 0.0f) + (wkd != 0.0f ? kl(v) : 0.0f); };
+    if (wkd == 0.0f && wce != 0.0f) stream(ce);
+    else if (wce == 0.0f && wkd != 0.0f) stream(kl);
+    else stream(at);
     wave_mem_sync();
-    // the label and the teacher's slots
+    // the label and the teacher's slots, those of this segment
+    auto mine = [&](int v) { return v >= c0 && v < c1; };
     bool label_named = false;
     if (p.tidx) {
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
             const int j = lane + 64 * u;
             if (j >= p.K || idx[u] < 0) continue;
+            if (idx[u] == label) label_named = true;
+            if (!mine(idx[u])) continue;
             float sum = 0.0f;
             bool first = true;
             for (int k = 0; k < p.K; ++k)
@@ -796,13 +1061,12 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
                     first = first && k >= j;
                     sum += s_q[w][k];
                 }
-            if (idx[u] == label) label_named = true;
             if (first)
-                Elem<T>::st(g + idx[u], dense(zt[u]) - wkd * sum - (idx[u] == label ? wce : 0.0f));
+                Elem<T>::st(g + idx[u], at(zt[u]) - wkd * sum - (idx[u] == label ? wce : 0.0f));
         }
     }
-    if (label >= 0 && __ballot(label_named) == 0 && lane == 0)
-        Elem<T>::st(g + label, dense(zy) - wce);
+    if (label >= 0 && mine(label) && __ballot(label_named) == 0 && lane == 0)
+        Elem<T>::st(g + label, at(zy) - wce);
 }
 
 // ------------------------------------------------------------- the calls
@@ -813,12 +1077,14 @@ inline bool head_sizes_ok(int T, int d, int V, int K, moe_dtype dt) {
 }
 
 constexpr size_t kHeadLimit = (size_t)4 << 30;
+constexpr int kFewRows = 2048;         // up to here dz has a buffer of its own
 
 struct HeadPlan {
     int piece, pieces, parts;
     long ldz;
     int dx_splits, dw_splits;
-    size_t rows, count, act, xc, zl, lse, tlse, stat, tstat, z, dxp, acc, dwp, total;
+    int segs, seg;                     // of a row of dz
+    size_t rows, count, act, xc, zl, norm, tnorm, stat, tstat, z, g, dxp, acc, dwp, total;
 };
 
 // Parts of the reduction of a product with `tiles` output tiles over K:
@@ -850,11 +1116,18 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     p.act = take(K > 0 ? (size_t)T * 4 : 0);
     p.xc = take((size_t)piece * d * b);
     p.zl = take((size_t)piece * 4);
-    p.lse = take((size_t)piece * 4);
-    p.tlse = take(K > 0 ? (size_t)piece * 4 : 0);
+    p.norm = take((size_t)piece * 8);
+    p.tnorm = take(K > 0 ? (size_t)piece * 8 : 0);
     p.stat = take((size_t)p.parts * piece * 8);
     p.tstat = take(K > 0 ? (size_t)p.parts * piece * 4 : 0);
     p.z = take(store ? (size_t)piece * p.ldz * 4 : 0);
+    // few rows: several waves a row, which cannot write in place
+    p.segs = 1, p.seg = (int)p.ldz;
+    if (grad && piece <= kFewRows) {
+        p.seg = std::max(2048, (int)align_up(cdiv(p.ldz * piece, 8192), 256));
+        p.segs = cdiv(p.ldz, p.seg);
+    }
+    p.g = take(grad ? (size_t)std::min(piece, kFewRows) * p.ldz * b : 0);
     // the partial sums of dx: room for any smaller piece too (fewer tiles, more
     // parts), so that a workspace for T tokens serves every smaller batch
     size_t dxp = 0;
@@ -917,8 +1190,8 @@ template <int ALAY, int BLAY, typename T, class Epi>
 void head_product(HeadGemm<T> g, long m, const Epi& epi, hipStream_t s, const char* name) {
     if constexpr (sizeof(T) == 2) {
         const int grid = head_grid<256, 256>(g, m);
-        MOE_LAUNCH(name, s, head_product_kernel<256, 256, 4, 2, 2, 64, ALAY, BLAY, Epi>
-                   <<<grid, 512, 0, s>>>(g, epi));
+        MOE_LAUNCH(name, s, head_product_kernel<HEAD_BK, 320 / HEAD_BK, ALAY, BLAY, Epi>
+                   <<<grid, 256, 0, s>>>(g, epi));
     } else {
         const int grid = head_grid<FBM, FBM>(g, m);
         MOE_LAUNCH(name, s, head_product_f32_kernel<ALAY, BLAY, Epi><<<grid, 256, 0, s>>>(g, epi));
@@ -933,11 +1206,11 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     float2* stat = reinterpret_cast<float2*>(ws + p.stat);
     float* tstat = teacher ? reinterpret_cast<float*>(ws + p.tstat) : nullptr;
     float* zl = reinterpret_cast<float*>(ws + p.zl);
-    float* rlse = reinterpret_cast<float*>(ws + p.lse);
-    float* rtlse = teacher ? reinterpret_cast<float*>(ws + p.tlse) : nullptr;
+    Norm2* norm = reinterpret_cast<Norm2*>(ws + p.norm);
+    Norm2* tnorm = teacher ? reinterpret_cast<Norm2*>(ws + p.tnorm) : nullptr;
     float* Z = store ? reinterpret_cast<float*>(ws + p.z) : nullptr;
     T* xc = reinterpret_cast<T*>(ws + p.xc);
-    const float inv_tau = 1.0f / c.tau;
+    const float inv_tau = 1.0f / c.tau, l2t = (float)(1.4426950408889634 / (double)c.tau);
     const int vpr = c.d * (int)sizeof(T) / 16;
     const int32_t* act = c.labels;
     int limit = c.V;
@@ -961,18 +1234,22 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
         g.count = count, g.p0 = p0, g.piece = p.piece;
         g.A = xc, g.lda = c.d, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
         g.M = bound, g.N = c.V, g.K = c.d, g.dyn = 1, g.splits = 1;
-        const EpiScores es = {c.V, stat, tstat, inv_tau, p.piece, c.labels, rows, p0, zl, Z, p.ldz};
+        const EpiScores es = {c.V, stat, tstat, l2t, p.piece, c.labels, rows, p0, zl, Z, p.ldz};
         head_product<KMAJ, KMAJ>(g, bound, es, s, "head_scores");
         MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(bound, 64), 1024, 0, s>>>(
-                       stat, tstat, p.parts, p.piece, inv_tau, zl, c.labels, c.V, rows, count, 0, p0,
-                       p.piece, rlse, rtlse, c.loss, c.lse));
+                       stat, tstat, p.parts, p.piece, l2t, zl, c.labels, c.V, rows, count, 0, p0,
+                       p.piece, norm, tnorm, c.loss, c.lse));
         if (!store) continue;
-        const HeadDz dz = {Z, p.ldz, c.V, rows, count, p0, p.piece, rlse, rtlse, c.labels, c.weight,
-                           c.tidx, c.tlogit, c.tweight, c.K, c.tau, inv_tau, c.kd, c.grad};
-        MOE_LAUNCH("head_dz", s, head_dz_kernel<T><<<cdiv(bound, 4), 256, 0, s>>>(dz));
+        // dz in place of z, row by row, or in its own buffer
+        T* G = p.segs > 1 ? reinterpret_cast<T*>(ws + p.g) : reinterpret_cast<T*>(Z);
+        const long ldg = p.segs > 1 ? p.ldz : p.ldz * (4 / (long)sizeof(T));
+        const int segs = c.grad ? p.segs : 1;
+        const HeadDz dz = {Z, p.ldz, G, ldg, segs, segs > 1 ? p.seg : (int)p.ldz, c.V, rows, count,
+                           p0, p.piece, norm, tnorm, c.labels, c.weight, c.tidx, c.tlogit,
+                           c.tweight, c.K, c.tau, inv_tau, l2t, c.kd, c.grad};
+        MOE_LAUNCH("head_dz", s,
+                   head_dz_kernel<T><<<cdiv((long)bound * segs, 4), 256, 0, s>>>(dz));
         if (!c.grad) continue;
-        const T* G = reinterpret_cast<const T*>(Z);
-        const long ldg = p.ldz * (4 / (long)sizeof(T));
         if (c.dx) {
             g.A = G, g.lda = ldg, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
             g.M = bound, g.N = c.d, g.K = c.V, g.dyn = 1, g.splits = p.dx_splits;
