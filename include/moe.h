@@ -444,7 +444,7 @@ moe_status moe_clip_grads(const void *const *grads, void *const *out,
  * and dWv are rounded once.
  *   ws: 16-byte aligned, no initial content needed; calls that may overlap in
  *   time need one each.  moe_head_workspace_bytes gives the size for the
- *   largest pieces of tokens that stay within `limit` bytes (0: 4 GiB), or the
+ *   largest pieces of tokens that stay within `limit` bytes (0: 8 GiB), or the
  *   smallest there is (pieces of 256 tokens) if none does; a call takes any size from
  *   the smallest on and uses the largest pieces that fit, so more memory is
  *   fewer pieces.  The answer for T covers every smaller T of the

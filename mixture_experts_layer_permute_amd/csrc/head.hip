@@ -16,10 +16,11 @@
 //               reduces every row's 128 columns to (max, sum of exp) from the
 //               fp32 accumulators, so the normaliser needs no second look at
 //               z, and z is stored (in fp32) only when something reads it;
-//  head_dz      z -> dz in place, one wave a row: no barriers, as a wave's
-//               stores at half the element size stay behind its loads;
-//  head_product dx = dz Wv (split over the vocabulary when the tiles are few)
-//               and dWv = dz^T x, summed over the pieces in fp32.
+//  head_dz      z -> dz, a stream; the scores are held for 2048 tokens at a time
+//               (8 row tiles share a column tile's weights), dz for the piece;
+//  head_product dx = dz Wv and dWv = dz^T x, the tiles after the last full round
+//               of the compute units split over the reduction; dWv is summed over the
+//               pieces in fp32.
 // Nothing is computed twice: 6 n d V operations, the least there is with z
 // not kept beyond its piece.  The other way, keeping no scores and computing
 // them again for dz, costs 8 n d V.
@@ -36,13 +37,10 @@ namespace moe {
 namespace {
 
 constexpr int kMaxK = 256;              // teacher slots of a token
-#ifndef HEAD_BK
-#define HEAD_BK 64
-#endif
 constexpr int kRowAlign = 256;          // tokens of a piece: whole row tiles
 
-// A wave's lane reads and writes ordered as written: the reads before it have
-// returned, the writes before it are done.
+// The wave's stores before it are done: a later one of another lane to the same
+// place comes behind them.
 __device__ __forceinline__ void wave_mem_sync() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
@@ -109,6 +107,32 @@ __global__ __launch_bounds__(256) void head_active_kernel(const int32_t* __restr
     if (lane == 0) act[t] = any ? 1 : -1;
 }
 
+constexpr int kRound = 256;             // compute units
+constexpr int kMaxParts = 32;           // of a tile
+constexpr int kMaxSlots = 768;          // rest tiles times parts
+
+// Parts of each of R rest tiles whose reduction has nj stages of 64 steps: the
+// fewest stage times over the rounds they take, with about 6 stages for a tile's
+// start and end, and a twelfth of one a slot for writing and adding it up (512 KB
+// at about 4.5 TB/s against 1.2 us a stage).
+__host__ __device__ inline int rest_parts(int R, int nj) {
+    int best = 1;
+    float least = 1e30f;
+    for (int S = 1; S <= kMaxParts && S * 4 <= nj + 3 && (S == 1 || R * S <= kMaxSlots); ++S) {
+        const int rounds = (R * S + kRound - 1) / kRound;
+        const float t = rounds * ((nj + S - 1) / S + 6.0f) + (S > 1 ? 4.0f + R * S * 0.085f : 0.0f);
+        if (t < least) least = t, best = S;
+    }
+    return best;
+}
+
+// For head_compact_kernel's last step: plan[2 piece + {0: dx, 1: dWv}] = the parts
+// of the product's rest tiles.
+struct HeadParts {
+    int32_t* plan;
+    int pieces, piece, d, V, bm;
+};
+
 // rows[0..n) = the tokens that have a loss, in order; *count = n; the outputs
 // of the others are zero.  act: labels (limit V) or head_active's (limit 2).
 // One block: each round takes 4096 tokens, four a thread.
@@ -118,7 +142,8 @@ __global__ __launch_bounds__(1024) void head_compact_kernel(const int32_t* __res
                                                             int32_t* __restrict__ count,
                                                             float* __restrict__ o0,
                                                             float* __restrict__ o1,
-                                                            float* __restrict__ o2) {
+                                                            float* __restrict__ o2,
+                                                            HeadParts hp) {
     __shared__ int sh[16];
     int base = 0;
     for (int t0 = 0; t0 < T; t0 += 4096) {
@@ -146,6 +171,13 @@ __global__ __launch_bounds__(1024) void head_compact_kernel(const int32_t* __res
         base += total;
     }
     if (threadIdx.x == 0) *count = base;
+    // how the products of each piece are split
+    for (int i = threadIdx.x; i < hp.pieces * 2; i += 1024) {
+        const int n = max(0, min(base - (i >> 1) * hp.piece, hp.piece));
+        const int nM = ((i & 1) ? hp.V + hp.bm - 1 : n + hp.bm - 1) / hp.bm;
+        const int tiles = nM * ((hp.d + hp.bm - 1) / hp.bm);
+        hp.plan[i] = rest_parts(tiles % kRound, ((i & 1) ? n + 63 : hp.V + 63) / 64);
+    }
 }
 
 // The active rows of one piece (of `piece` rows from compacted row p0 on).
@@ -179,8 +211,11 @@ __global__ __launch_bounds__(256) void head_zero_kernel(u32x4_t* __restrict__ p,
 
 // ------------------------------------------------------- matrix products
 
-// C [M,N] = A . B over K, in `splits` parts of the reduction.  Of M and K one
-// may be the piece's rows, known on the device only (dyn).
+// C [M,N] = A . B over K.  Of M and K one may be the piece's rows, known on the
+// device only (dyn).  The compute units take the output tiles in rounds of 256;
+// the rest of the tiles, after the last full round, may be split over the
+// reduction (plan: in how many parts), each part's product stored in fp32 in a slot of
+// its own for head_join to add up.
 template <typename T>
 struct HeadGemm {
     const T* A;
@@ -191,43 +226,56 @@ struct HeadGemm {
     int dyn;                 // 1: M, 2: K is the piece's rows (0: neither)
     const int32_t* count;
     int p0, piece;
-    int splits;
+    const int32_t* plan;     // parts of a rest tile (NULL: 1)
+    float* part;             // [slot][BM][BN]
     int xcd_run;
 };
 
 struct HeadTile {
     int m0, n0, rows, cols;  // tile origin, valid rows and columns
-    int M;
     int k0, k1;              // this part of the reduction
-    int split;
+    int slot;                // >= 0: a part, stored there
     bool live;
 };
 
-// Tiles in groups of 8 row tiles, every column tile of a group before the
-// next group, row tiles fastest: a run of 32 on one XCD is 8 x 4 tiles, which
-// share their operands in its L2.  The parts of the reduction go one after the other.
+// Tile w of nM x nN: in groups of 8 row tiles, every column tile of a group before
+// the next group, row tiles fastest: a run of 32 on one XCD is 8 x 4 tiles,
+// which share their operands in its L2.
+template <int BM, int BN>
+__device__ __forceinline__ void head_origin(int w, int nM, int nN, int& m0, int& n0) {
+    const int first = (w / (8 * nN)) * 8;
+    const int gm = min(8, nM - first);
+    w -= first * nN;
+    m0 = (first + w % gm) * BM;
+    n0 = (w / gm) * BN;
+}
+
 template <int BM, int BN, typename T>
 __device__ __forceinline__ HeadTile head_tile(const HeadGemm<T>& p) {
     HeadTile t;
     const int n = p.dyn ? piece_rows(p.count, p.p0, p.piece, p.piece) : 0;
-    t.M = p.dyn == 1 ? n : p.M;
-    const int K = p.dyn == 2 ? n : p.K;
-    const int nM = (t.M + BM - 1) / BM, nN = (p.N + BN - 1) / BN;
-    const int L = xcd_logical(blockIdx.x, p.xcd_run);
-    t.live = L < nM * nN * p.splits;
-    if (!t.live) return t;
-    t.split = L / (nM * nN);
-    const int w0 = L - t.split * (nM * nN);
-    const int first = (w0 / (8 * nN)) * 8;
-    const int gm = min(8, nM - first);
-    const int w = w0 - first * nN;
-    t.m0 = (first + w % gm) * BM;
-    t.n0 = (w / gm) * BN;
-    t.rows = min(BM, t.M - t.m0);
+    const int M = p.dyn == 1 ? n : p.M, K = p.dyn == 2 ? n : p.K;
+    const int nM = (M + BM - 1) / BM, nN = (p.N + BN - 1) / BN, tiles = nM * nN;
+    const int S = p.plan ? *p.plan : 1;
+    const int full = S > 1 ? tiles / kRound * kRound : tiles;
+    int L = xcd_logical(blockIdx.x, p.xcd_run);
+    t.slot = -1;
+    t.k0 = 0, t.k1 = K;
+    if (L >= full) {
+        const int R = tiles - full, item = L - full;
+        t.live = item < R * S;
+        if (!t.live) return t;
+        const int s = item / R;
+        const int kc = ((K + S - 1) / S + 63) / 64 * 64;
+        t.k0 = min(K, s * kc);
+        t.k1 = min(K, t.k0 + kc);
+        t.slot = item;
+        L = full + item - s * R;
+    }
+    t.live = true;
+    head_origin<BM, BN>(L, nM, nN, t.m0, t.n0);
+    t.rows = min(BM, M - t.m0);
     t.cols = min(BN, p.N - t.n0);
-    const int kc = ((K + p.splits - 1) / p.splits + 63) / 64 * 64;
-    t.k0 = min(K, t.split * kc);
-    t.k1 = min(K, t.k0 + kc);
     return t;
 }
 
@@ -268,6 +316,7 @@ __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2
 // exp(z - m) = 2^(z L - m'), L = log2 e, m' = m L rounded: one fused multiply-add
 // before the hardware's 2^x, the same m' wherever the sum is used.
 struct EpiScores {
+    static constexpr bool kSplits = false;
     int V;
     float2* stat;            // [parts][ldr] (m, sum)
     float* tstat;            // [parts][ldr] sum at the temperature, or NULL
@@ -384,6 +433,7 @@ __device__ __forceinline__ void store_row(T* out, bool in, int cl, int cols, con
 // dx rows, back at their tokens.
 template <typename T>
 struct EpiRows {
+    static constexpr bool kSplits = true;
     T* out;
     long ldo;
     const int32_t* rows;
@@ -395,23 +445,15 @@ struct EpiRows {
         store_row<Lanes>(out + (in ? (long)rows[p0 + ti.m0 + rl] : 0) * ldo + ti.n0, in, cl,
                          ti.cols, v);
     }
-};
-
-// One part of a split reduction, fp32.
-struct EpiPart {
-    float* part;
-    long ldo, stride;
-    template <class Lanes>
-    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
-                                        const f32x4 (&v)[8]) const {
-        store_row<Lanes>(part + ti.split * stride + (long)(ti.m0 + rl) * ldo + ti.n0,
-                         rl < ti.rows, cl, ti.cols, v);
+    __device__ __forceinline__ void put8(int r, int c, const float* v) const {
+        st8(out + (long)rows[p0 + r] * ldo + c, v);
     }
 };
 
 // dWv over the pieces: the running sum in fp32, the last piece rounds it.
 template <typename T>
 struct EpiSum {
+    static constexpr bool kSplits = true;
     T* out;
     float* acc;
     long ldo;
@@ -432,7 +474,25 @@ struct EpiSum {
         if (*count <= p0 + piece) store_row<Lanes>(out + at, in, cl, ti.cols, v);
         else store_row<Lanes>(acc + at, in, cl, ti.cols, v);
     }
+    __device__ __forceinline__ void put8(int r, int c, float* v) const {
+        const long at = (long)r * ldo + c;
+        if (p0 > 0) {
+            float a[8];
+            ld8(acc + at, a);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += a[q];
+        }
+        if (*count <= p0 + piece) st8(out + at, v);
+        else st8(acc + at, v);
+    }
 };
+
+// One row of a part into its slot.
+template <class Lanes, int BM, int BN>
+__device__ __forceinline__ void store_part(float* part, const HeadTile& ti, int rl, int cl,
+                                           const f32x4 (&v)[8]) {
+    store_row<Lanes>(part + (long)ti.slot * (BM * BN) + rl * BN, rl < ti.rows, cl, ti.cols, v);
+}
 
 // A piece past the last token adds nothing to dWv (the first always runs: it
 // writes the zeros of a batch without a loss).
@@ -696,6 +756,13 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // (loads of the empty stages)
     unroll<8>([&](auto I) { mfma_done(acc[I]); });
+    if (Epi::kSplits && ti.slot >= 0) {
+        unroll<8>([&](auto I) {
+            store_part<Quads16, 256, 256>(p.part, ti, wm * 128 + I * 16 + (lane & 15), wn * 128,
+                                          acc[I]);
+        });
+        return;
+    }
     unroll<8>([&](auto I) {
         epi.template row<Quads16>(ti, wm * 128 + I * 16 + (lane & 15), wn * 128, acc[I]);
     });
@@ -801,46 +868,44 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
         for (int q = 0; q < 8; ++q)
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[q][u] = acc[I][q >> 2][(q & 3) * 4 + u];
-        epi.template row<Quads32>(ti, wm * 64 + I * 32 + (lane & 31), wn * 64, v);
+        const int rl = wm * 64 + I * 32 + (lane & 31);
+        if (Epi::kSplits && ti.slot >= 0)
+            store_part<Quads32, FBM, FBM>(p.part, ti, rl, wn * 64, v);
+        else
+            epi.template row<Quads32>(ti, rl, wn * 64, v);
     });
 }
 
-// out = the parts of a split reduction added in order, for dx (rows != NULL:
-// row r goes to token rows[p0 + r]) or dWv (the pieces' running sum as in
-// EpiSum).  8 elements a thread; n8 = M * N / 8, N a multiple of 8.
-template <typename T>
-__global__ __launch_bounds__(256) void head_join_kernel(const float* __restrict__ part, int splits,
-                                                        long stride, long n8, int N,
-                                                        T* __restrict__ out,
-                                                        const int32_t* __restrict__ rows,
-                                                        float* __restrict__ acc,
-                                                        const int32_t* __restrict__ count, int p0,
-                                                        int piece) {
-    const long i = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (i >= n8 * 8) return;
-    const int have = *count;
-    const long r = i / N;
-    if (rows ? r >= have - p0 : (p0 > 0 && have <= p0)) return;
+// The rest tiles of a product whose reduction was split: their parts added in
+// order and put where the product's epilogue puts them.  8 elements a thread.
+template <int BM, int BN, typename T, class Epi>
+__global__ __launch_bounds__(1024) void head_join_kernel(HeadGemm<T> p, Epi epi) {
+    constexpr int PER = BM * BN / 8192;               // blocks of a tile
+    const int S = *p.plan;
+    if (S == 1 || piece_done(p)) return;
+    const int n = piece_rows(p.count, p.p0, p.piece, p.piece);
+    const int M = p.dyn == 1 ? n : p.M;
+    const int nM = (M + BM - 1) / BM, nN = (p.N + BN - 1) / BN;
+    const int full = nM * nN / kRound * kRound, R = nM * nN - full;
+    const int tile = blockIdx.x / PER;
+    if (tile >= R) return;
+    int m0, n0;
+    head_origin<BM, BN>(full + tile, nM, nN, m0, n0);
+    const int e = ((blockIdx.x % PER) * 1024 + threadIdx.x) * 8;
+    const int r = m0 + e / BN, c = n0 + e % BN;
+    if (r >= M || c >= p.N) return;
+    const float* q = p.part + (long)tile * (BM * BN) + e;
+    const long stride = (long)R * (BM * BN);
     float v[8];
-    ld8(part + i, v);
-    for (int s = 1; s < splits; ++s) {
+    ld8(q, v);
+#pragma unroll 4
+    for (int s = 1; s < S; ++s) {
         float a[8];
-        ld8(part + s * stride + i, a);
+        ld8(q + s * stride, a);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += a[q];
+        for (int u = 0; u < 8; ++u) v[u] += a[u];
     }
-    if (rows) {
-        st8(out + (long)rows[p0 + r] * N + (i - r * N), v);
-        return;
-    }
-    if (p0 > 0) {
-        float a[8];
-        ld8(acc + i, a);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += a[q];
-    }
-    if (have <= p0 + piece) st8(out + i, v);
-    else st8(acc + i, v);
+    epi.put8(r, c, v);
 }
 
 // --------------------------------------------------------- normalisers
@@ -860,44 +925,47 @@ __device__ __forceinline__ float norm_p(Norm2 n, float z, float l2) {
     return exp2_hw(fmaf(z, l2, -n.a) - n.b);
 }
 
-// The normalisers of a piece's rows from the parts: 64 rows a block, its 16
-// waves share the parts.  The loss of a labelled row goes to its token.
+// The normalisers of a piece's rows from the parts: 16 rows a block, 64 threads
+// share a row's parts.  The loss of a labelled row goes to its token.
 __global__ __launch_bounds__(1024) void head_lse_kernel(
     const float2* __restrict__ stat, const float* __restrict__ tstat, int parts, long ldr,
     float l2t, const float* __restrict__ zl, const int32_t* __restrict__ labels, int V,
     const int32_t* __restrict__ rows, const int32_t* __restrict__ count, int fixed, int p0,
     int piece, Norm2* __restrict__ norm, Norm2* __restrict__ tnorm, float* __restrict__ loss,
     float* __restrict__ lse) {
-    __shared__ float sm[16][64], ss[16][64], st[16][64];
+    __shared__ float sm[16][16], ss[16][16], st[16][16];
     const int n = piece_rows(count, p0, piece, fixed);
-    if (blockIdx.x * 64 >= n) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const long r = (long)blockIdx.x * 64 + lane;
+    if (blockIdx.x * 16 >= n) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = lane & 15;
+    const long r = (long)blockIdx.x * 16 + k;
     // a part's factor relative to the running maximum mx; a part without a column
     // (m = -inf) adds its sum as it is: 0, or the NaN of a score
     auto f = [](float m, float mx, float l2) {
         return m == -INFINITY ? 1.0f : exp2_hw(m * l2 - mx * l2);
     };
     float m = -INFINITY, s = 0.0f, t = 0.0f;
+    auto add = [&](float m1, float s1, float t1) {
+        const float mx = fmaxf(m, m1);
+        s = s * f(m, mx, kLog2e) + s1 * f(m1, mx, kLog2e);
+        if (tstat) t = t * f(m, mx, l2t) + t1 * f(m1, mx, l2t);
+        m = mx;
+    };
     if (r < n) {
 #pragma unroll 4
-        for (int q = w; q < parts; q += 16) {
+        for (int q = w * 4 + (lane >> 4); q < parts; q += 64) {
             const float2 a = stat[q * ldr + r];
-            const float mx = fmaxf(m, a.x);
-            s = s * f(m, mx, kLog2e) + a.y * f(a.x, mx, kLog2e);
-            if (tstat) t = t * f(m, mx, l2t) + tstat[q * ldr + r] * f(a.x, mx, l2t);
-            m = mx;
+            add(a.x, a.y, tstat ? tstat[q * ldr + r] : 0.0f);
         }
     }
-    sm[w][lane] = m, ss[w][lane] = s, st[w][lane] = t;
-    __syncthreads();
-    if (w != 0 || r >= n) return;
-    for (int q = 1; q < 16; ++q) m = fmaxf(m, sm[q][lane]);
-    s = 0.0f, t = 0.0f;
-    for (int q = 0; q < 16; ++q) {
-        s += ss[q][lane] * f(sm[q][lane], m, kLog2e);
-        t += st[q][lane] * f(sm[q][lane], m, l2t);
+#pragma unroll
+    for (int x = 16; x < 64; x += x) {
+        const float m1 = __shfl_xor(m, x), s1 = __shfl_xor(s, x), t1 = __shfl_xor(t, x);
+        add(m1, s1, t1);
     }
+    if (lane < 16) sm[w][k] = m, ss[w][k] = s, st[w][k] = t;
+    __syncthreads();
+    if (threadIdx.x >= 16 || r >= n) return;
+    for (int q = 1; q < 16; ++q) add(sm[q][k], ss[q][k], st[q][k]);
     const Norm2 nm = {m * kLog2e, __builtin_amdgcn_logf(s)};
     if (norm) norm[r] = nm;
     if (tnorm) tnorm[r] = {m * l2t, __builtin_amdgcn_logf(t)};
@@ -915,8 +983,7 @@ __global__ __launch_bounds__(1024) void head_lse_kernel(
 struct HeadDz {
     const float* Z;          // [piece][ldz] scores
     long ldz;
-    void* G;                 // [piece][ldg] dz: Z itself (segs = 1), or a buffer of its own
-    long ldg;                // in elements of dz
+    void* G;                 // [piece][ldz] dz
     int segs, seg;           // segments of a row, their length (a multiple of 256)
     int V;
     const int32_t* rows;
@@ -935,12 +1002,9 @@ struct HeadDz {
     int grad;
 };
 
-// One wave a row, or a segment of one when the rows are few.  The scores at the
-// label and the teacher's slots are read first and their dz is written last (an
-// entry named twice by its first slot, with the slots' q added in order); the
-// rest streams.  In place: unit c (256 elements) of the row's dz is stored after
-// units 0 .. c of z have come back, and at half the element size lies in front
-// of every unit still to be read (in fp32 in its own place).
+// One wave a row, or a segment of one when the rows are few.  The dz of the label
+// and the teacher's slots are written behind the others (an entry named twice by
+// its first slot, with the slots' q added in order).
 template <typename T>
 __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     __shared__ int s_idx[4][kMaxK];
@@ -1011,9 +1075,8 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     if (!p.grad) return;
     const float zy = label >= 0 ? z[label] : 0.0f;
     wave_lds_sync();
-    wave_mem_sync();                          // those reads are back before any store
 
-    T* g = static_cast<T*>(p.G) + (long)r * p.ldg;
+    T* g = static_cast<T*>(p.G) + (long)r * p.ldz;
     auto ce = [&](float v) { return wce * norm_p(nm, v, kLog2e); };
     auto kl = [&](float v) { return wkd * norm_p(tn, v, p.l2t); };
     auto stream = [&](auto&& dense) {
@@ -1076,22 +1139,24 @@ inline bool head_sizes_ok(int T, int d, int V, int K, moe_dtype dt) {
            V <= (1 << 20) && K >= 0 && K <= kMaxK && (dt == MOE_F32 || dt == MOE_BF16);
 }
 
-constexpr size_t kHeadLimit = (size_t)4 << 30;
-constexpr int kFewRows = 2048;         // up to here dz has a buffer of its own
+constexpr size_t kHeadLimit = (size_t)8 << 30;
+constexpr int kSubRows = 2048;         // rows whose scores are held at a time
 
+// A call takes its tokens in `pieces` of `piece` rows, whose dz (or x alone, for a
+// loss without gradient) is held at a time, and a piece in steps of `sub` rows,
+// whose scores are: 4 bytes a score for 2048 rows, 2 (fp32: 4) for the others.
 struct HeadPlan {
-    int piece, pieces, parts;
+    int piece, pieces, sub, parts;
     long ldz;
-    int dx_splits, dw_splits;
     int segs, seg;                     // of a row of dz
-    size_t rows, count, act, xc, zl, norm, tnorm, stat, tstat, z, g, dxp, acc, dwp, total;
+    size_t rows, count, plan, act, xc, zl, norm, tnorm, stat, tstat, z, g, part, acc, total;
 };
 
-// Parts of the reduction of a product with `tiles` output tiles over K:
-// enough for two rounds of the compute units, each at least 512 long.
-inline int head_splits(long tiles, long K) {
-    if (tiles >= 256 || tiles == 0) return 1;
-    return (int)std::max(1l, std::min((512 + tiles - 1) / tiles, K / 512));
+// Slots that a product with up to `tiles` tiles and K reduction steps can use
+// (no fewer for more of either, so that a workspace serves every smaller batch).
+inline long head_slots(long tiles, long K) {
+    const long parts = std::min((long)kMaxParts, (cdiv(K, 64) + 3) / 4l);
+    return parts > 1 ? std::min((long)kMaxSlots, std::min(tiles, (long)kRound - 1) * parts) : 0;
 }
 
 HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int piece) {
@@ -1101,10 +1166,12 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     const int bm = dt == MOE_BF16 ? 256 : 128, pc = dt == MOE_BF16 ? 128 : 64;
     p.piece = piece;
     p.pieces = T == 0 ? 0 : cdiv(T, piece);
+    p.sub = store ? std::min(piece, kSubRows) : piece;
     p.ldz = (long)align_up(V, 64);
     p.parts = cdiv(V, bm) * (bm / pc);
-    p.dx_splits = head_splits((long)cdiv(piece, bm) * cdiv(d, bm), V);
-    p.dw_splits = head_splits((long)cdiv(V, bm) * cdiv(d, bm), piece);
+    // about 8192 waves for a step's rows, each 2048 elements at least
+    p.seg = std::max(2048, (int)align_up(cdiv(p.ldz * p.sub, 8192), 256));
+    p.segs = cdiv(p.ldz, p.seg);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -1113,39 +1180,28 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     };
     p.rows = take((size_t)T * 4);
     p.count = take(4);
+    p.plan = take(grad ? (size_t)p.pieces * 8 : 0);
     p.act = take(K > 0 ? (size_t)T * 4 : 0);
     p.xc = take((size_t)piece * d * b);
-    p.zl = take((size_t)piece * 4);
-    p.norm = take((size_t)piece * 8);
-    p.tnorm = take(K > 0 ? (size_t)piece * 8 : 0);
-    p.stat = take((size_t)p.parts * piece * 8);
-    p.tstat = take(K > 0 ? (size_t)p.parts * piece * 4 : 0);
-    p.z = take(store ? (size_t)piece * p.ldz * 4 : 0);
-    // few rows: several waves a row, which cannot write in place
-    p.segs = 1, p.seg = (int)p.ldz;
-    if (grad && piece <= kFewRows) {
-        p.seg = std::max(2048, (int)align_up(cdiv(p.ldz * piece, 8192), 256));
-        p.segs = cdiv(p.ldz, p.seg);
-    }
-    p.g = take(grad ? (size_t)std::min(piece, kFewRows) * p.ldz * b : 0);
-    // the partial sums of dx: room for any smaller piece too (fewer tiles, more
-    // parts), so that a workspace for T tokens serves every smaller batch
-    size_t dxp = 0;
-    const int cols = cdiv(d, bm);
-    for (int u = 1; u <= cdiv(piece, bm) && u * cols < 256; ++u) {
-        const int sp = head_splits((long)u * cols, V);
-        if (sp > 1) dxp = std::max(dxp, (size_t)sp * std::min(u * bm, piece) * d * 4);
-    }
-    p.dxp = take(grad ? dxp : 0);
+    p.zl = take((size_t)p.sub * 4);
+    p.norm = take((size_t)p.sub * 8);
+    p.tnorm = take(K > 0 ? (size_t)p.sub * 8 : 0);
+    p.stat = take((size_t)p.parts * p.sub * 8);
+    p.tstat = take(K > 0 ? (size_t)p.parts * p.sub * 4 : 0);
+    p.z = take(store ? (size_t)p.sub * p.ldz * 4 : 0);
+    p.g = take(grad ? (size_t)piece * p.ldz * b : 0);
+    const long cols = cdiv(d, bm);
+    p.part = take(grad ? (size_t)std::max(head_slots(cdiv(piece, bm) * cols, V),
+                                          head_slots(cdiv(V, bm) * cols, piece)) * bm * bm * 4
+                       : 0);
     p.acc = take(grad && p.pieces > 1 ? (size_t)V * d * 4 : 0);
-    p.dwp = take(grad && p.dw_splits > 1 ? (size_t)p.dw_splits * V * d * 4 : 0);
     p.total = o;
     return p;
 }
 
-// The plan with the largest piece whose workspace stays within `limit`, or
-// the one with the smallest workspace if none does.  The fewest pieces of equal size (in whole row
-// tiles), so that the last one is not a small rest.
+// The plan with the largest piece whose workspace stays within `limit`, or the
+// one with the smallest workspace if none does.  The fewest pieces of equal size
+// (in whole row tiles), so that the last one is not a small rest.
 HeadPlan head_plan(int T, int d, int V, int K, moe_dtype dt, int grad, size_t limit) {
     const int units = std::max(1, cdiv(T, kRowAlign));
     int lo = 1, hi = units;              // pieces: the fewest that fit
@@ -1178,24 +1234,38 @@ struct HeadCall {
     void *dx, *dWv;
 };
 
-template <int BMT, int BNT, typename T>
+// Blocks of a product with up to m rows: its tiles, and the slots of its rest.
+template <int BM, typename T>
 int head_grid(HeadGemm<T>& g, long m) {
-    const long tiles = (long)cdiv(m, BMT) * cdiv(g.N, BNT) * g.splits;
+    const long tiles = (long)cdiv(m, BM) * cdiv(g.N, BM);
     g.xcd_run = 32;
+    const long blocks = g.plan ? std::max(tiles, tiles / kRound * kRound + kMaxSlots) : tiles;
     const long pad = NXCD * g.xcd_run;
-    return (int)((tiles + pad - 1) / pad * pad);
+    return (int)((blocks + pad - 1) / pad * pad);
 }
 
 template <int ALAY, int BLAY, typename T, class Epi>
 void head_product(HeadGemm<T> g, long m, const Epi& epi, hipStream_t s, const char* name) {
     if constexpr (sizeof(T) == 2) {
-        const int grid = head_grid<256, 256>(g, m);
-        MOE_LAUNCH(name, s, head_product_kernel<HEAD_BK, 320 / HEAD_BK, ALAY, BLAY, Epi>
+        const int grid = head_grid<256>(g, m);
+        MOE_LAUNCH(name, s, head_product_kernel<64, 5, ALAY, BLAY, Epi>
                    <<<grid, 256, 0, s>>>(g, epi));
     } else {
-        const int grid = head_grid<FBM, FBM>(g, m);
+        const int grid = head_grid<FBM>(g, m);
         MOE_LAUNCH(name, s, head_product_f32_kernel<ALAY, BLAY, Epi><<<grid, 256, 0, s>>>(g, epi));
     }
+}
+
+// The product and, where its rest tiles may be split, their sums.
+template <int ALAY, int BLAY, typename T, class Epi>
+void head_product_join(const HeadGemm<T>& g, long m, const Epi& epi, hipStream_t s,
+                       const char* name, const char* join) {
+    constexpr int BM = sizeof(T) == 2 ? 256 : FBM;
+    head_product<ALAY, BLAY>(g, m, epi, s, name);
+    if (!g.plan) return;
+    const long rest = std::min((long)kRound - 1, (long)cdiv(m, BM) * cdiv(g.N, BM));
+    MOE_LAUNCH(join, s, head_join_kernel<BM, BM, T, Epi>
+               <<<(int)(rest * (BM * BM / 8192)), 1024, 0, s>>>(g, epi));
 }
 
 template <typename T>
@@ -1203,15 +1273,19 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     const bool teacher = c.K > 0, store = c.grad || teacher;
     int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
     int32_t* count = reinterpret_cast<int32_t*>(ws + p.count);
+    int32_t* plan = c.grad ? reinterpret_cast<int32_t*>(ws + p.plan) : nullptr;
     float2* stat = reinterpret_cast<float2*>(ws + p.stat);
     float* tstat = teacher ? reinterpret_cast<float*>(ws + p.tstat) : nullptr;
     float* zl = reinterpret_cast<float*>(ws + p.zl);
     Norm2* norm = reinterpret_cast<Norm2*>(ws + p.norm);
     Norm2* tnorm = teacher ? reinterpret_cast<Norm2*>(ws + p.tnorm) : nullptr;
     float* Z = store ? reinterpret_cast<float*>(ws + p.z) : nullptr;
+    T* G = reinterpret_cast<T*>(ws + p.g);
+    float* part = reinterpret_cast<float*>(ws + p.part);
     T* xc = reinterpret_cast<T*>(ws + p.xc);
     const float inv_tau = 1.0f / c.tau, l2t = (float)(1.4426950408889634 / (double)c.tau);
     const int vpr = c.d * (int)sizeof(T) / 16;
+    constexpr int BM = sizeof(T) == 2 ? 256 : FBM;
     const int32_t* act = c.labels;
     int limit = c.V;
     if (teacher) {
@@ -1221,8 +1295,11 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
         act = a;
         limit = 2;
     }
+    const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM};
     MOE_LAUNCH("head_compact", s, head_compact_kernel<<<1, 1024, 0, s>>>(
-                   act, c.T, limit, rows, count, c.loss, c.lse, c.kd));
+                   act, c.T, limit, rows, count, c.loss, c.lse, c.kd, hp));
+    HeadGemm<T> g;
+    g.count = count;
     for (int i = 0; i < p.pieces; ++i) {
         const int p0 = i * p.piece, bound = std::min(p.piece, c.T - p0);
         u32x4_t* zero_dx = c.grad && c.dx && i == 0 ? static_cast<u32x4_t*>(c.dx) : nullptr;
@@ -1230,59 +1307,39 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
                    head_gather_kernel<<<cdiv((long)(zero_dx ? c.T : bound) * vpr, 256), 256, 0, s>>>(
                        static_cast<const u32x4_t*>(c.x), rows, count, p0, p.piece, vpr,
                        reinterpret_cast<u32x4_t*>(xc), act, c.T, limit, zero_dx));
-        HeadGemm<T> g;
-        g.count = count, g.p0 = p0, g.piece = p.piece;
-        g.A = xc, g.lda = c.d, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
-        g.M = bound, g.N = c.V, g.K = c.d, g.dyn = 1, g.splits = 1;
-        const EpiScores es = {c.V, stat, tstat, l2t, p.piece, c.labels, rows, p0, zl, Z, p.ldz};
-        head_product<KMAJ, KMAJ>(g, bound, es, s, "head_scores");
-        MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(bound, 64), 1024, 0, s>>>(
-                       stat, tstat, p.parts, p.piece, l2t, zl, c.labels, c.V, rows, count, 0, p0,
-                       p.piece, norm, tnorm, c.loss, c.lse));
-        if (!store) continue;
-        // dz in place of z, row by row, or in its own buffer
-        T* G = p.segs > 1 ? reinterpret_cast<T*>(ws + p.g) : reinterpret_cast<T*>(Z);
-        const long ldg = p.segs > 1 ? p.ldz : p.ldz * (4 / (long)sizeof(T));
-        const int segs = c.grad ? p.segs : 1;
-        const HeadDz dz = {Z, p.ldz, G, ldg, segs, segs > 1 ? p.seg : (int)p.ldz, c.V, rows, count,
-                           p0, p.piece, norm, tnorm, c.labels, c.weight, c.tidx, c.tlogit,
-                           c.tweight, c.K, c.tau, inv_tau, l2t, c.kd, c.grad};
-        MOE_LAUNCH("head_dz", s,
-                   head_dz_kernel<T><<<cdiv((long)bound * segs, 4), 256, 0, s>>>(dz));
+        for (int q0 = 0; q0 < bound; q0 += p.sub) {
+            const int s0 = p0 + q0, sn = std::min(p.sub, bound - q0);
+            g.A = xc + (long)q0 * c.d, g.lda = c.d, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
+            g.M = sn, g.N = c.V, g.K = c.d, g.dyn = 1, g.p0 = s0, g.piece = sn;
+            g.plan = nullptr, g.part = nullptr;
+            const EpiScores es = {c.V, stat, tstat, l2t, p.sub, c.labels, rows, s0, zl, Z, p.ldz};
+            head_product<KMAJ, KMAJ>(g, sn, es, s, "head_scores");
+            MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
+                           stat, tstat, p.parts, p.sub, l2t, zl, c.labels, c.V, rows, count, 0, s0,
+                           sn, norm, tnorm, c.loss, c.lse));
+            if (!store) continue;
+            const int segs = c.grad ? p.segs : 1;
+            const HeadDz dz = {Z, p.ldz, G + (long)q0 * p.ldz, segs, p.seg, c.V, rows, count, s0, sn,
+                               norm, tnorm, c.labels, c.weight, c.tidx, c.tlogit, c.tweight, c.K,
+                               c.tau, inv_tau, l2t, c.kd, c.grad};
+            MOE_LAUNCH("head_dz", s,
+                       head_dz_kernel<T><<<cdiv((long)sn * segs, 4), 256, 0, s>>>(dz));
+        }
         if (!c.grad) continue;
+        g.p0 = p0, g.piece = p.piece, g.part = part;
         if (c.dx) {
-            g.A = G, g.lda = ldg, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
-            g.M = bound, g.N = c.d, g.K = c.V, g.dyn = 1, g.splits = p.dx_splits;
-            T* dx = static_cast<T*>(c.dx);
-            if (p.dx_splits > 1) {
-                float* part = reinterpret_cast<float*>(ws + p.dxp);
-                const long stride = (long)p.piece * c.d;
-                head_product<KMAJ, MNMAJ>(g, bound, EpiPart{part, c.d, stride}, s, "head_dx");
-                const long n8 = (long)bound * c.d / 8;
-                MOE_LAUNCH("head_dx_join", s, head_join_kernel<T><<<cdiv(n8, 256), 256, 0, s>>>(
-                               part, p.dx_splits, stride, n8, c.d, dx, rows, nullptr, count, p0,
-                               p.piece));
-            } else {
-                head_product<KMAJ, MNMAJ>(g, bound, EpiRows<T>{dx, c.d, rows, p0}, s, "head_dx");
-            }
+            g.A = G, g.lda = p.ldz, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
+            g.M = bound, g.N = c.d, g.K = c.V, g.dyn = 1, g.plan = plan + 2 * i;
+            head_product_join<KMAJ, MNMAJ>(g, bound, EpiRows<T>{static_cast<T*>(c.dx), c.d, rows, p0},
+                                           s, "head_dx", "head_dx_join");
         }
         if (c.dWv) {
-            g.A = G, g.lda = ldg, g.B = xc, g.ldb = c.d;
-            g.M = c.V, g.N = c.d, g.K = bound, g.dyn = 2, g.splits = p.dw_splits;
-            T* dW = static_cast<T*>(c.dWv);
             float* acc = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
-            if (p.dw_splits > 1) {
-                float* part = reinterpret_cast<float*>(ws + p.dwp);
-                const long stride = (long)c.V * c.d;
-                head_product<MNMAJ, MNMAJ>(g, c.V, EpiPart{part, c.d, stride}, s, "head_dW");
-                const long n8 = stride / 8;
-                MOE_LAUNCH("head_dW_join", s, head_join_kernel<T><<<cdiv(n8, 256), 256, 0, s>>>(
-                               part, p.dw_splits, stride, n8, c.d, dW, nullptr, acc, count, p0,
-                               p.piece));
-            } else {
-                head_product<MNMAJ, MNMAJ>(g, c.V, EpiSum<T>{dW, acc, c.d, count, p0, p.piece}, s,
-                                           "head_dW");
-            }
+            g.A = G, g.lda = p.ldz, g.B = xc, g.ldb = c.d;
+            g.M = c.V, g.N = c.d, g.K = bound, g.dyn = 2, g.plan = plan + 2 * i + 1;
+            head_product_join<MNMAJ, MNMAJ>(
+                g, c.V, EpiSum<T>{static_cast<T*>(c.dWv), acc, c.d, count, p0, p.piece}, s, "head_dW",
+                "head_dW_join");
         }
     }
     return launch_status();

@@ -817,7 +817,7 @@ class HeadLoss:
     call, which like dWv the next call overwrites: two calls in flight at once
     need a HeadLoss each.  stream: a HIP stream handle, the current stream if None; the
     tensors have to be ready on it, and to be kept until the call is done.
-    limit: the workspace's size in bytes to stay within if possible (None: 4 GiB);
+    limit: the workspace's size in bytes to stay within if possible (None: 8 GiB);
     a larger one takes more tokens at a time.
     """
 
