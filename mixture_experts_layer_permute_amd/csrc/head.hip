@@ -16,8 +16,8 @@
 //               reduces every row's 128 columns to (max, sum of exp) from the
 //               fp32 accumulators, so the normaliser needs no second look at
 //               z, and z is stored (in fp32) only when something reads it;
-//  head_dz      z -> dz, a stream; the scores are held for 2048 tokens at a time
-//               (8 row tiles share a column tile's weights), dz for the piece;
+//  head_dz      z -> dz, a stream; the scores are held for up to 3072 tokens at a
+//               time (row tiles share a column tile's weights), dz for the piece;
 //  head_product dx = dz Wv and dWv = dz^T x, the tiles after the last full round
 //               of the compute units split over the reduction; dWv is summed over the
 //               pieces in fp32.
@@ -45,40 +45,45 @@ __device__ __forceinline__ void wave_mem_sync() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Sum or maximum over groups of 8 or 16 neighbouring lanes, in every lane of
-// the group: quad swaps, then the mirror of 8, then the mirror of 16 lanes
-// (mirrors, since the smaller groups' lanes agree by then).  Every lane of the
-// wave must be active.
+// Sums and maxima over lanes, in every lane of the group; every lane of the wave
+// must be active.  16 neighbouring lanes: quad swaps, then the mirror of 8, then
+// that of 16 (mirrors, since the smaller groups' lanes agree by then).  Lanes 16
+// and 32 apart: the swap of a register's halves with its own copy's.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(
         __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-template <int N>
-__device__ __forceinline__ float group_max(float v) {
+struct F2 {
+    float a, b;
+};
+__device__ __forceinline__ F2 swap16(float v) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return {__uint_as_float(s[0]), __uint_as_float(s[1])};
+}
+__device__ __forceinline__ F2 swap32(float v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return {__uint_as_float(s[0]), __uint_as_float(s[1])};
+}
+__device__ __forceinline__ float max16(float v) { const F2 s = swap16(v); return fmaxf(s.a, s.b); }
+__device__ __forceinline__ float max32(float v) { const F2 s = swap32(v); return fmaxf(s.a, s.b); }
+__device__ __forceinline__ float sum16(float v) { const F2 s = swap16(v); return s.a + s.b; }
+__device__ __forceinline__ float sum32(float v) { const F2 s = swap32(v); return s.a + s.b; }
+__device__ __forceinline__ float wave_max(float v) {
     v = fmaxf(v, dpp<0xB1>(v));                    // quad_perm 1,0,3,2
     v = fmaxf(v, dpp<0x4E>(v));                    // quad_perm 2,3,0,1
     v = fmaxf(v, dpp<0x141>(v));                   // row_half_mirror
-    if constexpr (N == 16) v = fmaxf(v, dpp<0x140>(v));   // row_mirror
-    return v;
+    v = fmaxf(v, dpp<0x140>(v));                   // row_mirror
+    return max32(max16(v));
 }
-template <int N>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float wave_sum(float v) {
     v += dpp<0xB1>(v);
     v += dpp<0x4E>(v);
     v += dpp<0x141>(v);
-    if constexpr (N == 16) v += dpp<0x140>(v);
-    return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-    v = group_max<16>(v);
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-    v = group_sum<16>(v);
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    v += dpp<0x140>(v);
+    return sum32(sum16(v));
 }
 
 // f(0), f(1), ... f(N - 1) with constants.
@@ -112,72 +117,125 @@ constexpr int kMaxParts = 32;           // of a tile
 constexpr int kMaxSlots = 768;          // rest tiles times parts
 
 // Parts of each of R rest tiles whose reduction has nj stages of 64 steps: the
-// fewest stage times over the rounds they take, with about 6 stages for a tile's
-// start and end, and a twelfth of one a slot for writing and adding it up (512 KB
-// at about 4.5 TB/s against 1.2 us a stage).
-__host__ __device__ inline int rest_parts(int R, int nj) {
+// fewest stage times over the rounds they take, with `ends` of them for a tile's
+// start and end and `slot` for writing and adding up a part.  bf16: 6 (10 us
+// against 1.2 a stage) and a twelfth (512 KB at about 4.5 TB/s); fp32: 1 and a
+// hundredth (128 KB against 3.4 us a stage).
+__host__ __device__ inline int rest_parts(int R, int nj, bool f32) {
+    const float ends = f32 ? 1.0f : 6.0f, slot = f32 ? 0.01f : 0.085f;
     int best = 1;
     float least = 1e30f;
     for (int S = 1; S <= kMaxParts && S * 4 <= nj + 3 && (S == 1 || R * S <= kMaxSlots); ++S) {
         const int rounds = (R * S + kRound - 1) / kRound;
-        const float t = rounds * ((nj + S - 1) / S + 6.0f) + (S > 1 ? 4.0f + R * S * 0.085f : 0.0f);
+        const float t = rounds * ((nj + S - 1) / S + ends) + (S > 1 ? ends + R * S * slot : 0.0f);
         if (t < least) least = t, best = S;
     }
     return best;
 }
 
-// For head_compact_kernel's last step: plan[2 piece + {0: dx, 1: dWv}] = the parts
-// of the product's rest tiles.
+// plan[2 piece + {0: dx, 1: dWv}] = the parts of the product's rest tiles.
 struct HeadParts {
     int32_t* plan;
     int pieces, piece, d, V, bm;
 };
 
-// rows[0..n) = the tokens that have a loss, in order; *count = n; the outputs
-// of the others are zero.  act: labels (limit V) or head_active's (limit 2).
-// One block: each round takes 4096 tokens, four a thread.
-__global__ __launch_bounds__(1024) void head_compact_kernel(const int32_t* __restrict__ act,
-                                                            int T, int limit,
-                                                            int32_t* __restrict__ rows,
-                                                            int32_t* __restrict__ count,
-                                                            float* __restrict__ o0,
-                                                            float* __restrict__ o1,
-                                                            float* __restrict__ o2,
-                                                            HeadParts hp) {
+// Whether token t has a loss: by its label, by its teacher's slots, or as
+// head_active_kernel found (tidx NULL, act then its flags with limit 2).
+struct HeadTokens {
+    const int32_t* act;      // labels (limit V) or flags (limit 2), or NULL
+    int limit;
+    const int32_t* tidx;     // or NULL
+    int K, V, T;
+    __device__ __forceinline__ bool has_loss(int t) const {
+        bool on = act && in_vocab(act[t], limit);
+        if (tidx)
+            for (int j = 0; j < K; ++j) on |= in_vocab(tidx[(long)t * K + j], V);
+        return on;
+    }
+};
+// What the compaction leaves besides the list: the count, zeros in the outputs
+// of the tokens without a loss, the split of the products.
+struct HeadStart {
+    int32_t* rows;
+    int32_t* count;
+    float* out[3];
+    HeadParts parts;
+    __device__ __forceinline__ void skip(int t) const {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (out[i]) out[i][t] = 0.0f;
+    }
+    __device__ __forceinline__ void finish(int n) const {
+        if (threadIdx.x == 0) *count = n;
+        for (int i = threadIdx.x; i < parts.pieces * 2; i += 1024) {
+            const int k = max(0, min(n - (i >> 1) * parts.piece, parts.piece));
+            const int nM = ((i & 1) ? parts.V + parts.bm - 1 : k + parts.bm - 1) / parts.bm;
+            const int tiles = nM * ((parts.d + parts.bm - 1) / parts.bm);
+            parts.plan[i] = rest_parts(tiles % kRound, ((i & 1) ? k + 63 : parts.V + 63) / 64,
+                                       parts.bm == 128);
+        }
+    }
+};
+constexpr int kStartTokens = 4096;      // of a block's round: four a thread
+// One round of the compaction: f(t, place) for the tokens t0 .. t0 + 4095 with a
+// loss, skip(t) for the others; returns the places used so far.
+template <class F, class G>
+__device__ __forceinline__ int compact_round(const HeadTokens& tk, int t0, int base, int* sh,
+                                             F&& f, G&& skip) {
+    const int t = t0 + threadIdx.x * 4;
+    bool on[4];
+    int c = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        on[q] = t + q < tk.T && tk.has_loss(t + q);
+        c += on[q];
+    }
+    int total;
+    int at = base + block_excl_scan<1024>(c, sh, &total);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (on[q]) f(t + q, at++);
+        else if (t + q < tk.T) skip(t + q);
+    }
+    return base + total;
+}
+
+// rows[0..n) = the tokens that have a loss, in order.  One block.
+__global__ __launch_bounds__(1024) void head_compact_kernel(HeadTokens tk, HeadStart st) {
     __shared__ int sh[16];
-    int base = 0;
-    for (int t0 = 0; t0 < T; t0 += 4096) {
-        const int t = t0 + threadIdx.x * 4;
-        bool on[4];
-        int c = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            on[q] = t + q < T && in_vocab(act[min(t + q, T - 1)], limit);
-            c += on[q];
-        }
-        int total;
-        int at = base + block_excl_scan<1024>(c, sh, &total);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (on[q]) {
-                MOE_DASSERT(at >= 0 && at < T);
-                rows[at++] = t + q;
-            } else if (t + q < T) {
-                if (o0) o0[t + q] = 0.0f;
-                if (o1) o1[t + q] = 0.0f;
-                if (o2) o2[t + q] = 0.0f;
-            }
-        }
-        base += total;
+    int n = 0;
+    for (int t0 = 0; t0 < tk.T; t0 += kStartTokens)
+        n = compact_round(tk, t0, n, sh, [&](int t, int at) {
+            MOE_DASSERT(at >= 0 && at < tk.T);
+            st.rows[at] = t;
+        }, [&](int t) { st.skip(t); });
+    st.finish(n);
+}
+
+// For up to 4096 tokens: the same and the row copies (head_gather) in one launch.
+// Every block makes the whole list, in LDS; block 0 writes it out.
+__global__ __launch_bounds__(1024) void head_start_kernel(HeadTokens tk, HeadStart st,
+                                                          const u32x4_t* __restrict__ x, int vpr,
+                                                          u32x4_t* __restrict__ xc,
+                                                          u32x4_t* __restrict__ dx) {
+    __shared__ int sh[16];
+    __shared__ int list[kStartTokens];
+    const bool first = blockIdx.x == 0;
+    const int n = compact_round(tk, 0, 0, sh, [&](int t, int at) {
+        MOE_DASSERT(at >= 0 && at < tk.T);
+        list[at] = t;
+        if (first) st.rows[at] = t;
+    }, [&](int t) { if (first) st.skip(t); });
+    __syncthreads();
+    if (first) st.finish(n);
+    const int step = gridDim.x * 1024;
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < n * vpr; i += step) {
+        const int r = i / vpr, c = i - r * vpr;
+        xc[i] = x[(long)list[r] * vpr + c];
     }
-    if (threadIdx.x == 0) *count = base;
-    // how the products of each piece are split
-    for (int i = threadIdx.x; i < hp.pieces * 2; i += 1024) {
-        const int n = max(0, min(base - (i >> 1) * hp.piece, hp.piece));
-        const int nM = ((i & 1) ? hp.V + hp.bm - 1 : n + hp.bm - 1) / hp.bm;
-        const int tiles = nM * ((hp.d + hp.bm - 1) / hp.bm);
-        hp.plan[i] = rest_parts(tiles % kRound, ((i & 1) ? n + 63 : hp.V + 63) / 64);
-    }
+    if (!dx || n == tk.T) return;
+    for (int i = blockIdx.x * 1024 + threadIdx.x; i < tk.T * vpr; i += step)
+        if (!tk.has_loss(i / vpr)) dx[i] = u32x4_t{0, 0, 0, 0};
 }
 
 // The active rows of one piece (of `piece` rows from compacted row p0 on).
@@ -191,17 +249,17 @@ __device__ __forceinline__ int piece_rows(const int32_t* count, int p0, int piec
 __global__ __launch_bounds__(256) void head_gather_kernel(
     const u32x4_t* __restrict__ x, const int32_t* __restrict__ rows,
     const int32_t* __restrict__ count, int p0, int piece, int vpr, u32x4_t* __restrict__ xc,
-    const int32_t* __restrict__ act, int T, int limit, u32x4_t* __restrict__ dx) {
+    HeadTokens tk, u32x4_t* __restrict__ dx) {
     const int n = piece_rows(count, p0, piece, 0);
     const long i = (long)blockIdx.x * 256 + threadIdx.x;
     const long r = i / vpr;
     const int c = (int)(i - r * vpr);
     if (r < n) {
         const int t = rows[p0 + r];
-        MOE_DASSERT(t >= 0 && t < T);
+        MOE_DASSERT(t >= 0 && t < tk.T);
         xc[r * vpr + c] = x[(long)t * vpr + c];
     }
-    if (dx && r < T && !in_vocab(act[r], limit)) dx[r * vpr + c] = u32x4_t{0, 0, 0, 0};
+    if (dx && r < tk.T && !tk.has_loss((int)r)) dx[r * vpr + c] = u32x4_t{0, 0, 0, 0};
 }
 
 __global__ __launch_bounds__(256) void head_zero_kernel(u32x4_t* __restrict__ p, long n) {
@@ -289,14 +347,8 @@ struct Quads16 {
     static constexpr int WIDTH = 128;
     static __device__ __forceinline__ int col(int q) { return q * 16 + ((threadIdx.x >> 4) & 3) * 4; }
     static __device__ __forceinline__ bool first() { return (threadIdx.x & 48) == 0; }
-    static __device__ __forceinline__ float max(float v) {
-        v = fmaxf(v, __shfl_xor(v, 16));
-        return fmaxf(v, __shfl_xor(v, 32));
-    }
-    static __device__ __forceinline__ float sum(float v) {
-        v += __shfl_xor(v, 16);
-        return v + __shfl_xor(v, 32);
-    }
+    static __device__ __forceinline__ float max(float v) { return max32(max16(v)); }
+    static __device__ __forceinline__ float sum(float v) { return sum32(sum16(v)); }
 };
 struct Quads32 {
     static constexpr int WIDTH = 64;
@@ -304,8 +356,8 @@ struct Quads32 {
         return (q >> 2) * 32 + (q & 3) * 8 + ((threadIdx.x >> 5) & 1) * 4;
     }
     static __device__ __forceinline__ bool first() { return (threadIdx.x & 32) == 0; }
-    static __device__ __forceinline__ float max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
-    static __device__ __forceinline__ float sum(float v) { return v + __shfl_xor(v, 32); }
+    static __device__ __forceinline__ float max(float v) { return max32(v); }
+    static __device__ __forceinline__ float sum(float v) { return sum32(v); }
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -318,10 +370,10 @@ __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2
 struct EpiScores {
     static constexpr bool kSplits = false;
     int V;
-    float2* stat;            // [parts][ldr] (m, sum)
-    float* tstat;            // [parts][ldr] sum at the temperature, or NULL
+    float2* stat;            // (m, sum) of a row's part: part * sp + row * sr
+    float* tstat;            // the sum at the temperature likewise, or NULL
+    long sp, sr;
     float l2t;               // L / tau
-    long ldr;
     const int32_t* labels;   // or NULL
     const int32_t* rows;     // compacted row -> token, or NULL: the row itself
     int p0;
@@ -372,7 +424,7 @@ struct EpiScores {
 #pragma unroll
             for (int u = 0; u < 4; ++u) s += exp2_hw(fmaf(v[q][u], kLog2e, -m2));
         s = Lanes::sum(s);
-        const long at = (long)(col / Lanes::WIDTH) * ldr + r;
+        const long at = (long)(col / Lanes::WIDTH) * sp + r * sr;
         if (tstat) {
             const float mt = ref * l2t;
             float t = 0.0f;
@@ -511,9 +563,9 @@ __device__ __forceinline__ bool piece_done(const HeadGemm<T>& p) {
 //    takes 4 reduction steps x 16 columns per 16 lanes; chunk c of step k at c ^
 //    4 (k mod 4) ^ 2 (k/8 mod 2): the four steps of a group and the two groups
 //    of half a wave lie in distinct banks.
-template <int LAY, int BK, int NW>
+template <int LAY, int BK, int NW, int ROWS = 256>
 struct HeadOperand {
-    static constexpr int ROWS = 256;
+    static_assert(LAY == KMAJ || ROWS == 256, "32 chunks a row of M/N-major units");
     static constexpr int CH = BK / 8;
     static constexpr int UNIT = ROWS * BK * 2;
     static constexpr int NLOAD = UNIT / 1024 / NW;
@@ -755,32 +807,76 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
         if (j < nj) stage(I0{}, j);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // (loads of the empty stages)
-    unroll<8>([&](auto I) { mfma_done(acc[I]); });
-    if (Epi::kSplits && ti.slot >= 0) {
-        unroll<8>([&](auto I) {
-            store_part<Quads16, 256, 256>(p.part, ti, wm * 128 + I * 16 + (lane & 15), wn * 128,
-                                          acc[I]);
-        });
-        return;
-    }
+    // (a row of fragments at a time, so that the others stay where they are)
+    const bool part = Epi::kSplits && ti.slot >= 0;
     unroll<8>([&](auto I) {
-        epi.template row<Quads16>(ti, wm * 128 + I * 16 + (lane & 15), wn * 128, acc[I]);
+        mfma_done(acc[I]);
+        const int rl = wm * 128 + I * 16 + (lane & 15);
+        if (part) store_part<Quads16, 256, 256>(p.part, ti, rl, wn * 128, acc[I]);
+        else epi.template row<Quads16>(ti, rl, wn * 128, acc[I]);
+        __builtin_amdgcn_sched_barrier(0);
     });
 }
 
-// fp32: 128 x 128 tiles, 4 waves of 64 x 64, v_mfma_f32_32x32x2_f32; tiles
-// staged through registers into k-major LDS, the next ones loaded during the
-// products of these.
-constexpr int FBM = 128, FBK = 16;
+// fp32: 128 x 128 tiles, 4 waves of 64 x 64, v_mfma_f32_32x32x2_f32, two
+// workgroups a compute unit.  The operands' units are those of the bf16 products
+// with an element as two: K-major 128 rows of 32 steps (128 bytes), M/N-major 32
+// steps of 128 elements.  A matrix instruction takes one step from each half of
+// the wave; the halves take steps 0-3 and 4-7 of every eight, so that K-major
+// operands are read four steps at a time.  The matrix pipe is busy for 4096 cycles a
+// stage of 32 KB: two stages in LDS, the compiler's order of instructions.
+constexpr int FBM = 128, FBK = 32;
+template <int LAY>
+struct HeadOperandF32 : HeadOperand<LAY, LAY == KMAJ ? 64 : 32, 4, LAY == KMAJ ? 128 : 256> {
+    typedef HeadOperand<LAY, LAY == KMAJ ? 64 : 32, 4, LAY == KMAJ ? 128 : 256> Base;
+    int w0;
+    __device__ __forceinline__ void init(const float* P, long ld, int rows, int k_lim, int w0_) {
+        Base::init(reinterpret_cast<const bf16_t*>(P), ld * 2, LAY == KMAJ ? rows : rows * 2, k_lim,
+                   0);
+        w0 = w0_;
+    }
+    __device__ __forceinline__ i32x4_t words32(int k0, bool some) const {
+        return Base::words(LAY == KMAJ ? (long)k0 * 2 : (long)k0, some);
+    }
+    // four steps (4 (lane / 32) on of the eight 8 b on) of row 32 i + lane % 32
+    __device__ __forceinline__ f32x4 read4(uint32_t u, int i, int b) const {
+        const int lane = threadIdx.x & 63, h = lane >> 5, r = w0 + i * 32 + (lane & 31);
+        if constexpr (LAY == KMAJ) {
+            const uint32_t o = u + r * 128 + (((2 * b + h) ^ ((r ^ (r >> 3)) & 7)) << 4);
+            return __builtin_bit_cast(f32x4, *reinterpret_cast<typename Base::lds_u32x4_t*>(o));
+        } else {
+            typedef __attribute__((address_space(3))) const float lds_f32_t;
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = 8 * b + 4 * h + e;
+                v[e] = *reinterpret_cast<lds_f32_t*>(u + k * 512 + (Base::mn_swz(k, r >> 2) << 4) +
+                                                     (r & 3) * 4);
+            }
+            return v;
+        }
+    }
+};
+
 template <int ALAY, int BLAY, class Epi>
 __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float> p, Epi epi) {
-    constexpr int LDT = FBM + 4;
-    __shared__ __attribute__((aligned(16))) float lds[2 * 2 * FBK * LDT];
+    constexpr int UNIT = 16384, STAGE = 2 * UNIT;
+    __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[2 * STAGE];
     if (piece_done(p)) return;
     const HeadTile ti = head_tile<FBM, FBM>(p);
     if (!ti.live) return;
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int wm = wv >> 1, wn = wv & 1;
+    typedef HeadOperandF32<ALAY> OpA;
+    typedef HeadOperandF32<BLAY> OpB;
+    constexpr int NL = OpA::NLOAD;
+    static_assert(NL == 4 && OpB::NLOAD == 4, "16 KB units");
+    OpA opA;
+    OpB opB;
+    opA.init(p.A + (ALAY == KMAJ ? (long)ti.m0 * p.lda : (long)ti.m0), p.lda, ti.rows, ti.k1,
+             wm * 64);
+    opB.init(p.B + (BLAY == KMAJ ? (long)ti.n0 * p.ldb : (long)ti.n0), p.ldb, ti.cols, ti.k1,
+             wn * 64);
     f32x16 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -788,80 +884,38 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    // two 16-byte vectors of each operand's stage a thread
-    float4 ra[2], rb[2];
-    auto load = [&](const float* P, long ld, int lay, int lim, int k, float4* r) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int i = tid + 256 * u;
-            float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (lay == KMAJ) {
-                const int row = i >> 2, kk = k + (i & 3) * 4;
-                if (row < lim && kk < ti.k1) {
-                    const float4 v = *reinterpret_cast<const float4*>(P + row * ld + kk);
-                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                }
-            } else {
-                const int kk = k + (i >> 5), c = (i & 31) * 4;
-                if (kk < ti.k1 && c < lim) {
-                    const float4 v = *reinterpret_cast<const float4*>(P + kk * ld + c);
-                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-                }
-            }
-            r[u] = make_float4(w[0], w[1], w[2], w[3]);
-        }
-    };
-    auto store = [&](float* s, int lay, const float4* r) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int i = tid + 256 * u;
-            if (lay == KMAJ) {
-                const int row = i >> 2, kk = (i & 3) * 4;
-                s[(kk + 0) * LDT + row] = r[u].x;
-                s[(kk + 1) * LDT + row] = r[u].y;
-                s[(kk + 2) * LDT + row] = r[u].z;
-                s[(kk + 3) * LDT + row] = r[u].w;
-            } else {
-                *reinterpret_cast<float4*>(s + (i >> 5) * LDT + (i & 31) * 4) = r[u];
-            }
-        }
-    };
-    const float* A = p.A + (ALAY == KMAJ ? (long)ti.m0 * p.lda : (long)ti.m0);
-    const float* B = p.B + (BLAY == KMAJ ? (long)ti.n0 * p.ldb : (long)ti.n0);
     const int nj = (ti.k1 - ti.k0 + FBK - 1) / FBK;
-    auto bufA = [&](int b) { return lds + b * 2 * FBK * LDT; };
-    auto bufB = [&](int b) { return lds + (b * 2 + 1) * FBK * LDT; };
-    if (nj > 0) {
-        load(A, p.lda, ALAY, ti.rows, ti.k0, ra);
-        load(B, p.ldb, BLAY, ti.cols, ti.k0, rb);
-        store(bufA(0), ALAY, ra);
-        store(bufB(0), BLAY, rb);
-        __syncthreads();
-    }
+    const uint32_t ring0 = lds_addr(ringbuf);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(ring0 + wv * 1024);
+    auto issue = [&](int j) {
+        const i32x4_t ra = opA.words32(ti.k0 + j * FBK, true);
+        const i32x4_t rb = opB.words32(ti.k0 + j * FBK, true);
+        const uint32_t at = lds0 + (uint32_t)((j & 1) * STAGE);
+        unroll<NL>([&](auto I) { opA.template load<decltype(I)::value>(ra, at); });
+        unroll<NL>([&](auto I) { opB.template load<decltype(I)::value>(rb, at + UNIT); });
+    };
+    if (nj > 0) issue(0);
 #pragma unroll 1
     for (int j = 0; j < nj; ++j) {
-        const bool more = j + 1 < nj;
-        if (more) {
-            load(A, p.lda, ALAY, ti.rows, ti.k0 + (j + 1) * FBK, ra);
-            load(B, p.ldb, BLAY, ti.cols, ti.k0 + (j + 1) * FBK, rb);
-        }
-        const float* sa = bufA(j & 1) + wm * 64 + (lane & 31);
-        const float* sb = bufB(j & 1) + wn * 64 + (lane & 31);
+        stage_barrier<0>();            // stage j landed, stage j - 1 read by every wave
+        if (j + 1 < nj) issue(j + 1);
+        const uint32_t u = ring0 + (uint32_t)((j & 1) * STAGE);
 #pragma unroll
-        for (int kk = 0; kk < FBK; kk += 2) {
-            const int o = (kk + (lane >> 5)) * LDT;
-            const float a0 = sa[o], a1 = sa[o + 32], b0 = sb[o], b1 = sb[o + 32];
-            acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a0, acc[0][0], 0, 0, 0);
-            acc[0][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a0, acc[0][1], 0, 0, 0);
-            acc[1][0] = __builtin_amdgcn_mfma_f32_32x32x2f32(b0, a1, acc[1][0], 0, 0, 0);
-            acc[1][1] = __builtin_amdgcn_mfma_f32_32x32x2f32(b1, a1, acc[1][1], 0, 0, 0);
+        for (int b = 0; b < 4; ++b) {
+            f32x4 a[2], c[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) a[i] = opA.read4(u, i, b), c[i] = opB.read4(u + UNIT, i, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)        // (columns as rows)
+                        acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x2f32(c[k][e], a[i][e], acc[i][k],
+                                                                        0, 0, 0);
         }
-        if (more) {                    // the other buffer: read two stages ago
-            store(bufA((j + 1) & 1), ALAY, ra);
-            store(bufB((j + 1) & 1), BLAY, rb);
-        }
-        __syncthreads();
     }
+    // 32 x 32 fragments: row = lane % 32, four columns by register and lane / 32
     unroll<2>([&](auto I) {
         f32x4 v[8];
 #pragma unroll
@@ -925,57 +979,56 @@ __device__ __forceinline__ float norm_p(Norm2 n, float z, float l2) {
     return exp2_hw(fmaf(z, l2, -n.a) - n.b);
 }
 
-// The normalisers of a piece's rows from the parts: 16 rows a block, 64 threads
-// share a row's parts.  The loss of a labelled row goes to its token.
+// A part's factor relative to the maximum mx: 2^(m' - mx'), m' as in the sums; a
+// part without a column (m = -inf) adds its sum as it is: 0, or the NaN of a score.
+__device__ __forceinline__ float part_factor(float m, float mx, float l2) {
+    return m == -INFINITY ? 1.0f : exp2_hw(m * l2 - mx * l2);
+}
+
+// A loss without gradient: lse of every row from its parts, 16 rows a block, 64
+// threads share a row's parts; loss and lse go to the row's token.
 __global__ __launch_bounds__(1024) void head_lse_kernel(
-    const float2* __restrict__ stat, const float* __restrict__ tstat, int parts, long ldr,
-    float l2t, const float* __restrict__ zl, const int32_t* __restrict__ labels, int V,
-    const int32_t* __restrict__ rows, const int32_t* __restrict__ count, int fixed, int p0,
-    int piece, Norm2* __restrict__ norm, Norm2* __restrict__ tnorm, float* __restrict__ loss,
+    const float2* __restrict__ stat, int parts, long ldr, const float* __restrict__ zl,
+    const int32_t* __restrict__ labels, int V, const int32_t* __restrict__ rows,
+    const int32_t* __restrict__ count, int p0, int piece, float* __restrict__ loss,
     float* __restrict__ lse) {
-    __shared__ float sm[16][16], ss[16][16], st[16][16];
-    const int n = piece_rows(count, p0, piece, fixed);
+    __shared__ float sm[16][16], ss[16][16];
+    const int n = piece_rows(count, p0, piece, piece);
     if (blockIdx.x * 16 >= n) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, k = lane & 15;
     const long r = (long)blockIdx.x * 16 + k;
-    // a part's factor relative to the running maximum mx; a part without a column
-    // (m = -inf) adds its sum as it is: 0, or the NaN of a score
-    auto f = [](float m, float mx, float l2) {
-        return m == -INFINITY ? 1.0f : exp2_hw(m * l2 - mx * l2);
-    };
-    float m = -INFINITY, s = 0.0f, t = 0.0f;
-    auto add = [&](float m1, float s1, float t1) {
+    float m = -INFINITY, s = 0.0f;
+    auto add = [&](float m1, float s1) {
         const float mx = fmaxf(m, m1);
-        s = s * f(m, mx, kLog2e) + s1 * f(m1, mx, kLog2e);
-        if (tstat) t = t * f(m, mx, l2t) + t1 * f(m1, mx, l2t);
+        s = s * part_factor(m, mx, kLog2e) + s1 * part_factor(m1, mx, kLog2e);
         m = mx;
     };
     if (r < n) {
 #pragma unroll 4
         for (int q = w * 4 + (lane >> 4); q < parts; q += 64) {
             const float2 a = stat[q * ldr + r];
-            add(a.x, a.y, tstat ? tstat[q * ldr + r] : 0.0f);
+            add(a.x, a.y);
         }
     }
-#pragma unroll
-    for (int x = 16; x < 64; x += x) {
-        const float m1 = __shfl_xor(m, x), s1 = __shfl_xor(s, x), t1 = __shfl_xor(t, x);
-        add(m1, s1, t1);
+    {
+        const F2 m1 = swap16(m), s1 = swap16(s);
+        m = m1.a, s = s1.a;
+        add(m1.b, s1.b);
     }
-    if (lane < 16) sm[w][k] = m, ss[w][k] = s, st[w][k] = t;
+    {
+        const F2 m1 = swap32(m), s1 = swap32(s);
+        m = m1.a, s = s1.a;
+        add(m1.b, s1.b);
+    }
+    if (lane < 16) sm[w][k] = m, ss[w][k] = s;
     __syncthreads();
     if (threadIdx.x >= 16 || r >= n) return;
-    for (int q = 1; q < 16; ++q) add(sm[q][k], ss[q][k], st[q][k]);
-    const Norm2 nm = {m * kLog2e, __builtin_amdgcn_logf(s)};
-    if (norm) norm[r] = nm;
-    if (tnorm) tnorm[r] = {m * l2t, __builtin_amdgcn_logf(t)};
+    for (int q = 1; q < 16; ++q) add(sm[q][k], ss[q][k]);
     const int tok = rows ? rows[p0 + r] : (int)r;
-    if (labels) {
-        const bool on = in_vocab(labels[tok], V);
-        const float l = norm_ln(nm, m, 1.0f, kLog2e);
-        if (loss) loss[tok] = on ? l - zl[r] : 0.0f;
-        if (lse) lse[tok] = on ? l : 0.0f;
-    }
+    const bool on = in_vocab(labels[tok], V);
+    const float l = norm_ln({m * kLog2e, __builtin_amdgcn_logf(s)}, m, 1.0f, kLog2e);
+    loss[tok] = on ? l - zl[r] : 0.0f;
+    if (lse) lse[tok] = on ? l : 0.0f;
 }
 
 // ----------------------------------------------------------------- dz
@@ -989,8 +1042,10 @@ struct HeadDz {
     const int32_t* rows;
     const int32_t* count;
     int p0, piece;
-    const Norm2* norm;       // of the row, and at the temperature
-    const Norm2* tnorm;
+    const float2* stat;      // [piece][parts] the scores' statistics
+    const float* tstat;
+    int parts;
+    float *loss, *lse;       // [T] or NULL
     const int32_t* labels;   // or NULL
     const float* weight;     // [T] or NULL: 1
     const int32_t* tidx;     // [T,K] or NULL
@@ -1020,16 +1075,31 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     int label = p.labels ? p.labels[t] : -1;
     if (!in_vocab(label, p.V)) label = -1;
     const float wce = label >= 0 ? (p.weight ? p.weight[t] : 1.0f) : 0.0f;
-    const Norm2 nm = p.norm[r];
+    // the row's normaliser (and that at the temperature) from its parts
+    float m = -INFINITY;
+    const float2* sp = p.stat + (long)r * p.parts;
+    for (int j = lane; j < p.parts; j += 64) m = fmaxf(m, sp[j].x);
+    m = wave_max(m);
+    float s = 0.0f, st = 0.0f;
+    for (int j = lane; j < p.parts; j += 64) {
+        const float2 a = sp[j];
+        s += a.y * part_factor(a.x, m, kLog2e);
+        if (p.tstat) st += p.tstat[(long)r * p.parts + j] * part_factor(a.x, m, p.l2t);
+    }
+    const Norm2 nm = {m * kLog2e, __builtin_amdgcn_logf(wave_sum(s))};
+    const Norm2 tn = {m * p.l2t, p.tstat ? __builtin_amdgcn_logf(wave_sum(st)) : 0.0f};
+    if (p.loss && part == 0 && lane == 0) {
+        const float l = norm_ln(nm, m, 1.0f, kLog2e);
+        p.loss[t] = label >= 0 ? l - z[label] : 0.0f;
+        if (p.lse) p.lse[t] = label >= 0 ? l : 0.0f;
+    }
 
     // the teacher's distribution
     constexpr int PL = kMaxK / 64;
     int idx[PL];
     float q[PL], zt[PL];
     float wkd = 0.0f;
-    Norm2 tn = {0.0f, 0.0f};
     if (p.tidx) {
-        tn = p.tnorm[r];
         float hi = -INFINITY;
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
@@ -1140,16 +1210,18 @@ inline bool head_sizes_ok(int T, int d, int V, int K, moe_dtype dt) {
 }
 
 constexpr size_t kHeadLimit = (size_t)8 << 30;
-constexpr int kSubRows = 2048;         // rows whose scores are held at a time
+constexpr int kSubUnits = 12;          // row tiles whose scores are held at a time, at most
 
 // A call takes its tokens in `pieces` of `piece` rows, whose dz (or x alone, for a
-// loss without gradient) is held at a time, and a piece in steps of `sub` rows,
-// whose scores are: 4 bytes a score for 2048 rows, 2 (fp32: 4) for the others.
+// loss without gradient) is held at a time, and a piece in steps of `sub`
+// rows, whose scores are: 4 bytes a score for 3072 rows at most, 2 (fp32: 4) for
+// the others.
 struct HeadPlan {
     int piece, pieces, sub, parts;
     long ldz;
     int segs, seg;                     // of a row of dz
-    size_t rows, count, plan, act, xc, zl, norm, tnorm, stat, tstat, z, g, part, acc, total;
+    size_t rows, count, plan, act, xc, zl, stat, tstat, z, g, part, acc, total;
+    bool direct, slots_dx, slots_dw;   // x as it is; products that may be split
 };
 
 // Slots that a product with up to `tiles` tiles and K reduction steps can use
@@ -1166,7 +1238,21 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     const int bm = dt == MOE_BF16 ? 256 : 128, pc = dt == MOE_BF16 ? 128 : 64;
     p.piece = piece;
     p.pieces = T == 0 ? 0 : cdiv(T, piece);
-    p.sub = store ? std::min(piece, kSubRows) : piece;
+    // steps of 6 to 12 row tiles, of those the ones that leave the fewest rounds of
+    // tiles partly empty (8192 tokens, 50257 entries: 9 row tiles 25 rounds, 8 28)
+    const int units = cdiv(piece, kRowAlign), most = std::min(units, kSubUnits);
+    int su = most;
+    auto rounds = [&](int u) {
+        auto of = [&](int n) {
+            return cdiv((long)cdiv((long)n * kRowAlign, bm) * cdiv(V, bm), kRound);
+        };
+        return units / u * of(u) + (units % u ? of(units % u) : 0);
+    };
+    for (int u = most - 1; u >= 6; --u)
+        if (rounds(u) < rounds(su)) su = u;
+    p.sub = store ? std::min(piece, su * kRowAlign) : piece;
+    // buffers for the longest step, as a smaller batch may choose it
+    const size_t rmax = store ? std::min(piece, kSubUnits * kRowAlign) : piece;
     p.ldz = (long)align_up(V, 64);
     p.parts = cdiv(V, bm) * (bm / pc);
     // about 8192 waves for a step's rows, each 2048 elements at least
@@ -1182,18 +1268,19 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     p.count = take(4);
     p.plan = take(grad ? (size_t)p.pieces * 8 : 0);
     p.act = take(K > 0 ? (size_t)T * 4 : 0);
-    p.xc = take((size_t)piece * d * b);
-    p.zl = take((size_t)p.sub * 4);
-    p.norm = take((size_t)p.sub * 8);
-    p.tnorm = take(K > 0 ? (size_t)p.sub * 8 : 0);
-    p.stat = take((size_t)p.parts * p.sub * 8);
-    p.tstat = take(K > 0 ? (size_t)p.parts * p.sub * 4 : 0);
-    p.z = take(store ? (size_t)p.sub * p.ldz * 4 : 0);
+    // a row tile's worth of tokens and no gradient: every token is scored
+    p.direct = !store && T <= kRowAlign;
+    p.xc = take(p.direct ? 0 : (size_t)piece * d * b);
+    p.zl = take(rmax * 4);
+    p.stat = take(rmax * p.parts * 8);
+    p.tstat = take(K > 0 ? rmax * p.parts * 4 : 0);
+    p.z = take(store ? rmax * p.ldz * 4 : 0);
     p.g = take(grad ? (size_t)piece * p.ldz * b : 0);
     const long cols = cdiv(d, bm);
-    p.part = take(grad ? (size_t)std::max(head_slots(cdiv(piece, bm) * cols, V),
-                                          head_slots(cdiv(V, bm) * cols, piece)) * bm * bm * 4
-                       : 0);
+    const long sx = head_slots(cdiv(piece, bm) * cols, V);
+    const long sw = head_slots(cdiv(V, bm) * cols, piece);
+    p.slots_dx = sx > 0, p.slots_dw = sw > 0;
+    p.part = take(grad ? (size_t)std::max(sx, sw) * bm * bm * 4 : 0);
     p.acc = take(grad && p.pieces > 1 ? (size_t)V * d * 4 : 0);
     p.total = o;
     return p;
@@ -1277,8 +1364,6 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     float2* stat = reinterpret_cast<float2*>(ws + p.stat);
     float* tstat = teacher ? reinterpret_cast<float*>(ws + p.tstat) : nullptr;
     float* zl = reinterpret_cast<float*>(ws + p.zl);
-    Norm2* norm = reinterpret_cast<Norm2*>(ws + p.norm);
-    Norm2* tnorm = teacher ? reinterpret_cast<Norm2*>(ws + p.tnorm) : nullptr;
     float* Z = store ? reinterpret_cast<float*>(ws + p.z) : nullptr;
     T* G = reinterpret_cast<T*>(ws + p.g);
     float* part = reinterpret_cast<float*>(ws + p.part);
@@ -1286,42 +1371,65 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     const float inv_tau = 1.0f / c.tau, l2t = (float)(1.4426950408889634 / (double)c.tau);
     const int vpr = c.d * (int)sizeof(T) / 16;
     constexpr int BM = sizeof(T) == 2 ? 256 : FBM;
-    const int32_t* act = c.labels;
-    int limit = c.V;
-    if (teacher) {
-        int32_t* a = reinterpret_cast<int32_t*>(ws + p.act);
-        MOE_LAUNCH("head_active", s, head_active_kernel<<<cdiv(c.T, 4), 256, 0, s>>>(
-                       c.labels, c.tidx, c.T, c.K, c.V, a));
-        act = a;
-        limit = 2;
-    }
-    const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM};
-    MOE_LAUNCH("head_compact", s, head_compact_kernel<<<1, 1024, 0, s>>>(
-                   act, c.T, limit, rows, count, c.loss, c.lse, c.kd, hp));
     HeadGemm<T> g;
-    g.count = count;
+    g.count = p.direct ? nullptr : count;
+    if (!p.direct) {
+        HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.K, c.V, c.T};
+        const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM};
+        const HeadStart st = {rows, count, {c.loss, c.lse, c.kd}, hp};
+        u32x4_t* dx0 = c.grad ? static_cast<u32x4_t*>(c.dx) : nullptr;
+        // (a thread of the compaction looks at its tokens' slots itself: few)
+        if (teacher && (long)c.T * c.K > 16384) {
+            int32_t* a = reinterpret_cast<int32_t*>(ws + p.act);
+            MOE_LAUNCH("head_active", s, head_active_kernel<<<cdiv(c.T, 4), 256, 0, s>>>(
+                           c.labels, c.tidx, c.T, c.K, c.V, a));
+            tk.act = a, tk.limit = 2, tk.tidx = nullptr;
+        }
+        if (c.T <= kStartTokens && p.pieces == 1) {
+            const int blocks = std::max(1, std::min(256, cdiv((long)c.T * vpr, 1024)));
+            MOE_LAUNCH("head_start", s, head_start_kernel<<<blocks, 1024, 0, s>>>(
+                           tk, st, static_cast<const u32x4_t*>(c.x), vpr,
+                           reinterpret_cast<u32x4_t*>(xc), dx0));
+        } else {
+            MOE_LAUNCH("head_compact", s, head_compact_kernel<<<1, 1024, 0, s>>>(tk, st));
+        }
+    }
     for (int i = 0; i < p.pieces; ++i) {
         const int p0 = i * p.piece, bound = std::min(p.piece, c.T - p0);
-        u32x4_t* zero_dx = c.grad && c.dx && i == 0 ? static_cast<u32x4_t*>(c.dx) : nullptr;
-        MOE_LAUNCH("head_gather", s,
-                   head_gather_kernel<<<cdiv((long)(zero_dx ? c.T : bound) * vpr, 256), 256, 0, s>>>(
-                       static_cast<const u32x4_t*>(c.x), rows, count, p0, p.piece, vpr,
-                       reinterpret_cast<u32x4_t*>(xc), act, c.T, limit, zero_dx));
+        if (!p.direct && (c.T > kStartTokens || p.pieces > 1)) {
+            u32x4_t* dx0 = c.grad && i == 0 ? static_cast<u32x4_t*>(c.dx) : nullptr;
+            HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.K, c.V, c.T};
+            if (teacher && (long)c.T * c.K > 16384) {
+                tk.act = reinterpret_cast<int32_t*>(ws + p.act);
+                tk.limit = 2, tk.tidx = nullptr;
+            }
+            MOE_LAUNCH("head_gather", s,
+                       head_gather_kernel<<<cdiv((long)(dx0 ? c.T : bound) * vpr, 256), 256, 0, s>>>(
+                           static_cast<const u32x4_t*>(c.x), rows, count, p0, p.piece, vpr,
+                           reinterpret_cast<u32x4_t*>(xc), tk, dx0));
+        }
         for (int q0 = 0; q0 < bound; q0 += p.sub) {
             const int s0 = p0 + q0, sn = std::min(p.sub, bound - q0);
-            g.A = xc + (long)q0 * c.d, g.lda = c.d, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
+            g.A = p.direct ? static_cast<const T*>(c.x) : xc + (long)q0 * c.d;
+            g.lda = c.d, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
             g.M = sn, g.N = c.V, g.K = c.d, g.dyn = 1, g.p0 = s0, g.piece = sn;
             g.plan = nullptr, g.part = nullptr;
-            const EpiScores es = {c.V, stat, tstat, l2t, p.sub, c.labels, rows, s0, zl, Z, p.ldz};
+            // statistics by row for head_dz, by part for head_lse; the label's score
+            // comes from z where that is kept
+            const EpiScores es = {c.V, stat, tstat, store ? 1 : (long)p.sub, store ? p.parts : 1, l2t,
+                                  store ? nullptr : c.labels, p.direct ? nullptr : rows, s0, zl, Z,
+                                  p.ldz};
             head_product<KMAJ, KMAJ>(g, sn, es, s, "head_scores");
-            MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
-                           stat, tstat, p.parts, p.sub, l2t, zl, c.labels, c.V, rows, count, 0, s0,
-                           sn, norm, tnorm, c.loss, c.lse));
-            if (!store) continue;
+            if (!store) {
+                MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
+                               stat, p.parts, p.sub, zl, c.labels, c.V, p.direct ? nullptr : rows,
+                               g.count, s0, sn, c.loss, c.lse));
+                continue;
+            }
             const int segs = c.grad ? p.segs : 1;
             const HeadDz dz = {Z, p.ldz, G + (long)q0 * p.ldz, segs, p.seg, c.V, rows, count, s0, sn,
-                               norm, tnorm, c.labels, c.weight, c.tidx, c.tlogit, c.tweight, c.K,
-                               c.tau, inv_tau, l2t, c.kd, c.grad};
+                               stat, tstat, p.parts, c.loss, c.lse, c.labels, c.weight, c.tidx,
+                               c.tlogit, c.tweight, c.K, c.tau, inv_tau, l2t, c.kd, c.grad};
             MOE_LAUNCH("head_dz", s,
                        head_dz_kernel<T><<<cdiv((long)sn * segs, 4), 256, 0, s>>>(dz));
         }
@@ -1329,14 +1437,16 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
         g.p0 = p0, g.piece = p.piece, g.part = part;
         if (c.dx) {
             g.A = G, g.lda = p.ldz, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
-            g.M = bound, g.N = c.d, g.K = c.V, g.dyn = 1, g.plan = plan + 2 * i;
+            g.M = bound, g.N = c.d, g.K = c.V, g.dyn = 1;
+            g.plan = p.slots_dx ? plan + 2 * i : nullptr;
             head_product_join<KMAJ, MNMAJ>(g, bound, EpiRows<T>{static_cast<T*>(c.dx), c.d, rows, p0},
                                            s, "head_dx", "head_dx_join");
         }
         if (c.dWv) {
             float* acc = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
             g.A = G, g.lda = p.ldz, g.B = xc, g.ldb = c.d;
-            g.M = c.V, g.N = c.d, g.K = bound, g.dyn = 2, g.plan = plan + 2 * i + 1;
+            g.M = c.V, g.N = c.d, g.K = bound, g.dyn = 2;
+            g.plan = p.slots_dw ? plan + 2 * i + 1 : nullptr;
             head_product_join<MNMAJ, MNMAJ>(
                 g, c.V, EpiSum<T>{static_cast<T*>(c.dWv), acc, c.d, count, p0, p.piece}, s, "head_dW",
                 "head_dW_join");
