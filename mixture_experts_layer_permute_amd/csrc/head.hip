@@ -120,17 +120,16 @@ constexpr int kMaxSlots = 768;          // rest tiles times parts
 // fewest stage times over the rounds they take, with `ends` of them for a tile's
 // start and end and `slot` for writing and adding up a part.  bf16: 6 (10 us
 // against 1.2 a stage) and a twelfth (512 KB at about 4.5 TB/s); fp32: 1 and a
-// hundredth (128 KB against 3.4 us a stage).
-__host__ __device__ inline int rest_parts(int R, int nj, bool f32) {
+// hundredth (128 KB against 3.4 us a stage).  One wave: lane i looks at i + 1.
+__device__ __forceinline__ int rest_parts(int R, int nj, bool f32) {
     const float ends = f32 ? 1.0f : 6.0f, slot = f32 ? 0.01f : 0.085f;
-    int best = 1;
-    float least = 1e30f;
-    for (int S = 1; S <= kMaxParts && S * 4 <= nj + 3 && (S == 1 || R * S <= kMaxSlots); ++S) {
-        const int rounds = (R * S + kRound - 1) / kRound;
-        const float t = rounds * ((nj + S - 1) / S + ends) + (S > 1 ? ends + R * S * slot : 0.0f);
-        if (t < least) least = t, best = S;
-    }
-    return best;
+    const int S = (threadIdx.x & 63) + 1;
+    const bool can = S == 1 || (S <= kMaxParts && S * 4 <= nj + 3 && R * S <= kMaxSlots);
+    const int rounds = (R * S + kRound - 1) / kRound;
+    const float t = can ? rounds * ((nj + S - 1) / S + ends) + (S > 1 ? ends + R * S * slot : 0.0f)
+                        : INFINITY;
+    const float least = -wave_max(-t);
+    return __ffsll((long long)__ballot(t == least));      // the fewest parts of equals
 }
 
 // plan[2 piece + {0: dx, 1: dWv}] = the parts of the product's rest tiles.
@@ -157,9 +156,15 @@ struct HeadTokens {
 // of the tokens without a loss, the split of the products.
 struct HeadStart {
     int32_t* rows;
+    int32_t* clab;           // the rows' labels, or NULL
     int32_t* count;
     float* out[3];
     HeadParts parts;
+    __device__ __forceinline__ void place(const HeadTokens& tk, int t, int at) const {
+        MOE_DASSERT(at >= 0 && at < tk.T);
+        rows[at] = t;
+        if (clab) clab[at] = tk.act[t];
+    }
     __device__ __forceinline__ void skip(int t) const {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -167,12 +172,13 @@ struct HeadStart {
     }
     __device__ __forceinline__ void finish(int n) const {
         if (threadIdx.x == 0) *count = n;
-        for (int i = threadIdx.x; i < parts.pieces * 2; i += 1024) {
+        for (int i = threadIdx.x >> 6; i < parts.pieces * 2; i += 16) {    // a wave each
             const int k = max(0, min(n - (i >> 1) * parts.piece, parts.piece));
             const int nM = ((i & 1) ? parts.V + parts.bm - 1 : k + parts.bm - 1) / parts.bm;
             const int tiles = nM * ((parts.d + parts.bm - 1) / parts.bm);
-            parts.plan[i] = rest_parts(tiles % kRound, ((i & 1) ? k + 63 : parts.V + 63) / 64,
-                                       parts.bm == 128);
+            const int best = rest_parts(tiles % kRound, ((i & 1) ? k + 63 : parts.V + 63) / 64,
+                                        parts.bm == 128);
+            if ((threadIdx.x & 63) == 0) parts.plan[i] = best;
         }
     }
 };
@@ -205,10 +211,8 @@ __global__ __launch_bounds__(1024) void head_compact_kernel(HeadTokens tk, HeadS
     __shared__ int sh[16];
     int n = 0;
     for (int t0 = 0; t0 < tk.T; t0 += kStartTokens)
-        n = compact_round(tk, t0, n, sh, [&](int t, int at) {
-            MOE_DASSERT(at >= 0 && at < tk.T);
-            st.rows[at] = t;
-        }, [&](int t) { st.skip(t); });
+        n = compact_round(tk, t0, n, sh, [&](int t, int at) { st.place(tk, t, at); },
+                          [&](int t) { st.skip(t); });
     st.finish(n);
 }
 
@@ -222,9 +226,8 @@ __global__ __launch_bounds__(1024) void head_start_kernel(HeadTokens tk, HeadSta
     __shared__ int list[kStartTokens];
     const bool first = blockIdx.x == 0;
     const int n = compact_round(tk, 0, 0, sh, [&](int t, int at) {
-        MOE_DASSERT(at >= 0 && at < tk.T);
         list[at] = t;
-        if (first) st.rows[at] = t;
+        if (first) st.place(tk, t, at);
     }, [&](int t) { if (first) st.skip(t); });
     __syncthreads();
     if (first) st.finish(n);
@@ -374,16 +377,18 @@ struct EpiScores {
     float* tstat;            // the sum at the temperature likewise, or NULL
     long sp, sr;
     float l2t;               // L / tau
-    const int32_t* labels;   // or NULL
-    const int32_t* rows;     // compacted row -> token, or NULL: the row itself
-    int p0;
+    const int32_t* labels;   // [rows] or NULL
     float* zl;               // [rows] label's score
     float* Z;                // or NULL
     long ldz;                // a multiple of 64
 
+    // what row() needs of a row from memory, asked for before the products
+    __device__ __forceinline__ int ask(const HeadTile& ti, int rl) const {
+        return labels && rl < ti.rows ? labels[ti.m0 + rl] : -1;
+    }
     template <class Lanes>
-    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
-                                        f32x4 (&v)[8]) const {
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, f32x4 (&v)[8],
+                                        int label) const {
         const int col = ti.n0 + cl;
         const bool in = rl < ti.rows;
         const long r = (long)ti.m0 + rl;
@@ -395,7 +400,7 @@ struct EpiScores {
             }
         }
         if (labels && in) {
-            const int y = labels[rows ? rows[p0 + r] : (int)r] - col;
+            const int y = label - col;
             if ((unsigned)y < (unsigned)Lanes::WIDTH && col + y < V) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -490,12 +495,13 @@ struct EpiRows {
     long ldo;
     const int32_t* rows;
     int p0;
+    __device__ __forceinline__ int ask(const HeadTile& ti, int rl) const {
+        return rl < ti.rows ? rows[p0 + ti.m0 + rl] : 0;
+    }
     template <class Lanes>
-    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
-                                        const f32x4 (&v)[8]) const {
-        const bool in = rl < ti.rows;
-        store_row<Lanes>(out + (in ? (long)rows[p0 + ti.m0 + rl] : 0) * ldo + ti.n0, in, cl,
-                         ti.cols, v);
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, const f32x4 (&v)[8],
+                                        int token) const {
+        store_row<Lanes>(out + (long)token * ldo + ti.n0, rl < ti.rows, cl, ti.cols, v);
     }
     __device__ __forceinline__ void put8(int r, int c, const float* v) const {
         st8(out + (long)rows[p0 + r] * ldo + c, v);
@@ -511,9 +517,10 @@ struct EpiSum {
     long ldo;
     const int32_t* count;
     int p0, piece;
+    __device__ __forceinline__ int ask(const HeadTile&, int) const { return 0; }
     template <class Lanes>
-    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl,
-                                        f32x4 (&v)[8]) const {
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, f32x4 (&v)[8],
+                                        int) const {
         const bool in = rl < ti.rows;
         const long at = (long)(ti.m0 + rl) * ldo + ti.n0;
         if (p0 > 0) {
@@ -692,6 +699,9 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int wm = wv >> 1, wn = wv & 1;
 
+    int asked[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asked[i] = epi.ask(ti, wm * 128 + i * 16 + (lane & 15));
     typedef HeadOperand<ALAY, BK, 4> OpA;
     typedef HeadOperand<BLAY, BK, 4> OpB;
     constexpr int NL = OpA::NLOAD;                     // loads of a unit
@@ -813,7 +823,7 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
         mfma_done(acc[I]);
         const int rl = wm * 128 + I * 16 + (lane & 15);
         if (part) store_part<Quads16, 256, 256>(p.part, ti, rl, wn * 128, acc[I]);
-        else epi.template row<Quads16>(ti, rl, wn * 128, acc[I]);
+        else epi.template row<Quads16>(ti, rl, wn * 128, acc[I], asked[I]);
         __builtin_amdgcn_sched_barrier(0);
     });
 }
@@ -867,6 +877,9 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
     if (!ti.live) return;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int wm = wv >> 1, wn = wv & 1;
+    int asked[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asked[i] = epi.ask(ti, wm * 64 + i * 32 + (lane & 31));
     typedef HeadOperandF32<ALAY> OpA;
     typedef HeadOperandF32<BLAY> OpB;
     constexpr int NL = OpA::NLOAD;
@@ -900,11 +913,18 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
         stage_barrier<0>();            // stage j landed, stage j - 1 read by every wave
         if (j + 1 < nj) issue(j + 1);
         const uint32_t u = ring0 + (uint32_t)((j & 1) * STAGE);
+        f32x4 fa[2][2], fc[2][2];
+        auto read = [&](int b) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                fa[b & 1][i] = opA.read4(u, i, b), fc[b & 1][i] = opB.read4(u + UNIT, i, b);
+        };
+        read(0);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            f32x4 a[2], c[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) a[i] = opA.read4(u, i, b), c[i] = opB.read4(u + UNIT, i, b);
+            if (b < 3) read(b + 1);
+            __builtin_amdgcn_sched_barrier(0);         // (those reads before these products)
+            const f32x4(&a)[2] = fa[b & 1], (&c)[2] = fc[b & 1];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -926,7 +946,7 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
         if (Epi::kSplits && ti.slot >= 0)
             store_part<Quads32, FBM, FBM>(p.part, ti, rl, wn * 64, v);
         else
-            epi.template row<Quads32>(ti, rl, wn * 64, v);
+            epi.template row<Quads32>(ti, rl, wn * 64, v, asked[I]);
     });
 }
 
@@ -1155,7 +1175,9 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
             f32x4 v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (c + 256 * u < c1) v[u] = *reinterpret_cast<const f32x4*>(z + c + 256 * u);
+                if (c + 256 * u < c1)          // read once: not kept (565 us to 466, 8192 x 50257)
+                    v[u] = __builtin_nontemporal_load(
+                        reinterpret_cast<const f32x4*>(z + c + 256 * u));
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int cu = c + 256 * u;
@@ -1220,7 +1242,7 @@ struct HeadPlan {
     int piece, pieces, sub, parts;
     long ldz;
     int segs, seg;                     // of a row of dz
-    size_t rows, count, plan, act, xc, zl, stat, tstat, z, g, part, acc, total;
+    size_t rows, clab, count, plan, act, xc, zl, stat, tstat, z, g, part, acc, total;
     bool direct, slots_dx, slots_dw;   // x as it is; products that may be split
 };
 
@@ -1265,6 +1287,7 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
         return at;
     };
     p.rows = take((size_t)T * 4);
+    p.clab = take(store ? 0 : (size_t)T * 4);
     p.count = take(4);
     p.plan = take(grad ? (size_t)p.pieces * 8 : 0);
     p.act = take(K > 0 ? (size_t)T * 4 : 0);
@@ -1361,6 +1384,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
     int32_t* count = reinterpret_cast<int32_t*>(ws + p.count);
     int32_t* plan = c.grad ? reinterpret_cast<int32_t*>(ws + p.plan) : nullptr;
+    int32_t* clab = store ? nullptr : reinterpret_cast<int32_t*>(ws + p.clab);
     float2* stat = reinterpret_cast<float2*>(ws + p.stat);
     float* tstat = teacher ? reinterpret_cast<float*>(ws + p.tstat) : nullptr;
     float* zl = reinterpret_cast<float*>(ws + p.zl);
@@ -1376,7 +1400,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     if (!p.direct) {
         HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.K, c.V, c.T};
         const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM};
-        const HeadStart st = {rows, count, {c.loss, c.lse, c.kd}, hp};
+        const HeadStart st = {rows, clab, count, {c.loss, c.lse, c.kd}, hp};
         u32x4_t* dx0 = c.grad ? static_cast<u32x4_t*>(c.dx) : nullptr;
         // (a thread of the compaction looks at its tokens' slots itself: few)
         if (teacher && (long)c.T * c.K > 16384) {
@@ -1417,8 +1441,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
             // statistics by row for head_dz, by part for head_lse; the label's score
             // comes from z where that is kept
             const EpiScores es = {c.V, stat, tstat, store ? 1 : (long)p.sub, store ? p.parts : 1, l2t,
-                                  store ? nullptr : c.labels, p.direct ? nullptr : rows, s0, zl, Z,
-                                  p.ldz};
+                                  store ? nullptr : p.direct ? c.labels : clab + s0, zl, Z, p.ldz};
             head_product<KMAJ, KMAJ>(g, sn, es, s, "head_scores");
             if (!store) {
                 MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
