@@ -112,6 +112,7 @@ __global__ __launch_bounds__(256) void head_active_kernel(const int32_t* __restr
     if (lane == 0) act[t] = any ? 1 : -1;
 }
 
+constexpr int kXcdRun = 32;             // neighbouring tiles on one XCD
 constexpr int kRound = 256;             // compute units
 constexpr int kMaxParts = 32;           // of a tile
 constexpr int kMaxSlots = 768;          // rest tiles times parts
@@ -124,7 +125,8 @@ constexpr int kMaxSlots = 768;          // rest tiles times parts
 __device__ __forceinline__ int rest_parts(int R, int nj, bool f32) {
     const float ends = f32 ? 1.0f : 6.0f, slot = f32 ? 0.01f : 0.085f;
     const int S = (threadIdx.x & 63) + 1;
-    const bool can = S == 1 || (S <= kMaxParts && S * 4 <= nj + 3 && R * S <= kMaxSlots);
+    const bool can = S == 1 || (S <= kMaxParts && (f32 ? S <= nj : S * 4 <= nj + 3) &&
+                               R * S <= kMaxSlots);
     const int rounds = (R * S + kRound - 1) / kRound;
     const float t = can ? rounds * ((nj + S - 1) / S + ends) + (S > 1 ? ends + R * S * slot : 0.0f)
                         : INFINITY;
@@ -289,7 +291,6 @@ struct HeadGemm {
     int p0, piece;
     const int32_t* plan;     // parts of a rest tile (NULL: 1)
     float* part;             // [slot][BM][BN]
-    int xcd_run;
 };
 
 struct HeadTile {
@@ -312,14 +313,14 @@ __device__ __forceinline__ void head_origin(int w, int nM, int nN, int& m0, int&
 }
 
 template <int BM, int BN, typename T>
-__device__ __forceinline__ HeadTile head_tile(const HeadGemm<T>& p) {
+__device__ __forceinline__ HeadTile head_tile(const HeadGemm<T>& p, int block) {
     HeadTile t;
     const int n = p.dyn ? piece_rows(p.count, p.p0, p.piece, p.piece) : 0;
     const int M = p.dyn == 1 ? n : p.M, K = p.dyn == 2 ? n : p.K;
     const int nM = (M + BM - 1) / BM, nN = (p.N + BN - 1) / BN, tiles = nM * nN;
     const int S = p.plan ? *p.plan : 1;
     const int full = S > 1 ? tiles / kRound * kRound : tiles;
-    int L = xcd_logical(blockIdx.x, p.xcd_run);
+    int L = xcd_logical(block, kXcdRun);
     t.slot = -1;
     t.k0 = 0, t.k1 = K;
     if (L >= full) {
@@ -677,7 +678,7 @@ __device__ __forceinline__ void mfma_done(f32x4 (&c)[8]) {
 
 // bf16: 256 x 256 tiles, four waves of 128 x 128 (one a SIMD), operands straight
 // from HBM into a ring of NU units (a unit: one operand's 256 rows of a stage of
-// BK reduction steps; A's and B's take turns, unit u in slot u mod NU).
+// BK reduction steps, 32 KB; A's and B's take turns, unit u in slot u mod NU).
 //
 // The order of the instructions is the kernel: the matrix pipe takes one
 // 16x16x32 product every 16 cycles, and between two of them a wave issues at
@@ -687,14 +688,14 @@ __device__ __forceinline__ void mfma_done(f32x4 (&c)[8]) {
 // barrier a stage, at the start of its last step: by then every wave has read the
 // whole stage (its two slots are free for the loads that follow) and the next
 // stage, which that step reads from, has landed.
-template <int BK, int NU, int ALAY, int BLAY, class Epi>
-__global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p, Epi epi) {
-    constexpr int UNIT = 256 * BK * 2;
-    constexpr int NS = BK / 32;                        // steps of a stage
-    static_assert(NU * UNIT <= 160 * 1024 && NU >= 5, "LDS");
-    __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[NU * UNIT];
+constexpr int BK = 64, NU = 5, UNIT = 256 * BK * 2;
+constexpr int kRingBytes = NU * UNIT;
+template <int ALAY, int BLAY, class Epi>
+__device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, const Epi& epi,
+                                                  int block, uint8_t* ringbuf) {
+    static_assert(kRingBytes <= 160 * 1024, "LDS");
     if (piece_done(p)) return;
-    const HeadTile ti = head_tile<256, 256>(p);
+    const HeadTile ti = head_tile<256, 256>(p, block);
     if (!ti.live) return;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int wm = wv >> 1, wn = wv & 1;
@@ -758,9 +759,8 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
     typedef std::integral_constant<int, 0> I0;
     typedef std::integral_constant<int, 1> I1;
 
-    // units 0 .. NU - 1 but those that the first stage's loads bring
-    constexpr int PRE = NU - (NS == 2 ? 1 : 0);
-    unroll<PRE>([&](auto U) {
+    // units 0 .. 3: stages 0 and 1
+    unroll<4>([&](auto U) {
         constexpr int u = decltype(U)::value;
         const i32x4_t rs = u % 2 ? rsB(u / 2) : rsA(u / 2);
         unroll<NL>([&](auto I) {
@@ -768,53 +768,27 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
             else opA.template load<decltype(I)::value>(rs, slot(u));
         });
     });
-    stage_barrier<NL * (PRE - 2)>();                   // stage 0 landed
+    stage_barrier<NL * 2>();                           // stage 0 landed
     unroll<16>([&](auto R) { read1(R, I0{}, I0{}, unit(0), unit(1)); });
     int qa = 0;                                        // slot of A's unit of stage j
-    if constexpr (NS == 2) {
-        // stage j: units 2j, 2j+1; A of stage j+2 is loaded in its first step, B of
-        // stage j+2 right behind its barrier
-        constexpr int G0 = 32 / NL;
-        typedef std::integral_constant<int, G0> GAP;
-        typedef std::integral_constant<int, NL> CNT;
+    // stage j: units 2j, 2j+1; A of stage j+2 is loaded in its first step, B of stage
+    // j+2 right behind its barrier
+    typedef std::integral_constant<int, 32 / NL> GAP;
+    typedef std::integral_constant<int, NL> CNT;
 #pragma unroll 1
-        for (int j = 0; j < nj; ++j) {
-            const uint32_t ua = unit(qa), ub = unit(wrap(qa + 1));
-            const i32x4_t ra = rsA(j + 2);
-            step(I0{}, I1{}, ua, ub, std::integral_constant<int, 33>{}, GAP{}, CNT{}, [&](auto I) {
-                opA.template load<decltype(I)::value>(ra, slot(wrap(qa + 4)));
-            });
-            stage_barrier<NL>();                       // stage j read, stage j+1 landed
-            const i32x4_t rb = rsB(j + 2);
-            const int qn = wrap(qa + 2);
-            step(I1{}, I0{}, unit(qn), unit(wrap(qn + 1)), I1{}, GAP{}, CNT{}, [&](auto I) {
-                opB.template load<decltype(I)::value>(rb, slot(qa));
-            });
-            qa = qn;
-        }
-    } else {
-        // stage j is one step, its set of fragments read during stage j-1; loads of stage
-        // j + NU / 2 into its slots
-        auto stage = [&](auto BUF, int j) {
-            stage_barrier<NL * (NU - 4)>();            // stage j read, stage j+1 landed
-            const i32x4_t ra = rsA(j + NU / 2), rb = rsB(j + NU / 2);
-            const int qn = wrap(qa + 2);
-            step(BUF, I0{}, unit(qn), unit(qn + 1), std::integral_constant<int, 33>{},
-                 std::integral_constant<int, 30 / (2 * NL)>{}, std::integral_constant<int, 2 * NL>{},
-                 [&](auto I) {
-                     constexpr int i = decltype(I)::value;
-                     if constexpr (i < NL) opA.template load<i>(ra, slot(qa));
-                     else opB.template load<i - NL>(rb, slot(qa + 1));
-                 });
-            qa = qn;
-        };
-        int j = 0;
-#pragma unroll 1
-        for (; j + 1 < nj; j += 2) {
-            stage(I0{}, j);
-            stage(I1{}, j + 1);
-        }
-        if (j < nj) stage(I0{}, j);
+    for (int j = 0; j < nj; ++j) {
+        const uint32_t ua = unit(qa), ub = unit(wrap(qa + 1));
+        const i32x4_t ra = rsA(j + 2);
+        step(I0{}, I1{}, ua, ub, std::integral_constant<int, 33>{}, GAP{}, CNT{}, [&](auto I) {
+            opA.template load<decltype(I)::value>(ra, slot(wrap(qa + 4)));
+        });
+        stage_barrier<NL>();                           // stage j read, stage j+1 landed
+        const i32x4_t rb = rsB(j + 2);
+        const int qn = wrap(qa + 2);
+        step(I1{}, I0{}, unit(qn), unit(wrap(qn + 1)), I1{}, GAP{}, CNT{}, [&](auto I) {
+            opB.template load<decltype(I)::value>(rb, slot(qa));
+        });
+        qa = qn;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // (loads of the empty stages)
     // (a row of fragments at a time, so that the others stay where they are)
@@ -826,6 +800,12 @@ __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p
         else epi.template row<Quads16>(ti, rl, wn * 128, acc[I], asked[I]);
         __builtin_amdgcn_sched_barrier(0);
     });
+}
+
+template <int ALAY, int BLAY, class Epi>
+__global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p, Epi epi) {
+    __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[kRingBytes];
+    head_product_body<ALAY, BLAY>(p, epi, blockIdx.x, ringbuf);
 }
 
 // fp32: 128 x 128 tiles, 4 waves of 64 x 64, v_mfma_f32_32x32x2_f32, two
@@ -868,12 +848,14 @@ struct HeadOperandF32 : HeadOperand<LAY, LAY == KMAJ ? 64 : 32, 4, LAY == KMAJ ?
     }
 };
 
+constexpr int kRingBytesF32 = 65536;
 template <int ALAY, int BLAY, class Epi>
-__global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float> p, Epi epi) {
+__device__ __forceinline__ void head_product_body(const HeadGemm<float>& p, const Epi& epi,
+                                                  int block, uint8_t* ringbuf) {
     constexpr int UNIT = 16384, STAGE = 2 * UNIT;
-    __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[2 * STAGE];
+    static_assert(2 * STAGE <= kRingBytesF32, "LDS");
     if (piece_done(p)) return;
-    const HeadTile ti = head_tile<FBM, FBM>(p);
+    const HeadTile ti = head_tile<FBM, FBM>(p, block);
     if (!ti.live) return;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int wm = wv >> 1, wn = wv & 1;
@@ -950,10 +932,36 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
     });
 }
 
+template <int ALAY, int BLAY, class Epi>
+__global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float> p, Epi epi) {
+    __shared__ __attribute__((aligned(16384))) uint8_t ringbuf[kRingBytesF32];
+    head_product_body<ALAY, BLAY>(p, epi, blockIdx.x, ringbuf);
+}
+
+// Both gradients' products in one launch: blocks 0 .. nx - 1 make dx = dz Wv, the
+// others dWv = dz^T x, so that the second fills the rounds that the first leaves.
+__global__ __launch_bounds__(256, 1) void head_grads_kernel(HeadGemm<bf16_t> gx,
+                                                            EpiRows<bf16_t> ex,
+                                                            HeadGemm<bf16_t> gw,
+                                                            EpiSum<bf16_t> ew, int nx) {
+    __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[kRingBytes];
+    const int b = blockIdx.x;
+    if (b < nx) head_product_body<KMAJ, MNMAJ>(gx, ex, b, ringbuf);
+    else head_product_body<MNMAJ, MNMAJ>(gw, ew, b - nx, ringbuf);
+}
+__global__ __launch_bounds__(256, 2) void head_grads_kernel(HeadGemm<float> gx, EpiRows<float> ex,
+                                                            HeadGemm<float> gw, EpiSum<float> ew,
+                                                            int nx) {
+    __shared__ __attribute__((aligned(16384))) uint8_t ringbuf[kRingBytesF32];
+    const int b = blockIdx.x;
+    if (b < nx) head_product_body<KMAJ, MNMAJ>(gx, ex, b, ringbuf);
+    else head_product_body<MNMAJ, MNMAJ>(gw, ew, b - nx, ringbuf);
+}
+
 // The rest tiles of a product whose reduction was split: their parts added in
 // order and put where the product's epilogue puts them.  8 elements a thread.
 template <int BM, int BN, typename T, class Epi>
-__global__ __launch_bounds__(1024) void head_join_kernel(HeadGemm<T> p, Epi epi) {
+__device__ __forceinline__ void head_join_body(const HeadGemm<T>& p, const Epi& epi, int block) {
     constexpr int PER = BM * BN / 8192;               // blocks of a tile
     const int S = *p.plan;
     if (S == 1 || piece_done(p)) return;
@@ -961,11 +969,11 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadGemm<T> p, Epi epi)
     const int M = p.dyn == 1 ? n : p.M;
     const int nM = (M + BM - 1) / BM, nN = (p.N + BN - 1) / BN;
     const int full = nM * nN / kRound * kRound, R = nM * nN - full;
-    const int tile = blockIdx.x / PER;
+    const int tile = block / PER;
     if (tile >= R) return;
     int m0, n0;
     head_origin<BM, BN>(full + tile, nM, nN, m0, n0);
-    const int e = ((blockIdx.x % PER) * 1024 + threadIdx.x) * 8;
+    const int e = ((block % PER) * 1024 + threadIdx.x) * 8;
     const int r = m0 + e / BN, c = n0 + e % BN;
     if (r >= M || c >= p.N) return;
     const float* q = p.part + (long)tile * (BM * BN) + e;
@@ -980,6 +988,13 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadGemm<T> p, Epi epi)
         for (int u = 0; u < 8; ++u) v[u] += a[u];
     }
     epi.put8(r, c, v);
+}
+template <int BM, typename T>
+__global__ __launch_bounds__(1024) void head_join_kernel(HeadGemm<T> gx, EpiRows<T> ex,
+                                                         HeadGemm<T> gw, EpiSum<T> ew, int nx) {
+    const int b = blockIdx.x;
+    if (b < nx) head_join_body<BM, BM>(gx, ex, b);
+    else head_join_body<BM, BM>(gw, ew, b - nx);
 }
 
 // --------------------------------------------------------- normalisers
@@ -1242,14 +1257,14 @@ struct HeadPlan {
     int piece, pieces, sub, parts;
     long ldz;
     int segs, seg;                     // of a row of dz
-    size_t rows, clab, count, plan, act, xc, zl, stat, tstat, z, g, part, acc, total;
+    size_t rows, clab, count, plan, act, xc, zl, stat, tstat, z, g, part_dx, part_dw, acc, total;
     bool direct, slots_dx, slots_dw;   // x as it is; products that may be split
 };
 
 // Slots that a product with up to `tiles` tiles and K reduction steps can use
 // (no fewer for more of either, so that a workspace serves every smaller batch).
-inline long head_slots(long tiles, long K) {
-    const long parts = std::min((long)kMaxParts, (cdiv(K, 64) + 3) / 4l);
+inline long head_slots(long tiles, long K, bool f32) {
+    const long parts = std::min((long)kMaxParts, f32 ? (long)cdiv(K, 64) : (cdiv(K, 64) + 3) / 4l);
     return parts > 1 ? std::min((long)kMaxSlots, std::min(tiles, (long)kRound - 1) * parts) : 0;
 }
 
@@ -1300,10 +1315,11 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     p.z = take(store ? rmax * p.ldz * 4 : 0);
     p.g = take(grad ? (size_t)piece * p.ldz * b : 0);
     const long cols = cdiv(d, bm);
-    const long sx = head_slots(cdiv(piece, bm) * cols, V);
-    const long sw = head_slots(cdiv(V, bm) * cols, piece);
+    const long sx = head_slots(cdiv(piece, bm) * cols, V, dt == MOE_F32);
+    const long sw = head_slots(cdiv(V, bm) * cols, piece, dt == MOE_F32);
     p.slots_dx = sx > 0, p.slots_dw = sw > 0;
-    p.part = take(grad ? (size_t)std::max(sx, sw) * bm * bm * 4 : 0);
+    p.part_dx = take(grad ? (size_t)sx * bm * bm * 4 : 0);
+    p.part_dw = take(grad ? (size_t)sw * bm * bm * 4 : 0);
     p.acc = take(grad && p.pieces > 1 ? (size_t)V * d * 4 : 0);
     p.total = o;
     return p;
@@ -1346,36 +1362,26 @@ struct HeadCall {
 
 // Blocks of a product with up to m rows: its tiles, and the slots of its rest.
 template <int BM, typename T>
-int head_grid(HeadGemm<T>& g, long m) {
+int head_grid(const HeadGemm<T>& g, long m) {
     const long tiles = (long)cdiv(m, BM) * cdiv(g.N, BM);
-    g.xcd_run = 32;
     const long blocks = g.plan ? std::max(tiles, tiles / kRound * kRound + kMaxSlots) : tiles;
-    const long pad = NXCD * g.xcd_run;
+    const long pad = NXCD * kXcdRun;
     return (int)((blocks + pad - 1) / pad * pad);
 }
-
-template <int ALAY, int BLAY, typename T, class Epi>
-void head_product(HeadGemm<T> g, long m, const Epi& epi, hipStream_t s, const char* name) {
-    if constexpr (sizeof(T) == 2) {
-        const int grid = head_grid<256>(g, m);
-        MOE_LAUNCH(name, s, head_product_kernel<64, 5, ALAY, BLAY, Epi>
-                   <<<grid, 256, 0, s>>>(g, epi));
-    } else {
-        const int grid = head_grid<FBM>(g, m);
-        MOE_LAUNCH(name, s, head_product_f32_kernel<ALAY, BLAY, Epi><<<grid, 256, 0, s>>>(g, epi));
-    }
+// Blocks that add up its rest tiles.
+template <int BM, typename T>
+int head_join_grid(const HeadGemm<T>& g, long m) {
+    const long rest = std::min((long)kRound - 1, (long)cdiv(m, BM) * cdiv(g.N, BM));
+    return g.plan ? (int)(rest * (BM * BM / 8192)) : 0;
 }
 
-// The product and, where its rest tiles may be split, their sums.
-template <int ALAY, int BLAY, typename T, class Epi>
-void head_product_join(const HeadGemm<T>& g, long m, const Epi& epi, hipStream_t s,
-                       const char* name, const char* join) {
-    constexpr int BM = sizeof(T) == 2 ? 256 : FBM;
-    head_product<ALAY, BLAY>(g, m, epi, s, name);
-    if (!g.plan) return;
-    const long rest = std::min((long)kRound - 1, (long)cdiv(m, BM) * cdiv(g.N, BM));
-    MOE_LAUNCH(join, s, head_join_kernel<BM, BM, T, Epi>
-               <<<(int)(rest * (BM * BM / 8192)), 1024, 0, s>>>(g, epi));
+void head_scores(const HeadGemm<bf16_t>& g, long m, const EpiScores& e, hipStream_t s) {
+    MOE_LAUNCH("head_scores", s, head_product_kernel<KMAJ, KMAJ, EpiScores>
+               <<<head_grid<256>(g, m), 256, 0, s>>>(g, e));
+}
+void head_scores(const HeadGemm<float>& g, long m, const EpiScores& e, hipStream_t s) {
+    MOE_LAUNCH("head_scores", s, head_product_f32_kernel<KMAJ, KMAJ, EpiScores>
+               <<<head_grid<FBM>(g, m), 256, 0, s>>>(g, e));
 }
 
 template <typename T>
@@ -1390,7 +1396,6 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     float* zl = reinterpret_cast<float*>(ws + p.zl);
     float* Z = store ? reinterpret_cast<float*>(ws + p.z) : nullptr;
     T* G = reinterpret_cast<T*>(ws + p.g);
-    float* part = reinterpret_cast<float*>(ws + p.part);
     T* xc = reinterpret_cast<T*>(ws + p.xc);
     const float inv_tau = 1.0f / c.tau, l2t = (float)(1.4426950408889634 / (double)c.tau);
     const int vpr = c.d * (int)sizeof(T) / 16;
@@ -1442,7 +1447,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
             // comes from z where that is kept
             const EpiScores es = {c.V, stat, tstat, store ? 1 : (long)p.sub, store ? p.parts : 1, l2t,
                                   store ? nullptr : p.direct ? c.labels : clab + s0, zl, Z, p.ldz};
-            head_product<KMAJ, KMAJ>(g, sn, es, s, "head_scores");
+            head_scores(g, sn, es, s);
             if (!store) {
                 MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
                                stat, p.parts, p.sub, zl, c.labels, c.V, p.direct ? nullptr : rows,
@@ -1457,23 +1462,28 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
                        head_dz_kernel<T><<<cdiv((long)sn * segs, 4), 256, 0, s>>>(dz));
         }
         if (!c.grad) continue;
-        g.p0 = p0, g.piece = p.piece, g.part = part;
-        if (c.dx) {
-            g.A = G, g.lda = p.ldz, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
-            g.M = bound, g.N = c.d, g.K = c.V, g.dyn = 1;
-            g.plan = p.slots_dx ? plan + 2 * i : nullptr;
-            head_product_join<KMAJ, MNMAJ>(g, bound, EpiRows<T>{static_cast<T*>(c.dx), c.d, rows, p0},
-                                           s, "head_dx", "head_dx_join");
-        }
-        if (c.dWv) {
-            float* acc = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
-            g.A = G, g.lda = p.ldz, g.B = xc, g.ldb = c.d;
-            g.M = c.V, g.N = c.d, g.K = bound, g.dyn = 2;
-            g.plan = p.slots_dw ? plan + 2 * i + 1 : nullptr;
-            head_product_join<MNMAJ, MNMAJ>(
-                g, c.V, EpiSum<T>{static_cast<T*>(c.dWv), acc, c.d, count, p0, p.piece}, s, "head_dW",
-                "head_dW_join");
-        }
+        HeadGemm<T> gx = g, gw = g;
+        gx.p0 = gw.p0 = p0, gx.piece = gw.piece = p.piece;
+        gx.A = gw.A = G, gx.lda = gw.lda = p.ldz;
+        gx.B = static_cast<const T*>(c.Wv), gx.ldb = c.d;
+        gx.M = bound, gx.N = c.d, gx.K = c.V, gx.dyn = 1;
+        gx.plan = p.slots_dx ? plan + 2 * i : nullptr;
+        gx.part = reinterpret_cast<float*>(ws + p.part_dx);
+        gw.B = xc, gw.ldb = c.d;
+        gw.M = c.V, gw.N = c.d, gw.K = bound, gw.dyn = 2;
+        gw.plan = p.slots_dw ? plan + 2 * i + 1 : nullptr;
+        gw.part = reinterpret_cast<float*>(ws + p.part_dw);
+        const EpiRows<T> ex = {static_cast<T*>(c.dx), c.d, rows, p0};
+        float* acc = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
+        const EpiSum<T> ew = {static_cast<T*>(c.dWv), acc, c.d, count, p0, p.piece};
+        const int nx = c.dx ? head_grid<BM>(gx, bound) : 0;
+        const int nw = c.dWv ? head_grid<BM>(gw, c.V) : 0;
+        MOE_LAUNCH("head_grads", s, head_grads_kernel<<<nx + nw, 256, 0, s>>>(gx, ex, gw, ew, nx));
+        const int jx = c.dx ? head_join_grid<BM>(gx, bound) : 0;
+        const int jw = c.dWv ? head_join_grid<BM>(gw, c.V) : 0;
+        if (jx + jw)
+            MOE_LAUNCH("head_join", s,
+                       head_join_kernel<BM, T><<<jx + jw, 1024, 0, s>>>(gx, ex, gw, ew, jx));
     }
     return launch_status();
 }
