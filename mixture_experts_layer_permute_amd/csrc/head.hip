@@ -15,7 +15,7 @@
 //  head_scores  z of a 256 x 256 tile in the matrix cores; the epilogue
 //               reduces every row's 128 columns to (max, sum of exp) from the
 //               fp32 accumulators, so the normaliser needs no second look at
-//               z, and z is stored (in fp32) only when something reads it;
+//               z, and z is stored only when something reads it;
 //  head_dz      z -> dz, a stream; the scores are held for up to 3072 tokens at a
 //               time (row tiles share a column tile's weights), dz for the piece;
 //  head_product dx = dz Wv and dWv = dz^T x, the tiles after the last full round
@@ -26,7 +26,8 @@
 // them again for dz, costs 8 n d V.
 //
 // Roundings (bf16): dz is rounded once to bf16 as an operand of the matrix
-// cores; every sum is fp32; dx and dWv are rounded once.
+// cores (the cross entropy's from scores kept within 3.4e-4 of exp(z), see
+// code_pair); every sum is fp32; dx and dWv are rounded once.
 #include <algorithm>
 #include <type_traits>
 
@@ -367,6 +368,51 @@ struct Quads32 {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
 
+// Coded scores.  Where only the cross entropy's dz needs them (which bf16 rounds
+// to 2^-9), a score is kept in 16 bits, as how far below the largest of its 128
+// columns it lies, in steps of 64 / 65535 of log2: exp(z) comes back within 2^-11 ln 2 =
+// 3.4e-4, a sixth of that rounding, at half the bytes of fp32 (8192 x 50257
+// scores: writing them 1.65 GB to 0.82, the pass that reads them 466 us to 330).  What lies 64
+// or more below (2^-64 of that maximum) counts as 64 below.  The label's own score and the
+// statistics stay fp32.
+// The coding is the hardware's conversion of [0, 1] to 0 .. 65535, clamped and rounded.
+constexpr float kCodeRange = 64.0f, kCodeStep = 64.0f / 65535.0f;
+__device__ __forceinline__ uint32_t code_pair(float lo, float hi) {      // log2, <= 0
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(
+                                            lo * (-1.0f / kCodeRange), hi * (-1.0f / kCodeRange)));
+}
+
+// (fmaxf would first turn signalling NaNs into quiet ones, an instruction each)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// Quads16 of 16-bit elements (pairs w) in 16-byte stores: two lanes 16 apart
+// trade halves of two neighbouring fragments.  After the swap of X's odd 16-lane
+// rows with Y's even ones a lane of an even row holds 8 columns of fragment q, of
+// an odd one of fragment q + 1.
+template <bool EDGE>
+__device__ __forceinline__ void store_pairs(void* out, bool in, int cols,
+                                            const uint32_t (&w)[8][2]) {
+    const int g = (threadIdx.x >> 4) & 3;
+    const int c0 = (g & 1) * 16 + (g >> 1) * 8;
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+        u32x4_t x;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const auto sw = __builtin_amdgcn_permlane16_swap(w[q][u], w[q + 1][u], false, false);
+            x[u] = sw[0];
+            x[2 + u] = sw[1];
+        }
+        const int c = c0 + q * 16;
+        if (in && (!EDGE || c < cols))
+            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + c) = x;
+    }
+}
+
 // Scores: per row and 128 (64 in fp32) columns the maximum m and the sums of
 // exp(z - m) and exp((z - m) / tau); the label's score; z itself if kept.
 // exp(z - m) = 2^(z L - m'), L = log2 e, m' = m L rounded: one fused multiply-add
@@ -380,7 +426,8 @@ struct EpiScores {
     float l2t;               // L / tau
     const int32_t* labels;   // [rows] or NULL
     float* zl;               // [rows] label's score
-    float* Z;                // or NULL
+    float* Z;                // z, or NULL
+    uint16_t* code;          // z coded (bf16 products only), or NULL
     long ldz;                // a multiple of 64
 
     // what row() needs of a row from memory, asked for before the products
@@ -388,60 +435,81 @@ struct EpiScores {
         return labels && rl < ti.rows ? labels[ti.m0 + rl] : -1;
     }
     template <class Lanes>
-    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, f32x4 (&v)[8],
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, const f32x4 (&acc)[8],
                                         int label) const {
-        const int col = ti.n0 + cl;
+        // (the wave's columns all inside the vocabulary: nothing to test)
+        if (ti.n0 + cl + Lanes::WIDTH <= V) row_of<Lanes, false>(ti, rl, cl, acc, label);
+        else row_of<Lanes, true>(ti, rl, cl, acc, label);
+    }
+    template <class Lanes, bool EDGE>
+    __device__ __forceinline__ void row_of(const HeadTile& ti, int rl, int cl,
+                                           const f32x4 (&acc)[8], int label) const {
+        constexpr bool kCodes = Lanes::WIDTH == 128;
+        const int col = ti.n0 + cl, left = V - col, room = (int)ldz - col;
         const bool in = rl < ti.rows;
         const long r = (long)ti.m0 + rl;
+        f32x4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = acc[q];
         if (Z && in) {
+            float* z = Z + r * ldz + col;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int c = col + Lanes::col(q);
-                if (c < ldz) *reinterpret_cast<f32x4*>(Z + r * ldz + c) = v[q];
-            }
+            for (int q = 0; q < 8; ++q)
+                if (!EDGE || Lanes::col(q) < room) *reinterpret_cast<f32x4*>(z + Lanes::col(q)) = v[q];
         }
-        if (labels && in) {
-            const int y = label - col;
-            if ((unsigned)y < (unsigned)Lanes::WIDTH && col + y < V) {
+        const int y = label - col;
+        if (label >= 0 && (unsigned)y < (unsigned)Lanes::WIDTH && y < left) {
+            // this lane's quad with column y, if it has it
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (y == Lanes::col(q) + u) zl[r] = v[q][u];
-            }
+            for (int q = 0; q < 8; ++q)
+                if ((y & ~3) == Lanes::col(q)) {
+                    const float lo = y & 1 ? v[q][1] : v[q][0], hi = y & 1 ? v[q][3] : v[q][2];
+                    zl[r] = y & 2 ? hi : lo;
+                }
         }
-        if (col + Lanes::WIDTH > V) {                  // the vocabulary's end
+        if (EDGE) {                                    // the vocabulary's end
 #pragma unroll
             for (int q = 0; q < 8; ++q)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (col + Lanes::col(q) + u >= V) v[q][u] = -INFINITY;
+                    v[q][u] = Lanes::col(q) + u < left ? v[q][u] : -INFINITY;
         }
-        float m = -INFINITY;
+        float m = fmaxf(v[0][0], v[0][1]);
+        m = max3(m, v[0][2], v[0][3]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            m = fmaxf(fmaxf(m, fmaxf(v[q][0], v[q][1])), fmaxf(v[q][2], v[q][3]));
+        for (int q = 1; q < 8; ++q) m = max3(max3(m, v[q][0], v[q][1]), v[q][2], v[q][3]);
         m = Lanes::max(m);
         const float ref = m == -INFINITY ? 0.0f : m;   // no column here, or none finite
         const float m2 = ref * kLog2e;
-        float s = 0.0f;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t w[8][2];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 8; ++q) {
+            float x[4], e[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) s += exp2_hw(fmaf(v[q][u], kLog2e, -m2));
-        s = Lanes::sum(s);
+            for (int u = 0; u < 4; ++u) x[u] = fmaf(v[q][u], kLog2e, -m2);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) e[u] = exp2_hw(x[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] += e[u];
+            if (kCodes)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) w[q][u] = code_pair(x[2 * u], x[2 * u + 1]);
+        }
+        if (kCodes && code) store_pairs<EDGE>(code + r * ldz + col, in, room, w);
+        const float sum = Lanes::sum((s[0] + s[1]) + (s[2] + s[3]));
         const long at = (long)(col / Lanes::WIDTH) * sp + r * sr;
         if (tstat) {
             const float mt = ref * l2t;
-            float t = 0.0f;
+            float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < 8; ++q)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) t += exp2_hw(fmaf(v[q][u], l2t, -mt));
-            t = Lanes::sum(t);
-            if (in && Lanes::first()) tstat[at] = t;
+                for (int u = 0; u < 4; ++u) t[u] += exp2_hw(fmaf(v[q][u], l2t, -mt));
+            const float tsum = Lanes::sum((t[0] + t[1]) + (t[2] + t[3]));
+            if (in && Lanes::first()) tstat[at] = tsum;
         }
-        if (in && Lanes::first()) stat[at] = make_float2(m, s);
+        if (in && Lanes::first()) stat[at] = make_float2(m, sum);
     }
 };
 
@@ -456,35 +524,30 @@ __device__ __forceinline__ void ld8(const T* p, float* v) {
     if constexpr (sizeof(T) == 4) Vec16<T>::ld(p + 4, v + 4);
 }
 
-// A row's quads to out (row start): bf16 ones in 16-byte stores, two lanes 16
-// apart trading halves of two neighbouring fragments.
+// A row's quads to out (row start).
 template <class Lanes, typename T>
 __device__ __forceinline__ void store_row(T* out, bool in, int cl, int cols, const f32x4 (&v)[8]) {
     if constexpr (sizeof(T) == 4) {
+        out += cl;
+        cols -= cl;
+        if (cols >= Lanes::WIDTH) {
+            if (in)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int c = cl + Lanes::col(q);
-            if (in && c < cols) *reinterpret_cast<f32x4*>(out + c) = v[q];
+                for (int q = 0; q < 8; ++q) *reinterpret_cast<f32x4*>(out + Lanes::col(q)) = v[q];
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (in && Lanes::col(q) < cols)
+                    *reinterpret_cast<f32x4*>(out + Lanes::col(q)) = v[q];
         }
     } else {
-        // after the swap of X's odd 16-lane rows with Y's even ones a lane of an
-        // even row holds 8 columns of fragment q, of an odd one of fragment q + 1
-        const int g = (threadIdx.x >> 4) & 3;
-        const int c0 = cl + (g & 1) * 16 + (g >> 1) * 8;
+        uint32_t w[8][2];
 #pragma unroll
-        for (int q = 0; q < 8; q += 2) {
-            u32x4_t w;
+        for (int q = 0; q < 8; ++q)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const auto sw = __builtin_amdgcn_permlane16_swap(
-                    pack_bf16x2(v[q][2 * u], v[q][2 * u + 1]),
-                    pack_bf16x2(v[q + 1][2 * u], v[q + 1][2 * u + 1]), false, false);
-                w[u] = sw[0];
-                w[2 + u] = sw[1];
-            }
-            const int c = c0 + q * 16;
-            if (in && c < cols) *reinterpret_cast<u32x4_t*>(out + c) = w;
-        }
+            for (int u = 0; u < 2; ++u) w[q][u] = pack_bf16x2(v[q][2 * u], v[q][2 * u + 1]);
+        if (cols - cl >= Lanes::WIDTH) store_pairs<false>(out + cl, in, cols - cl, w);
+        else store_pairs<true>(out + cl, in, cols - cl, w);
     }
 }
 
@@ -664,18 +727,14 @@ struct HeadOperand {
 
 // c += a b, the accumulators kept in the accumulation registers: 64 fragments
 // fill all 256 of them, and the compiler, left to choose, moves some of them to
-// the others and back in every step.
+// the others and back in every step.  The compiler does not see the waits that
+// go with it (behind it a read of the result, before it a vector instruction that
+// writes an operand), so it stands only in the loop, where its operands come
+// from LDS and its results go to the next one; a tile's last stage is made with
+// the compiler's own form.
 __device__ __forceinline__ void mfma16(f32x4& c, const bf16x8& a, const bf16x8& b) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
-// The wait between the last of them and the first read of their results, which
-// depends on it through the operands.
-__device__ __forceinline__ void mfma_done(f32x4 (&c)[8]) {
-    asm volatile("s_nop 15\n\ts_nop 15"
-                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]),
-                   "+a"(c[6]), "+a"(c[7]));
-}
-
 // bf16: 256 x 256 tiles, four waves of 128 x 128 (one a SIMD), operands straight
 // from HBM into a ring of NU units (a unit: one operand's 256 rows of a stage of
 // BK reduction steps, 32 KB; A's and B's take turns, unit u in slot u mod NU).
@@ -697,7 +756,8 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
     if (piece_done(p)) return;
     const HeadTile ti = head_tile<256, 256>(p, block);
     if (!ti.live) return;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);    // (uniform, for the branches)
     const int wm = wv >> 1, wn = wv & 1;
 
     int asked[8];
@@ -720,11 +780,12 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
         for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     bf16x8 af[2][8], bfr[2][8];
 
-    const int nj = (ti.k1 - ti.k0 + BK - 1) / BK;
     // stages past the end are loaded too, from an empty range: no memory is
-    // read, and the counts of loads in flight stay the same to the end
-    auto rsA = [&](int j) { return opA.words((long)ti.k0 + (long)j * BK, j < nj); };
-    auto rsB = [&](int j) { return opB.words((long)ti.k0 + (long)j * BK, j < nj); };
+    // read, and the counts of loads in flight stay the same to the end (an empty
+    // reduction is one such stage: zeros)
+    const int some = (ti.k1 - ti.k0 + BK - 1) / BK, nj = max(some, 1);
+    auto rsA = [&](int j) { return opA.words((long)ti.k0 + (long)j * BK, j < some); };
+    auto rsB = [&](int j) { return opB.words((long)ti.k0 + (long)j * BK, j < some); };
     auto wrap = [](int q) { return q >= NU ? q - NU : q; };
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(ringbuf) + wv * 1024);
     auto slot = [&](int q) { return lds0 + (uint32_t)(q * UNIT); };
@@ -744,11 +805,16 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
                     auto COUNT, auto&& load) {
         constexpr int buf = decltype(BUF)::value, first = decltype(FIRST)::value,
                       gap = decltype(GAP)::value, n = decltype(COUNT)::value;
-        static_assert(first + gap * (n - 1) < 64, "loads behind the products");
+        constexpr bool last = n == 0;          // (a tile's last stage, which loads nothing)
+        static_assert(n == 0 || first + gap * (n - 1) < 64, "loads behind the products");
         unroll<64>([&](auto Q) {
             constexpr int q = decltype(Q)::value;
-            mfma16(acc[q / 8][q % 8], bfr[buf][q % 8], af[buf][q / 8]);   // (columns as rows)
-            if constexpr (q % 2 == 0 && q < 32)
+            if constexpr (last)                // (columns as rows)
+                acc[q / 8][q % 8] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    bfr[buf][q % 8], af[buf][q / 8], acc[q / 8][q % 8], 0, 0, 0);
+            else
+                mfma16(acc[q / 8][q % 8], bfr[buf][q % 8], af[buf][q / 8]);
+            if constexpr (q % 2 == 0 && q < 32 && !(last && buf == 1))
                 read1(std::integral_constant<int, q / 2>{}, S, std::integral_constant<int, 1 - buf>{},
                       ua, ub);
             if constexpr (q >= first && (q - first) % gap == 0 && (q - first) / gap < n)
@@ -776,7 +842,7 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
     typedef std::integral_constant<int, 32 / NL> GAP;
     typedef std::integral_constant<int, NL> CNT;
 #pragma unroll 1
-    for (int j = 0; j < nj; ++j) {
+    for (int j = 0; j + 1 < nj; ++j) {
         const uint32_t ua = unit(qa), ub = unit(wrap(qa + 1));
         const i32x4_t ra = rsA(j + 2);
         step(I0{}, I1{}, ua, ub, std::integral_constant<int, 33>{}, GAP{}, CNT{}, [&](auto I) {
@@ -790,11 +856,12 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
         });
         qa = qn;
     }
+    step(I0{}, I1{}, unit(qa), unit(wrap(qa + 1)), I1{}, I1{}, I0{}, [](auto) {});
+    step(I1{}, I0{}, 0u, 0u, I1{}, I1{}, I0{}, [](auto) {});
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // (loads of the empty stages)
     // (a row of fragments at a time, so that the others stay where they are)
     const bool part = Epi::kSplits && ti.slot >= 0;
     unroll<8>([&](auto I) {
-        mfma_done(acc[I]);
         const int rl = wm * 128 + I * 16 + (lane & 15);
         if (part) store_part<Quads16, 256, 256>(p.part, ti, rl, wn * 128, acc[I]);
         else epi.template row<Quads16>(ti, rl, wn * 128, acc[I], asked[I]);
@@ -857,7 +924,8 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<float>& p, cons
     if (piece_done(p)) return;
     const HeadTile ti = head_tile<FBM, FBM>(p, block);
     if (!ti.live) return;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wv >> 1, wn = wv & 1;
     int asked[2];
 #pragma unroll
@@ -1069,7 +1137,9 @@ __global__ __launch_bounds__(1024) void head_lse_kernel(
 // ----------------------------------------------------------------- dz
 
 struct HeadDz {
-    const float* Z;          // [piece][ldz] scores
+    const float* Z;          // [piece][ldz] scores, or
+    const uint16_t* code;    // coded ones and the labels' scores
+    const float* zl;         // [piece]
     long ldz;
     void* G;                 // [piece][ldz] dz
     int segs, seg;           // segments of a row, their length (a multiple of 256)
@@ -1095,17 +1165,18 @@ struct HeadDz {
 // One wave a row, or a segment of one when the rows are few.  The dz of the label
 // and the teacher's slots are written behind the others (an entry named twice by
 // its first slot, with the slots' q added in order).
-template <typename T>
+template <typename T, bool CODED>
 __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
-    __shared__ int s_idx[4][kMaxK];
-    __shared__ float s_q[4][kMaxK];
+    static_assert(!CODED || sizeof(T) == 2, "coded scores are for bf16 dz");
+    __shared__ int s_idx[CODED ? 1 : 4][kMaxK];
+    __shared__ float s_q[CODED ? 1 : 4][kMaxK];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int n = piece_rows(p.count, p.p0, p.piece, 0);
     const int item = blockIdx.x * 4 + w;
     const int r = item / p.segs, part = item - r * p.segs;
     if (r >= n) return;                       // whole waves; no block barrier below
     const int t = p.rows[p.p0 + r];
-    const float* z = p.Z + (long)r * p.ldz;
+    const float* z = CODED ? nullptr : p.Z + (long)r * p.ldz;
     const int c0 = part * p.seg, c1 = (int)min(p.ldz, (long)c0 + p.seg);
     int label = p.labels ? p.labels[t] : -1;
     if (!in_vocab(label, p.V)) label = -1;
@@ -1125,8 +1196,46 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     const Norm2 tn = {m * p.l2t, p.tstat ? __builtin_amdgcn_logf(wave_sum(st)) : 0.0f};
     if (p.loss && part == 0 && lane == 0) {
         const float l = norm_ln(nm, m, 1.0f, kLog2e);
-        p.loss[t] = label >= 0 ? l - z[label] : 0.0f;
+        p.loss[t] = label >= 0 ? l - (CODED ? p.zl[r] : z[label]) : 0.0f;
         if (p.lse) p.lse[t] = label >= 0 ? l : 0.0f;
+    }
+    if constexpr (CODED) {
+        // every row has a label; dz = w 2^(m' - step * code - log2 of the sum), m' the part's
+        bf16_t* g = static_cast<bf16_t*>(p.G) + (long)r * p.ldz;
+        const uint16_t* cr = p.code + (long)r * p.ldz;
+        const float norm = nm.a + nm.b;
+        constexpr int U = 4;                  // units of 512 in flight
+        for (int c = c0 + lane * 8; c < c1; c += 512 * U) {
+            u32x4_t w[U];
+            float top[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + 512 * u < c1) {       // read once: not kept
+                    w[u] = __builtin_nontemporal_load(
+                        reinterpret_cast<const u32x4_t*>(cr + c + 512 * u));
+                    top[u] = sp[(c + 512 * u) >> 7].x;
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int cu = c + 512 * u;
+                if (cu >= c1) break;
+                const float b = top[u] * kLog2e - norm;
+                u32x4_t o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float lo = (float)(w[u][e] & 0xffffu), hi = (float)(w[u][e] >> 16);
+                    const float vl = wce * exp2_hw(fmaf(lo, -kCodeStep, b));
+                    const float vh = wce * exp2_hw(fmaf(hi, -kCodeStep, b));
+                    o[e] = pack_bf16x2(cu + 2 * e < p.V ? vl : 0.0f,
+                                       cu + 2 * e + 1 < p.V ? vh : 0.0f);
+                }
+                *reinterpret_cast<u32x4_t*>(g + cu) = wce != 0.0f ? o : u32x4_t{0, 0, 0, 0};
+            }
+        }
+        wave_mem_sync();
+        if (lane == 0 && label >= c0 && label < c1 && wce != 0.0f)
+            g[label] = f32_to_bf16(wce * norm_p(nm, p.zl[r], kLog2e) - wce);
+        return;
     }
 
     // the teacher's distribution
@@ -1251,14 +1360,15 @@ constexpr int kSubUnits = 12;          // row tiles whose scores are held at a t
 
 // A call takes its tokens in `pieces` of `piece` rows, whose dz (or x alone, for a
 // loss without gradient) is held at a time, and a piece in steps of `sub`
-// rows, whose scores are: 4 bytes a score for 3072 rows at most, 2 (fp32: 4) for
-// the others.
+// rows, whose scores are: 4 (coded: 2) bytes a score for 3072 rows at most, 2
+// (fp32: 4) for dz.
 struct HeadPlan {
     int piece, pieces, sub, parts;
     long ldz;
     int segs, seg;                     // of a row of dz
     size_t rows, clab, count, plan, act, xc, zl, stat, tstat, z, g, part_dx, part_dw, acc, total;
-    bool direct, slots_dx, slots_dw;   // x as it is; products that may be split
+    bool direct, coded;                // x as it is; scores in 16 bits
+    bool slots_dx, slots_dw;           // products that may be split
 };
 
 // Slots that a product with up to `tiles` tiles and K reduction steps can use
@@ -1273,6 +1383,7 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     const size_t b = dt == MOE_BF16 ? 2 : 4;
     const bool store = grad || K > 0;
     const int bm = dt == MOE_BF16 ? 256 : 128, pc = dt == MOE_BF16 ? 128 : 64;
+    p.coded = grad && K == 0 && dt == MOE_BF16;
     p.piece = piece;
     p.pieces = T == 0 ? 0 : cdiv(T, piece);
     // steps of 6 to 12 row tiles, of those the ones that leave the fewest rounds of
@@ -1302,7 +1413,7 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
         return at;
     };
     p.rows = take((size_t)T * 4);
-    p.clab = take(store ? 0 : (size_t)T * 4);
+    p.clab = take(K == 0 ? (size_t)T * 4 : 0);
     p.count = take(4);
     p.plan = take(grad ? (size_t)p.pieces * 8 : 0);
     p.act = take(K > 0 ? (size_t)T * 4 : 0);
@@ -1312,7 +1423,7 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     p.zl = take(rmax * 4);
     p.stat = take(rmax * p.parts * 8);
     p.tstat = take(K > 0 ? rmax * p.parts * 4 : 0);
-    p.z = take(store ? rmax * p.ldz * 4 : 0);
+    p.z = take(store ? rmax * p.ldz * (p.coded ? 2 : 4) : 0);
     p.g = take(grad ? (size_t)piece * p.ldz * b : 0);
     const long cols = cdiv(d, bm);
     const long sx = head_slots(cdiv(piece, bm) * cols, V, dt == MOE_F32);
@@ -1390,11 +1501,12 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
     int32_t* count = reinterpret_cast<int32_t*>(ws + p.count);
     int32_t* plan = c.grad ? reinterpret_cast<int32_t*>(ws + p.plan) : nullptr;
-    int32_t* clab = store ? nullptr : reinterpret_cast<int32_t*>(ws + p.clab);
+    int32_t* clab = teacher ? nullptr : reinterpret_cast<int32_t*>(ws + p.clab);
     float2* stat = reinterpret_cast<float2*>(ws + p.stat);
     float* tstat = teacher ? reinterpret_cast<float*>(ws + p.tstat) : nullptr;
     float* zl = reinterpret_cast<float*>(ws + p.zl);
-    float* Z = store ? reinterpret_cast<float*>(ws + p.z) : nullptr;
+    float* Z = store && !p.coded ? reinterpret_cast<float*>(ws + p.z) : nullptr;
+    uint16_t* code = p.coded ? reinterpret_cast<uint16_t*>(ws + p.z) : nullptr;
     T* G = reinterpret_cast<T*>(ws + p.g);
     T* xc = reinterpret_cast<T*>(ws + p.xc);
     const float inv_tau = 1.0f / c.tau, l2t = (float)(1.4426950408889634 / (double)c.tau);
@@ -1446,7 +1558,8 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
             // statistics by row for head_dz, by part for head_lse; the label's score
             // comes from z where that is kept
             const EpiScores es = {c.V, stat, tstat, store ? 1 : (long)p.sub, store ? p.parts : 1, l2t,
-                                  store ? nullptr : p.direct ? c.labels : clab + s0, zl, Z, p.ldz};
+                                  teacher ? nullptr : p.direct ? c.labels : clab + s0, zl, Z, code,
+                                  p.ldz};
             head_scores(g, sn, es, s);
             if (!store) {
                 MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
@@ -1455,11 +1568,17 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
                 continue;
             }
             const int segs = c.grad ? p.segs : 1;
-            const HeadDz dz = {Z, p.ldz, G + (long)q0 * p.ldz, segs, p.seg, c.V, rows, count, s0, sn,
+            const HeadDz dz = {Z, code, zl, p.ldz, G + (long)q0 * p.ldz, segs, p.seg, c.V, rows, count, s0, sn,
                                stat, tstat, p.parts, c.loss, c.lse, c.labels, c.weight, c.tidx,
                                c.tlogit, c.tweight, c.K, c.tau, inv_tau, l2t, c.kd, c.grad};
-            MOE_LAUNCH("head_dz", s,
-                       head_dz_kernel<T><<<cdiv((long)sn * segs, 4), 256, 0, s>>>(dz));
+            const int blocks = cdiv((long)sn * segs, 4);
+            if constexpr (sizeof(T) == 2) {
+                if (p.coded) {
+                    MOE_LAUNCH("head_dz", s, head_dz_kernel<T, true><<<blocks, 256, 0, s>>>(dz));
+                    continue;
+                }
+            }
+            MOE_LAUNCH("head_dz", s, head_dz_kernel<T, false><<<blocks, 256, 0, s>>>(dz));
         }
         if (!c.grad) continue;
         HeadGemm<T> gx = g, gw = g;

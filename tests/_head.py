@@ -10,7 +10,11 @@ matrix instructions whose inner order and rounding are not specified):
          of z - m, m + ln s and their like
   loss   e(lse) + e(z) + 2^-22 |loss|
   kd     tau^2 sum_j q_j (e(z)/tau + e(lse at tau) + 2^-19 (1 + |terms|))
-  p      relative: e(z) + e(lse)
+  p      relative: e(z) + e(lse); for the bf16 cross entropy without a teacher also
+         ln 2 * 2^-11, half a step of the 16-bit scores that dz is made from (steps
+         of 2^-10 of log2: a score is off by at most 2^-11 there, its exponential
+         by the factor 2^(2^-11)), plus 2^-64 of the largest p where a score lies
+         64 or more below its 128 columns' largest and counts as 64
   dz     w p e(p) + u |dz|  (the rounding to the storage type)
   dx     |e(dz)| |Wv| + g(V) |dz| |Wv| + u |dx|,  dWv likewise
 """
@@ -73,6 +77,8 @@ def reference(x, Wv, labels=None, weight=None, teacher=None, tau=1.0, dt="bf16")
         dz += p
         dz[row, at] -= w
         edz += p.abs() * (ez + el[:, None] + 2.0 ** -20)
+        if dt == "bf16" and teacher is None:
+            edz += p.abs() * math.log(2.0) * 2.0 ** -11 + w.abs()[:, None] * 2.0 ** -64
     if teacher is not None:
         l, el = lse_of(1.0 / tau)
         q = torch.softmax(torch.where(on, score / tau, torch.full_like(score, -math.inf)), 1)
