@@ -16,8 +16,8 @@
 //               reduces every row's 128 columns to (max, sum of exp) from the
 //               fp32 accumulators, so the normaliser needs no second look at
 //               z, and z is stored only when something reads it;
-//  head_dz      z -> dz, a stream; the scores are held for up to 3072 tokens at a
-//               time (row tiles share a column tile's weights), dz for the piece;
+//  head_dz      z -> dz, a stream; the scores are held for a few row tiles at a
+//               time (they share a column tile's weights), dz for the piece;
 //  head_product dx = dz Wv and dWv = dz^T x, the tiles after the last full round
 //               of the compute units split over the reduction; dWv is summed over the
 //               pieces in fp32.
@@ -27,7 +27,11 @@
 //
 // Roundings (bf16): dz is rounded once to bf16 as an operand of the matrix
 // cores (the cross entropy's from scores kept within 3.4e-4 of exp(z), see
-// code_pair); every sum is fp32; dx and dWv are rounded once.
+// code_pair); every sum is fp32; dx and dWv are rounded once.  A row of dz mostly is
+// its label's entry, or a teacher's first one, whose rounding alone would be as
+// large as that of the results: what it loses stays in fp32 (HeadTop) and is added
+// to the row of dx.  In dWv the roundings of many tokens average out, with few
+// tokens they do not: up to 128 tokens dz is two bf16 terms there (HeadGemm::terms).
 #include <algorithm>
 #include <type_traits>
 
@@ -39,6 +43,14 @@ namespace {
 
 constexpr int kMaxK = 256;              // teacher slots of a token
 constexpr int kRowAlign = 256;          // tokens of a piece: whole row tiles
+constexpr int kTermTokens = 128;        // up to so many, dz is two terms in dWv
+
+// What bf16 took from the largest of a row's named entries of dz (the label, the
+// teacher's slots): dz there is the rounded value plus `lost`.
+struct HeadTop {
+    int col;
+    float lost;
+};
 
 // The wave's stores before it are done: a later one of another lane to the same
 // place comes behind them.
@@ -139,6 +151,7 @@ __device__ __forceinline__ int rest_parts(int R, int nj, bool f32) {
 struct HeadParts {
     int32_t* plan;
     int pieces, piece, d, V, bm;
+    int terms;               // of dz in dWv
 };
 
 // Whether token t has a loss: by its label, by its teacher's slots, or as
@@ -179,7 +192,8 @@ struct HeadStart {
             const int k = max(0, min(n - (i >> 1) * parts.piece, parts.piece));
             const int nM = ((i & 1) ? parts.V + parts.bm - 1 : k + parts.bm - 1) / parts.bm;
             const int tiles = nM * ((parts.d + parts.bm - 1) / parts.bm);
-            const int best = rest_parts(tiles % kRound, ((i & 1) ? k + 63 : parts.V + 63) / 64,
+            const int best = rest_parts(tiles % kRound,
+                                        ((i & 1) ? k * parts.terms + 63 : parts.V + 63) / 64,
                                         parts.bm == 128);
             if ((threadIdx.x & 63) == 0) parts.plan[i] = best;
         }
@@ -220,10 +234,11 @@ __global__ __launch_bounds__(1024) void head_compact_kernel(HeadTokens tk, HeadS
 }
 
 // For up to 4096 tokens: the same and the row copies (head_gather) in one launch.
-// Every block makes the whole list, in LDS; block 0 writes it out.
+// Every block makes the whole list, in LDS; block 0 writes it out.  copies: of a row,
+// one behind the other (one per term of dz).
 __global__ __launch_bounds__(1024) void head_start_kernel(HeadTokens tk, HeadStart st,
                                                           const u32x4_t* __restrict__ x, int vpr,
-                                                          u32x4_t* __restrict__ xc,
+                                                          u32x4_t* __restrict__ xc, int copies,
                                                           u32x4_t* __restrict__ dx) {
     __shared__ int sh[16];
     __shared__ int list[kStartTokens];
@@ -237,7 +252,8 @@ __global__ __launch_bounds__(1024) void head_start_kernel(HeadTokens tk, HeadSta
     const int step = gridDim.x * 1024;
     for (int i = blockIdx.x * 1024 + threadIdx.x; i < n * vpr; i += step) {
         const int r = i / vpr, c = i - r * vpr;
-        xc[i] = x[(long)list[r] * vpr + c];
+        const u32x4_t v = x[(long)list[r] * vpr + c];
+        for (int k = 0; k < copies; ++k) xc[((long)r * copies + k) * vpr + c] = v;
     }
     if (!dx || n == tk.T) return;
     for (int i = blockIdx.x * 1024 + threadIdx.x; i < tk.T * vpr; i += step)
@@ -257,21 +273,26 @@ __global__ __launch_bounds__(256) void head_gather_kernel(
     const int32_t* __restrict__ count, int p0, int piece, int vpr, u32x4_t* __restrict__ xc,
     HeadTokens tk, u32x4_t* __restrict__ dx) {
     const int n = piece_rows(count, p0, piece, 0);
-    const long i = (long)blockIdx.x * 256 + threadIdx.x;
-    const long r = i / vpr;
-    const int c = (int)(i - r * vpr);
-    if (r < n) {
-        const int t = rows[p0 + r];
-        MOE_DASSERT(t >= 0 && t < tk.T);
-        xc[r * vpr + c] = x[(long)t * vpr + c];
+    const long end = (long)(dx ? tk.T : n) * vpr;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < end; i += (long)gridDim.x * 256) {
+        const long r = i / vpr;
+        const int c = (int)(i - r * vpr);
+        if (r < n) {
+            const int t = rows[p0 + r];
+            MOE_DASSERT(t >= 0 && t < tk.T);
+            xc[i] = x[(long)t * vpr + c];
+        }
+        if (dx && !tk.has_loss((int)r)) dx[i] = u32x4_t{0, 0, 0, 0};
     }
-    if (dx && r < tk.T && !tk.has_loss((int)r)) dx[r * vpr + c] = u32x4_t{0, 0, 0, 0};
 }
 
 __global__ __launch_bounds__(256) void head_zero_kernel(u32x4_t* __restrict__ p, long n) {
-    const long i = (long)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = u32x4_t{0, 0, 0, 0};
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256)
+        p[i] = u32x4_t{0, 0, 0, 0};
 }
+// Blocks of 256 threads for n items, by those kernels' strides: a launch has fewer
+// than 2^32 threads.
+inline int head_blocks(long n) { return (int)std::min((n + 255) / 256, 1l << 22); }
 
 // ------------------------------------------------------- matrix products
 
@@ -288,6 +309,7 @@ struct HeadGemm {
     long ldb;
     int M, N, K;
     int dyn;                 // 1: M, 2: K is the piece's rows (0: neither)
+    int terms;               // reduction rows of a piece's row (dyn 2)
     const int32_t* count;
     int p0, piece;
     const int32_t* plan;     // parts of a rest tile (NULL: 1)
@@ -317,7 +339,7 @@ template <int BM, int BN, typename T>
 __device__ __forceinline__ HeadTile head_tile(const HeadGemm<T>& p, int block) {
     HeadTile t;
     const int n = p.dyn ? piece_rows(p.count, p.p0, p.piece, p.piece) : 0;
-    const int M = p.dyn == 1 ? n : p.M, K = p.dyn == 2 ? n : p.K;
+    const int M = p.dyn == 1 ? n : p.M, K = p.dyn == 2 ? n * p.terms : p.K;
     const int nM = (M + BM - 1) / BM, nN = (p.N + BN - 1) / BN, tiles = nM * nN;
     const int S = p.plan ? *p.plan : 1;
     const int full = S > 1 ? tiles / kRound * kRound : tiles;
@@ -419,6 +441,7 @@ __device__ __forceinline__ void store_pairs(void* out, bool in, int cols,
 // before the hardware's 2^x, the same m' wherever the sum is used.
 struct EpiScores {
     static constexpr bool kSplits = false;
+    typedef int Ask;
     int V;
     float2* stat;            // (m, sum) of a row's part: part * sp + row * sr
     float* tstat;            // the sum at the temperature likewise, or NULL
@@ -551,7 +574,7 @@ __device__ __forceinline__ void store_row(T* out, bool in, int cl, int cols, con
     }
 }
 
-// dx rows, back at their tokens.
+// dx rows, back at their tokens, with what dz lost in bf16: lost * Wv[col].
 template <typename T>
 struct EpiRows {
     static constexpr bool kSplits = true;
@@ -559,16 +582,53 @@ struct EpiRows {
     long ldo;
     const int32_t* rows;
     int p0;
-    __device__ __forceinline__ int ask(const HeadTile& ti, int rl) const {
-        return rl < ti.rows ? rows[p0 + ti.m0 + rl] : 0;
+    const HeadTop* top;      // [piece] (bf16)
+    const T* Wv;             // [V][ldo]
+    // a piece's row: its token, and what it lost (fp32: nothing)
+    struct Ask {
+        int token;
+        HeadTop lost;
+    };
+    __device__ __forceinline__ Ask of(int r) const {
+        if constexpr (sizeof(T) == 2) return {rows[p0 + r], top[r]};
+        else return {rows[p0 + r], {0, 0.0f}};
+    }
+    __device__ __forceinline__ Ask ask(const HeadTile& ti, int rl) const {
+        return rl < ti.rows ? of(ti.m0 + rl) : Ask{0, {0, 0.0f}};
     }
     template <class Lanes>
-    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, const f32x4 (&v)[8],
-                                        int token) const {
-        store_row<Lanes>(out + (long)token * ldo + ti.n0, rl < ti.rows, cl, ti.cols, v);
+    __device__ __forceinline__ void row(const HeadTile& ti, int rl, int cl, f32x4 (&v)[8],
+                                        const Ask& k) const {
+        const bool in = rl < ti.rows;
+        if constexpr (sizeof(T) == 2) {
+            const HeadTop a = k.lost;
+            if (a.lost != 0.0f) {
+                const T* w = Wv + (long)a.col * ldo + ti.n0 + cl;
+                uint2 b[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    b[q] = cl + Lanes::col(q) < ti.cols
+                               ? *reinterpret_cast<const uint2*>(w + Lanes::col(q)) : uint2{0, 0};
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    v[q][0] = fmaf(a.lost, __uint_as_float(b[q].x << 16), v[q][0]);
+                    v[q][1] = fmaf(a.lost, __uint_as_float(b[q].x & 0xffff0000u), v[q][1]);
+                    v[q][2] = fmaf(a.lost, __uint_as_float(b[q].y << 16), v[q][2]);
+                    v[q][3] = fmaf(a.lost, __uint_as_float(b[q].y & 0xffff0000u), v[q][3]);
+                }
+            }
+        }
+        store_row<Lanes>(out + (long)k.token * ldo + ti.n0, in, cl, ti.cols, v);
     }
-    __device__ __forceinline__ void put8(int r, int c, const float* v) const {
-        st8(out + (long)rows[p0 + r] * ldo + c, v);
+    __device__ __forceinline__ void put8(int r, int c, float* v) const {
+        const Ask k = of(r);
+        if (sizeof(T) == 2 && k.lost.lost != 0.0f) {
+            float w[8];
+            ld8(Wv + (long)k.lost.col * ldo + c, w);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = fmaf(k.lost.lost, w[u], v[u]);
+        }
+        st8(out + (long)k.token * ldo + c, v);
     }
 };
 
@@ -576,6 +636,7 @@ struct EpiRows {
 template <typename T>
 struct EpiSum {
     static constexpr bool kSplits = true;
+    typedef int Ask;
     T* out;
     float* acc;
     long ldo;
@@ -760,7 +821,7 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);    // (uniform, for the branches)
     const int wm = wv >> 1, wn = wv & 1;
 
-    int asked[8];
+    typename Epi::Ask asked[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) asked[i] = epi.ask(ti, wm * 128 + i * 16 + (lane & 15));
     typedef HeadOperand<ALAY, BK, 4> OpA;
@@ -927,7 +988,7 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<float>& p, cons
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wv >> 1, wn = wv & 1;
-    int asked[2];
+    typename Epi::Ask asked[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) asked[i] = epi.ask(ti, wm * 64 + i * 32 + (lane & 31));
     typedef HeadOperandF32<ALAY> OpA;
@@ -1136,12 +1197,37 @@ __global__ __launch_bounds__(1024) void head_lse_kernel(
 
 // ----------------------------------------------------------------- dz
 
+// The second bf16 terms of two values whose first ones are `hi`.
+__device__ __forceinline__ uint32_t second_terms(float a, float b, uint32_t hi) {
+    return pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+// What a value loses as an element of T (exact in fp32); 0 if it is not finite there.
+template <typename T>
+__device__ __forceinline__ float lost_of(float v) {
+    if constexpr (sizeof(T) == 4) {
+        return 0.0f;
+    } else {
+        const float lost = v - bf16_to_f32(f32_to_bf16(v));
+        return fabsf(lost) < INFINITY ? lost : 0.0f;
+    }
+}
+// One element of dz, in one or two terms.
+template <bool TERMS, typename T>
+__device__ __forceinline__ float put_dz(T* g, long second, float v) {
+    const float lost = lost_of<T>(v);
+    Elem<T>::st(g, v);
+    if (TERMS) Elem<T>::st(g + second, lost);
+    return lost;
+}
+
 struct HeadDz {
     const float* Z;          // [piece][ldz] scores, or
     const uint16_t* code;    // coded ones and the labels' scores
     const float* zl;         // [piece]
     long ldz;
-    void* G;                 // [piece][ldz] dz
+    void* G;                 // [piece][ldg] dz, its second term (if any) ldz further
+    long ldg;
+    HeadTop* top;            // [piece] (bf16)
     int segs, seg;           // segments of a row, their length (a multiple of 256)
     int V;
     const int32_t* rows;
@@ -1165,9 +1251,9 @@ struct HeadDz {
 // One wave a row, or a segment of one when the rows are few.  The dz of the label
 // and the teacher's slots are written behind the others (an entry named twice by
 // its first slot, with the slots' q added in order).
-template <typename T, bool CODED>
+template <typename T, bool CODED, bool TERMS>
 __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
-    static_assert(!CODED || sizeof(T) == 2, "coded scores are for bf16 dz");
+    static_assert((!CODED && !TERMS) || sizeof(T) == 2, "coded scores, two terms: bf16 dz");
     __shared__ int s_idx[CODED ? 1 : 4][kMaxK];
     __shared__ float s_q[CODED ? 1 : 4][kMaxK];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -1201,7 +1287,7 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     }
     if constexpr (CODED) {
         // every row has a label; dz = w 2^(m' - step * code - log2 of the sum), m' the part's
-        bf16_t* g = static_cast<bf16_t*>(p.G) + (long)r * p.ldz;
+        bf16_t* g = static_cast<bf16_t*>(p.G) + (long)r * p.ldg;
         const uint16_t* cr = p.code + (long)r * p.ldz;
         const float norm = nm.a + nm.b;
         constexpr int U = 4;                  // units of 512 in flight
@@ -1220,21 +1306,29 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
                 const int cu = c + 512 * u;
                 if (cu >= c1) break;
                 const float b = top[u] * kLog2e - norm;
-                u32x4_t o;
+                u32x4_t o, o2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float lo = (float)(w[u][e] & 0xffffu), hi = (float)(w[u][e] >> 16);
                     const float vl = wce * exp2_hw(fmaf(lo, -kCodeStep, b));
                     const float vh = wce * exp2_hw(fmaf(hi, -kCodeStep, b));
-                    o[e] = pack_bf16x2(cu + 2 * e < p.V ? vl : 0.0f,
-                                       cu + 2 * e + 1 < p.V ? vh : 0.0f);
+                    const float a = cu + 2 * e < p.V ? vl : 0.0f;
+                    const float b2 = cu + 2 * e + 1 < p.V ? vh : 0.0f;
+                    o[e] = pack_bf16x2(a, b2);
+                    if (TERMS) o2[e] = second_terms(a, b2, o[e]);
                 }
-                *reinterpret_cast<u32x4_t*>(g + cu) = wce != 0.0f ? o : u32x4_t{0, 0, 0, 0};
+                const bool on = wce != 0.0f;
+                *reinterpret_cast<u32x4_t*>(g + cu) = on ? o : u32x4_t{0, 0, 0, 0};
+                if (TERMS)
+                    *reinterpret_cast<u32x4_t*>(g + p.ldz + cu) = on ? o2 : u32x4_t{0, 0, 0, 0};
             }
         }
         wave_mem_sync();
-        if (lane == 0 && label >= c0 && label < c1 && wce != 0.0f)
-            g[label] = f32_to_bf16(wce * norm_p(nm, p.zl[r], kLog2e) - wce);
+        if (lane == 0 && label >= c0 && label < c1) {
+            const float v = wce != 0.0f ? wce * norm_p(nm, p.zl[r], kLog2e) - wce : 0.0f;
+            const float lost = put_dz<TERMS>(g + label, p.ldz, v);
+            p.top[r] = {label, lost};
+        }
         return;
     }
 
@@ -1290,7 +1384,7 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     const float zy = label >= 0 ? z[label] : 0.0f;
     wave_lds_sync();
 
-    T* g = static_cast<T*>(p.G) + (long)r * p.ldz;
+    T* g = static_cast<T*>(p.G) + (long)r * p.ldg;
     auto ce = [&](float v) { return wce * norm_p(nm, v, kLog2e); };
     auto kl = [&](float v) { return wkd * norm_p(tn, v, p.l2t); };
     auto stream = [&](auto&& dense) {
@@ -1311,8 +1405,13 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
                 if constexpr (sizeof(T) == 4) {
                     *reinterpret_cast<f32x4*>(g + cu) = v[u];
                 } else {
-                    *reinterpret_cast<uint2*>(g + cu) =
+                    const uint2 o =
                         make_uint2(pack_bf16x2(v[u][0], v[u][1]), pack_bf16x2(v[u][2], v[u][3]));
+                    *reinterpret_cast<uint2*>(g + cu) = o;
+                    if (TERMS)
+                        *reinterpret_cast<uint2*>(g + p.ldz + cu) =
+                            make_uint2(second_terms(v[u][0], v[u][1], o.x),
+                                       second_terms(v[u][2], v[u][3], o.y));
                 }
             }
         }
@@ -1323,16 +1422,23 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     else if (wce == 0.0f && wkd != 0.0f) stream(kl);
     else stream(at);
     wave_mem_sync();
-    // the label and the teacher's slots, those of this segment
+    // the label and the teacher's slots: written by the segment that has them; the
+    // first segment finds which of them loses most in bf16
     auto mine = [&](int v) { return v >= c0 && v < c1; };
     bool label_named = false;
+    HeadTop top = {0, 0.0f};
+    auto put = [&](int v, float dz) {
+        const float lost = lost_of<T>(dz);
+        if (fabsf(lost) > fabsf(top.lost)) top = {v, lost};
+        if (mine(v)) put_dz<TERMS>(g + v, p.ldz, dz);
+    };
     if (p.tidx) {
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
             const int j = lane + 64 * u;
             if (j >= p.K || idx[u] < 0) continue;
             if (idx[u] == label) label_named = true;
-            if (!mine(idx[u])) continue;
+            if (part > 0 && !mine(idx[u])) continue;
             float sum = 0.0f;
             bool first = true;
             for (int k = 0; k < p.K; ++k)
@@ -1340,12 +1446,15 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
                     first = first && k >= j;
                     sum += s_q[w][k];
                 }
-            if (first)
-                Elem<T>::st(g + idx[u], at(zt[u]) - wkd * sum - (idx[u] == label ? wce : 0.0f));
+            if (first) put(idx[u], at(zt[u]) - wkd * sum - (idx[u] == label ? wce : 0.0f));
         }
     }
-    if (label >= 0 && mine(label) && __ballot(label_named) == 0 && lane == 0)
-        Elem<T>::st(g + label, at(zy) - wce);
+    if (label >= 0 && __ballot(label_named) == 0 && lane == 0) put(label, at(zy) - wce);
+    if (sizeof(T) == 2 && part == 0) {
+        const float most = wave_max(fabsf(top.lost));
+        const int from = __ffsll((long long)__ballot(fabsf(top.lost) == most)) - 1;
+        if (lane == from) p.top[r] = top;
+    }
 }
 
 // ------------------------------------------------------------- the calls
@@ -1356,19 +1465,22 @@ inline bool head_sizes_ok(int T, int d, int V, int K, moe_dtype dt) {
 }
 
 constexpr size_t kHeadLimit = (size_t)8 << 30;
-constexpr int kSubUnits = 12;          // row tiles whose scores are held at a time, at most
+constexpr int kSubUnits = 11;          // row tiles whose scores are held at a time, at most
+// scores of a piece: its score product's blocks (a thread for 64 of them, in fp32)
+// stay below a launch's 2^32 threads
+constexpr long kPieceScores = 1l << 37;
 
 // A call takes its tokens in `pieces` of `piece` rows, whose dz (or x alone, for a
 // loss without gradient) is held at a time, and a piece in steps of `sub`
-// rows, whose scores are: 4 (coded: 2) bytes a score for 3072 rows at most, 2
-// (fp32: 4) for dz.
+// rows, whose scores are: 4 (coded: 2) bytes a score, 2 (fp32: 4) for dz.
 struct HeadPlan {
     int piece, pieces, sub, parts;
     long ldz;
     int segs, seg;                     // of a row of dz
-    size_t rows, clab, count, plan, act, xc, zl, stat, tstat, z, g, part_dx, part_dw, acc, total;
+    size_t rows, clab, count, plan, act, xc, zl, top, stat, tstat, z, g, part_dx, part_dw, acc, total;
     bool direct, coded;                // x as it is; scores in 16 bits
     bool slots_dx, slots_dw;           // products that may be split
+    int terms;                         // of dz in dWv
 };
 
 // Slots that a product with up to `tiles` tiles and K reduction steps can use
@@ -1386,7 +1498,7 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     p.coded = grad && K == 0 && dt == MOE_BF16;
     p.piece = piece;
     p.pieces = T == 0 ? 0 : cdiv(T, piece);
-    // steps of 6 to 12 row tiles, of those the ones that leave the fewest rounds of
+    // steps of 6 to 11 row tiles, of those the ones that leave the fewest rounds of
     // tiles partly empty (8192 tokens, 50257 entries: 9 row tiles 25 rounds, 8 28)
     const int units = cdiv(piece, kRowAlign), most = std::min(units, kSubUnits);
     int su = most;
@@ -1402,6 +1514,10 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     // buffers for the longest step, as a smaller batch may choose it
     const size_t rmax = store ? std::min(piece, kSubUnits * kRowAlign) : piece;
     p.ldz = (long)align_up(V, 64);
+    const bool bgrad = grad && dt == MOE_BF16;
+    p.terms = bgrad && T <= kTermTokens ? 2 : 1;
+    // rows of dz: for any smaller batch too
+    const size_t gmax = bgrad ? std::max(piece, 2 * kTermTokens) : piece;
     p.parts = cdiv(V, bm) * (bm / pc);
     // about 8192 waves for a step's rows, each 2048 elements at least
     p.seg = std::max(2048, (int)align_up(cdiv(p.ldz * p.sub, 8192), 256));
@@ -1419,15 +1535,16 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     p.act = take(K > 0 ? (size_t)T * 4 : 0);
     // a row tile's worth of tokens and no gradient: every token is scored
     p.direct = !store && T <= kRowAlign;
-    p.xc = take(p.direct ? 0 : (size_t)piece * d * b);
+    p.xc = take(p.direct ? 0 : gmax * d * b);
     p.zl = take(rmax * 4);
+    p.top = take(bgrad ? (size_t)piece * 8 : 0);
     p.stat = take(rmax * p.parts * 8);
     p.tstat = take(K > 0 ? rmax * p.parts * 4 : 0);
     p.z = take(store ? rmax * p.ldz * (p.coded ? 2 : 4) : 0);
-    p.g = take(grad ? (size_t)piece * p.ldz * b : 0);
+    p.g = take(grad ? gmax * p.ldz * b : 0);
     const long cols = cdiv(d, bm);
     const long sx = head_slots(cdiv(piece, bm) * cols, V, dt == MOE_F32);
-    const long sw = head_slots(cdiv(V, bm) * cols, piece, dt == MOE_F32);
+    const long sw = head_slots(cdiv(V, bm) * cols, gmax, dt == MOE_F32);
     p.slots_dx = sx > 0, p.slots_dw = sw > 0;
     p.part_dx = take(grad ? (size_t)sx * bm * bm * 4 : 0);
     p.part_dw = take(grad ? (size_t)sw * bm * bm * 4 : 0);
@@ -1441,13 +1558,14 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
 // (in whole row tiles), so that the last one is not a small rest.
 HeadPlan head_plan(int T, int d, int V, int K, moe_dtype dt, int grad, size_t limit) {
     const int units = std::max(1, cdiv(T, kRowAlign));
-    int lo = 1, hi = units;              // pieces: the fewest that fit
+    const int most = (int)std::min((long)units, std::max(1l, kPieceScores / kRowAlign / V));
+    int lo = cdiv(units, most), hi = units;              // pieces: the fewest that fit
     auto of = [&](int pieces) {
         const int u = cdiv(units, pieces);
         return head_layout(T, d, V, K, dt, grad,
                            T <= kRowAlign ? std::max(T, 1) : u * kRowAlign);
     };
-    const HeadPlan whole = of(1);        // (no running sum of dWv: it may be the smallest)
+    const HeadPlan whole = of(lo);       // (often no running sum of dWv: it may be the smallest)
     if (whole.total <= limit) return whole;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -1509,6 +1627,8 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     uint16_t* code = p.coded ? reinterpret_cast<uint16_t*>(ws + p.z) : nullptr;
     T* G = reinterpret_cast<T*>(ws + p.g);
     T* xc = reinterpret_cast<T*>(ws + p.xc);
+    HeadTop* top = reinterpret_cast<HeadTop*>(ws + p.top);
+    const long ldx = (long)c.d * p.terms, ldg = p.ldz * p.terms;
     const float inv_tau = 1.0f / c.tau, l2t = (float)(1.4426950408889634 / (double)c.tau);
     const int vpr = c.d * (int)sizeof(T) / 16;
     constexpr int BM = sizeof(T) == 2 ? 256 : FBM;
@@ -1516,7 +1636,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     g.count = p.direct ? nullptr : count;
     if (!p.direct) {
         HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.K, c.V, c.T};
-        const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM};
+        const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM, p.terms};
         const HeadStart st = {rows, clab, count, {c.loss, c.lse, c.kd}, hp};
         u32x4_t* dx0 = c.grad ? static_cast<u32x4_t*>(c.dx) : nullptr;
         // (a thread of the compaction looks at its tokens' slots itself: few)
@@ -1530,7 +1650,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
             const int blocks = std::max(1, std::min(256, cdiv((long)c.T * vpr, 1024)));
             MOE_LAUNCH("head_start", s, head_start_kernel<<<blocks, 1024, 0, s>>>(
                            tk, st, static_cast<const u32x4_t*>(c.x), vpr,
-                           reinterpret_cast<u32x4_t*>(xc), dx0));
+                           reinterpret_cast<u32x4_t*>(xc), p.terms, dx0));
         } else {
             MOE_LAUNCH("head_compact", s, head_compact_kernel<<<1, 1024, 0, s>>>(tk, st));
         }
@@ -1545,15 +1665,15 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
                 tk.limit = 2, tk.tidx = nullptr;
             }
             MOE_LAUNCH("head_gather", s,
-                       head_gather_kernel<<<cdiv((long)(dx0 ? c.T : bound) * vpr, 256), 256, 0, s>>>(
+                       head_gather_kernel<<<head_blocks((long)(dx0 ? c.T : bound) * vpr), 256, 0, s>>>(
                            static_cast<const u32x4_t*>(c.x), rows, count, p0, p.piece, vpr,
                            reinterpret_cast<u32x4_t*>(xc), tk, dx0));
         }
         for (int q0 = 0; q0 < bound; q0 += p.sub) {
             const int s0 = p0 + q0, sn = std::min(p.sub, bound - q0);
-            g.A = p.direct ? static_cast<const T*>(c.x) : xc + (long)q0 * c.d;
-            g.lda = c.d, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
-            g.M = sn, g.N = c.V, g.K = c.d, g.dyn = 1, g.p0 = s0, g.piece = sn;
+            g.A = p.direct ? static_cast<const T*>(c.x) : xc + (long)q0 * ldx;
+            g.lda = p.direct ? c.d : ldx, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
+            g.M = sn, g.N = c.V, g.K = c.d, g.dyn = 1, g.terms = 1, g.p0 = s0, g.piece = sn;
             g.plan = nullptr, g.part = nullptr;
             // statistics by row for head_dz, by part for head_lse; the label's score
             // comes from z where that is kept
@@ -1568,31 +1688,37 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
                 continue;
             }
             const int segs = c.grad ? p.segs : 1;
-            const HeadDz dz = {Z, code, zl, p.ldz, G + (long)q0 * p.ldz, segs, p.seg, c.V, rows, count, s0, sn,
+            const HeadDz dz = {Z, code, zl, p.ldz, G + (long)q0 * ldg, ldg,
+                               top + q0, segs, p.seg, c.V, rows, count, s0, sn,
                                stat, tstat, p.parts, c.loss, c.lse, c.labels, c.weight, c.tidx,
                                c.tlogit, c.tweight, c.K, c.tau, inv_tau, l2t, c.kd, c.grad};
             const int blocks = cdiv((long)sn * segs, 4);
-            if constexpr (sizeof(T) == 2) {
-                if (p.coded) {
-                    MOE_LAUNCH("head_dz", s, head_dz_kernel<T, true><<<blocks, 256, 0, s>>>(dz));
-                    continue;
-                }
-            }
-            MOE_LAUNCH("head_dz", s, head_dz_kernel<T, false><<<blocks, 256, 0, s>>>(dz));
+            auto launch = [&](auto CODED, auto TERMS) {
+                MOE_LAUNCH("head_dz", s,
+                           head_dz_kernel<T, decltype(CODED)::value, decltype(TERMS)::value>
+                           <<<blocks, 256, 0, s>>>(dz));
+            };
+            typedef std::true_type Yes;
+            typedef std::false_type No;
+            if constexpr (sizeof(T) == 4) launch(No{}, No{});
+            else if (p.coded && p.terms == 2) launch(Yes{}, Yes{});
+            else if (p.coded) launch(Yes{}, No{});
+            else if (p.terms == 2) launch(No{}, Yes{});
+            else launch(No{}, No{});
         }
         if (!c.grad) continue;
         HeadGemm<T> gx = g, gw = g;
         gx.p0 = gw.p0 = p0, gx.piece = gw.piece = p.piece;
-        gx.A = gw.A = G, gx.lda = gw.lda = p.ldz;
+        gx.A = gw.A = G, gx.lda = ldg, gw.lda = p.ldz;
         gx.B = static_cast<const T*>(c.Wv), gx.ldb = c.d;
         gx.M = bound, gx.N = c.d, gx.K = c.V, gx.dyn = 1;
         gx.plan = p.slots_dx ? plan + 2 * i : nullptr;
         gx.part = reinterpret_cast<float*>(ws + p.part_dx);
         gw.B = xc, gw.ldb = c.d;
-        gw.M = c.V, gw.N = c.d, gw.K = bound, gw.dyn = 2;
+        gw.M = c.V, gw.N = c.d, gw.K = bound * p.terms, gw.dyn = 2, gw.terms = p.terms;
         gw.plan = p.slots_dw ? plan + 2 * i + 1 : nullptr;
         gw.part = reinterpret_cast<float*>(ws + p.part_dw);
-        const EpiRows<T> ex = {static_cast<T*>(c.dx), c.d, rows, p0};
+        const EpiRows<T> ex = {static_cast<T*>(c.dx), c.d, rows, p0, top, static_cast<const T*>(c.Wv)};
         float* acc = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
         const EpiSum<T> ew = {static_cast<T*>(c.dWv), acc, c.d, count, p0, p.piece};
         const int nx = c.dx ? head_grid<BM>(gx, bound) : 0;
@@ -1636,7 +1762,7 @@ moe_status head_call(const HeadCall& c, moe_dtype dt, void* ws, size_t ws_bytes,
     if (c.T == 0) {
         if (!c.grad || !c.dWv) return MOE_OK;
         const long n = (long)(nw / 16);
-        MOE_LAUNCH("head_zero", s, head_zero_kernel<<<cdiv(n, 256), 256, 0, s>>>(
+        MOE_LAUNCH("head_zero", s, head_zero_kernel<<<head_blocks(n), 256, 0, s>>>(
                        static_cast<u32x4_t*>(c.dWv), n));
         return launch_status();
     }

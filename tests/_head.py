@@ -16,7 +16,10 @@ matrix instructions whose inner order and rounding are not specified):
          by the factor 2^(2^-11)), plus 2^-64 of the largest p where a score lies
          64 or more below its 128 columns' largest and counts as 64
   dz     w p e(p) + u |dz|  (the rounding to the storage type)
-  dx     |e(dz)| |Wv| + g(V) |dz| |Wv| + u |dx|,  dWv likewise
+  dx     |e(dz)| |Wv| + g(V) |dz| |Wv| + u |dx|,  dWv likewise; but in bf16
+         without a teacher the label's entry of dz loses nothing in dx (what its rounding
+         takes is added again in fp32: 2^-23 |dz| instead of u |dz|), and with up to 128
+         tokens every entry is two terms in dWv (u^2 |dz|)
 """
 import math
 
@@ -99,11 +102,16 @@ def reference(x, Wv, labels=None, weight=None, teacher=None, tau=1.0, dt="bf16")
         dz.scatter_add_(1, at, -c * q)
         edz += p.abs() * (ez / tau + el[:, None] + 2.0 ** -20)
         edz.scatter_add_(1, at, c.abs() * q * (K * E32 + 2.0 ** -20))
-    edz = edz * (1 + u) + u * dz.abs() + 2.0 ** -126
+    base = edz
+    edz = base * (1 + u) + u * dz.abs() + 2.0 ** -126
+    edw = base * (1 + u) + u * u * dz.abs() + 2.0 ** -126 if dt == "bf16" and T <= 128 else edz
+    if dt == "bf16" and teacher is None:
+        edz = edz.clone()
+        edz[row, lab.clamp(0, V - 1)] -= (u - E32) * dz[row, lab.clamp(0, V - 1)].abs()
     dx = dz @ W
     dW = dz.t() @ X
     out["dx"] = (dx, edz @ W.abs() + V * E32 * (dz.abs() @ W.abs()) + u * dx.abs() + 2.0 ** -126)
-    out["dWv"] = (dW, edz.t() @ X.abs() + T * E32 * (dz.abs().t() @ X.abs()) + u * dW.abs()
+    out["dWv"] = (dW, edw.t() @ X.abs() + T * E32 * (dz.abs().t() @ X.abs()) + u * dW.abs()
                   + 2.0 ** -126)
     return out
 
