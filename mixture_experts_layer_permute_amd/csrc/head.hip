@@ -977,6 +977,7 @@ struct HeadOperandF32 : HeadOperand<LAY, LAY == KMAJ ? 64 : 32, 4, LAY == KMAJ ?
 };
 
 constexpr int kRingBytesF32 = 65536;
+constexpr int kSumStages = 2;
 template <int ALAY, int BLAY, class Epi>
 __device__ __forceinline__ void head_product_body(const HeadGemm<float>& p, const Epi& epi,
                                                   int block, uint8_t* ringbuf) {
@@ -1019,32 +1020,46 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<float>& p, cons
         unroll<NL>([&](auto I) { opB.template load<decltype(I)::value>(rb, at + UNIT); });
     };
     if (nj > 0) issue(0);
+    // the sums of kSumStages stages are made by themselves and then added: a chain of
+    // hundreds of additions, each rounded at the size of the whole, would lose more than
+    // the rounding of z that the loss shows
 #pragma unroll 1
-    for (int j = 0; j < nj; ++j) {
-        stage_barrier<0>();            // stage j landed, stage j - 1 read by every wave
-        if (j + 1 < nj) issue(j + 1);
-        const uint32_t u = ring0 + (uint32_t)((j & 1) * STAGE);
-        f32x4 fa[2][2], fc[2][2];
-        auto read = [&](int b) {
+    for (int j0 = 0; j0 < nj; j0 += kSumStages) {
+        f32x16 sum[2][2] = {};
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                fa[b & 1][i] = opA.read4(u, i, b), fc[b & 1][i] = opB.read4(u + UNIT, i, b);
-        };
-        read(0);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (b < 3) read(b + 1);
-            __builtin_amdgcn_sched_barrier(0);         // (those reads before these products)
-            const f32x4(&a)[2] = fa[b & 1], (&c)[2] = fc[b & 1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
+        for (int k = 0; k < kSumStages; ++k) {
+            const int j = j0 + k;
+            if (k > 0 && j >= nj) break;
+            stage_barrier<0>();        // stage j landed, stage j - 1 read by every wave
+            if (j + 1 < nj) issue(j + 1);
+            uint32_t u = ring0 + (uint32_t)((j & 1) * STAGE);
+            asm volatile("" : "+s"(u));    // (addresses of both stages would not fit the registers)
+            f32x4 fa[2][2], fc[2][2];
+            auto read = [&](int b) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
+                    fa[b & 1][i] = opA.read4(u, i, b), fc[b & 1][i] = opB.read4(u + UNIT, i, b);
+            };
+            read(0);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)        // (columns as rows)
-                        acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x2f32(c[k][e], a[i][e], acc[i][k],
-                                                                        0, 0, 0);
+            for (int b = 0; b < 4; ++b) {
+                if (b < 3) read(b + 1);
+                __builtin_amdgcn_sched_barrier(0);     // (those reads before these products)
+                const f32x4(&a)[2] = fa[b & 1], (&c)[2] = fc[b & 1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)    // (columns as rows)
+                            sum[i][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                c[n][e], a[i][e], sum[i][n], 0, 0, 0);
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) acc[i][n] += sum[i][n];
     }
     // 32 x 32 fragments: row = lane % 32, four columns by register and lane / 32
     unroll<2>([&](auto I) {

@@ -308,3 +308,98 @@ def test_a_training_step():
     assert abs(float(norm) - math.sqrt(sq)) <= 1e-6 * math.sqrt(sq)
     # scaled by half: exact up to the factor's rounding, then one of bf16
     assert torch.allclose(head.dWv.double(), before[0].double() * 0.5, rtol=2.0 ** -8, atol=1e-30)
+
+
+@pytest.mark.parametrize("K", [0, 7])
+@pytest.mark.parametrize("T,n", [(128, 128), (129, 129), (200, 100), (200, 128), (1000, 1), (128, 65)])
+def test_few_tokens_in_a_larger_workspace(T, n, K):
+    """dz in two terms (up to 128 tokens) and in one, in the workspace of more."""
+    d, V = 192, 2003
+    banner("head few tokens", T, n, K)
+    head = M.HeadLoss(T, d, V, torch.bfloat16, K=K, tau=2.0, device="cuda")
+    x, Wv, labels, weight, teacher = inputs(n, d, V, masked=0.2, K=K, seed=T + n)
+    head.bind(Wv)
+    head.step(x, labels, weight, teacher)
+    got = {k: getattr(head, k) for k in ("loss", "lse", "dx", "dWv") + (("kd",) if K else ())}
+    check(got, reference(x, Wv, labels, weight, teacher, 2.0), "%d of %d" % (n, T))
+
+
+@pytest.mark.parametrize("T", [1, 19, 300])
+def test_rounding_of_the_gradients(T):
+    """dx is as near to 64 bits as its own rounding: half a step, and of the entries
+    beside the label's, sqrt(V) e(dz) at most, a tenth of that here (the label takes
+    more than nine tenths of the squares of its row).  dWv likewise up to 128 tokens."""
+    d, V = 256, 5000
+    banner("head rounding", T)
+    x, Wv, labels, weight, _ = inputs(T, d, V, seed=T)
+    ref = reference(x, Wv, labels, weight)
+    got = run(x, Wv, labels, weight)
+    for name in ("dx", "dWv") if T <= 128 else ("dx",):
+        val = ref[name][0]
+        own = (val.to(torch.bfloat16).double() - val).norm()
+        err = (got[name].double() - val).norm()
+        assert err <= 1.1 * own, (name, float(err / own))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [0, 3])
+def test_no_tokens(K, dt):
+    """T = 0: dWv is zeros, and nothing else happens."""
+    d, V = 128, 77
+    banner("head no tokens", K, dt)
+    x, Wv, labels, weight, teacher = inputs(0, d, V, dt, K=K)
+    res = run(x, Wv, labels, weight, teacher, 2.0, out={"dWv": torch.full_like(Wv, 3.0)})
+    assert not bool(res["dWv"].any()) and res["dx"].shape == (0, d)
+    res = run(x, Wv, labels, None, teacher, 2.0, grad=False)
+    assert res["loss"].shape == (0,)
+
+
+@pytest.mark.parametrize("tau", [0.05, 50.0])
+def test_sharp_and_flat_temperatures(tau):
+    T, d, V, K = 70, 64, 999, 9
+    banner("head tau", tau)
+    x, Wv, labels, weight, teacher = inputs(T, d, V, "f32", K=K, seed=3)
+    ref = reference(x, Wv, labels, weight, teacher, tau, "f32")
+    check(run(x, Wv, labels, weight, teacher, tau), ref, "tau %g" % tau)
+
+
+def test_two_losses_at_once_on_two_streams():
+    """Two calls in flight, each with a workspace of its own."""
+    T, d, V = 600, 256, 4001
+    banner("head two streams")
+    heads, wants, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        x, Wv, labels, weight, _ = inputs(T, d, V, masked=0.1, seed=i)
+        wants.append({k: v.clone() for k, v in run(x, Wv, labels, weight).items()})
+        h = M.HeadLoss(T, d, V, torch.bfloat16, device="cuda")
+        h.bind(Wv)
+        heads.append((h, x, labels, weight))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for (h, x, labels, weight), s in zip(heads, streams):
+            with torch.cuda.stream(s):
+                h.step(x, labels, weight)
+    torch.cuda.synchronize()
+    for (h, *_), want in zip(heads, wants):
+        for k in ("loss", "lse", "dx", "dWv"):
+            assert torch.equal(getattr(h, k), want[k]), k
+
+
+def test_gradient_past_32_bit_offsets():
+    """dz of one piece is more than 4 GB: the last rows' and entries' offsets pass 32
+    bits.  The tokens repeat (weights included), so that every copy of a token has the
+    first one's dx bit for bit, and dWv of a vocabulary entry at the end is checked
+    against the formula."""
+    T, d, V, base = 20480, 64, 131008, 256
+    banner("head offsets", T, d, V)
+    x, Wv, labels, weight, _ = inputs(base, d, V, seed=1)
+    labels[-1] = V - 1
+    got = run(x.repeat(T // base, 1), Wv, labels.repeat(T // base), weight.repeat(T // base))
+    one = got["dx"][:base]
+    assert torch.equal(got["dx"].view(T // base, base, d), one.expand(T // base, base, d))
+    assert torch.equal(got["loss"].view(-1, base), got["loss"][:base].expand(T // base, base))
+    ref = reference(x, Wv, labels, weight)
+    check({k: got[k][:base] for k in ("loss", "lse", "dx")}, ref, "first copy")
+    val, tol = (t[-64:] * (T // base) for t in ref["dWv"])
+    assert bool(((got["dWv"][-64:].double() - val).abs() <= 1.05 * tol + T * 2.0 ** -23 * val.abs()
+                 .max()).all())
