@@ -431,8 +431,8 @@ moe_status moe_clip_grads(const void *const *grads, void *const *out,
  *   dz[t,v] = weight[t] * (exp(z[t,v] - lse[t]) - [v == labels[t]])
  *   dx = dz Wv, dWv = dz^T x
  * The scores are never kept whole: the loss alone keeps a maximum and a sum per
- * 128 of them, the gradient the scores of as many tokens at a time as the
- * workspace holds.  A token whose label lies outside [0,V) (padding, a prompt)
+ * 128 (fp32: 64) of them, the gradient dz for a piece of tokens, as many as the
+ * workspace holds, and the scores of a part of it.  A token whose label lies outside [0,V) (padding, a prompt)
  * has no loss: loss, lse and its row of dx are 0, it adds nothing to dWv, and
  * its row of x is not read.
  *   x [T,d] dt, Wv [V,d] dt (row v scores entry v, the layout of an embedding
@@ -440,8 +440,14 @@ moe_status moe_clip_grads(const void *const *grads, void *const *out,
  *   ones; the mean over n tokens is 1/n each), loss [T] float, lse [T] float or
  *   NULL, dx [T,d] dt and dWv [V,d] dt (either may be NULL: not wanted; both
  *   overwritten; they overlap neither each other nor x nor Wv).
- * Sums are fp32; for bf16 dz is rounded to bf16 for its two products, and dx
- * and dWv are rounded once.
+ * Sums, statistics, loss and lse are fp32, and dx and dWv are rounded once.  For
+ * bf16 dz is rounded to bf16 for its two products, after its scores were kept in 16
+ * bits below the largest of their 128 (exp z within 3.4e-4; with a teacher in fp32).
+ * What that takes from the label's entry, which is most of a row (with a teacher:
+ * from the named entry that loses most), is added to dx in fp32; up to 128 tokens
+ * dWv is made from dz in two bf16 terms.  Past that a step's rounding of dz stays in
+ * dWv, about as large as dWv's own.  Every order is fixed: the same call gives the
+ * same bits.
  *   ws: 16-byte aligned, no initial content needed; calls that may overlap in
  *   time need one each.  moe_head_workspace_bytes gives the size for the
  *   largest pieces of tokens that stay within `limit` bytes (0: 8 GiB), or the

@@ -260,6 +260,9 @@ __global__ __launch_bounds__(1024) void head_start_kernel(HeadTokens tk, HeadSta
         if (!tk.has_loss(i / vpr)) dx[i] = u32x4_t{0, 0, 0, 0};
 }
 
+// Both copies are bound by launch and bandwidth: 8192 rows of 1024 bf16, list 10 us
+// (one block), copy 9 us (3.6 TB/s); 777 rows in one launch 5 us.
+
 // The active rows of one piece (of `piece` rows from compacted row p0 on).
 __device__ __forceinline__ int piece_rows(const int32_t* count, int p0, int piece, int fixed) {
     const int n = count ? *count : fixed;
@@ -930,6 +933,9 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
     });
 }
 
+// The scores: 8192 x 50257 from d 1024 900 us with 16-bit scores stored (935
+// TFLOP/s; 16 stages and a 10 us epilogue a tile, pipes busy 42%), 620 for the loss
+// alone; 16 tokens, d 4096, 128000 entries 236 us (Wv at 4.5 TB/s).
 template <int ALAY, int BLAY, class Epi>
 __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p, Epi epi) {
     __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[kRingBytes];
@@ -1082,6 +1088,9 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
     head_product_body<ALAY, BLAY>(p, epi, blockIdx.x, ringbuf);
 }
 
+// Bound by the matrix pipes and the power they draw: 68% of their cycles busy at
+// 1.9 GHz; 8192 tokens, d 1024, 50257 entries 1200 us (1405 TFLOP/s), 16384, 4096,
+// 128000 23.7 ms (1450); fp32 1999, 1088, 8191 650 us (104).
 // Both gradients' products in one launch: blocks 0 .. nx - 1 make dx = dz Wv, the
 // others dWv = dz^T x, so that the second fills the rounds that the first leaves.
 __global__ __launch_bounds__(256, 1) void head_grads_kernel(HeadGemm<bf16_t> gx,
@@ -1164,6 +1173,7 @@ __device__ __forceinline__ float part_factor(float m, float mx, float l2) {
     return m == -INFINITY ? 1.0f : exp2_hw(m * l2 - mx * l2);
 }
 
+// 8192 rows of 393 parts: 7 us (26 MB, 3.7 TB/s); 16 rows of 1000: 6.6, latency.
 // A loss without gradient: lse of every row from its parts, 16 rows a block, 64
 // threads share a row's parts; loss and lse go to the row's token.
 __global__ __launch_bounds__(1024) void head_lse_kernel(
@@ -1263,6 +1273,8 @@ struct HeadDz {
     int grad;
 };
 
+// Bound by HBM: 8192 x 50257 in bf16 from coded scores 290 us (1.65 GB, 5.7 TB/s), with
+// a teacher from fp32 ones 520 us (2.5 GB, 4.8 TB/s; two exponentials an entry).
 // One wave a row, or a segment of one when the rows are few.  The dz of the label
 // and the teacher's slots are written behind the others (an entry named twice by
 // its first slot, with the slots' q added in order).
