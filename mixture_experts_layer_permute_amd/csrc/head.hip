@@ -1029,44 +1029,56 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<float>& p, cons
     // the sums of kSumStages stages are made by themselves and then added: a chain of
     // hundreds of additions, each rounded at the size of the whole, would lose more than
     // the rounding of z that the loss shows
+    // NI: the wave's row fragments that have rows; up to 32 tokens half of the waves
+    // then have none and the others one of two (1 token, d 1600, 101207 entries: 970 us
+    // to 640; 24, 512, 5000: 90 to 69; full tiles the same)
+    auto products = [&](auto NI) {
+        constexpr int ni = decltype(NI)::value;
 #pragma unroll 1
-    for (int j0 = 0; j0 < nj; j0 += kSumStages) {
-        f32x16 sum[2][2] = {};
+        for (int j0 = 0; j0 < nj; j0 += kSumStages) {
+            f32x16 sum[2][2] = {};
 #pragma unroll
-        for (int k = 0; k < kSumStages; ++k) {
-            const int j = j0 + k;
-            if (k > 0 && j >= nj) break;
-            stage_barrier<0>();        // stage j landed, stage j - 1 read by every wave
-            if (j + 1 < nj) issue(j + 1);
-            uint32_t u = ring0 + (uint32_t)((j & 1) * STAGE);
-            asm volatile("" : "+s"(u));    // (addresses of both stages would not fit the registers)
-            f32x4 fa[2][2], fc[2][2];
-            auto read = [&](int b) {
+            for (int k = 0; k < kSumStages; ++k) {
+                const int j = j0 + k;
+                if (k > 0 && j >= nj) break;
+                stage_barrier<0>();        // stage j landed, stage j - 1 read by every wave
+                if (j + 1 < nj) issue(j + 1);
+                uint32_t u = ring0 + (uint32_t)((j & 1) * STAGE);
+                asm volatile("" : "+s"(u));    // (addresses of both stages would not fit the registers)
+                f32x4 fa[2][2], fc[2][2];
+                auto read = [&](int b) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    fa[b & 1][i] = opA.read4(u, i, b), fc[b & 1][i] = opB.read4(u + UNIT, i, b);
-            };
-            read(0);
+                    for (int i = 0; i < 2; ++i) {
+                        if (i < ni) fa[b & 1][i] = opA.read4(u, i, b);
+                        if (ni > 0) fc[b & 1][i] = opB.read4(u + UNIT, i, b);
+                    }
+                };
+                read(0);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b < 3) read(b + 1);
-                __builtin_amdgcn_sched_barrier(0);     // (those reads before these products)
-                const f32x4(&a)[2] = fa[b & 1], (&c)[2] = fc[b & 1];
+                for (int b = 0; b < 4; ++b) {
+                    if (b < 3) read(b + 1);
+                    __builtin_amdgcn_sched_barrier(0);     // (those reads before these products)
+                    const f32x4(&a)[2] = fa[b & 1], (&c)[2] = fc[b & 1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                        for (int i = 0; i < ni; ++i)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)    // (columns as rows)
-                            sum[i][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-                                c[n][e], a[i][e], sum[i][n], 0, 0, 0);
+                            for (int n = 0; n < 2; ++n)    // (columns as rows)
+                                sum[i][n] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                    c[n][e], a[i][e], sum[i][n], 0, 0, 0);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < ni; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) acc[i][n] += sum[i][n];
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) acc[i][n] += sum[i][n];
-    }
+    };
+    const int some = (ti.rows - wm * 64 + 31) / 32;
+    if (some >= 2) products(std::integral_constant<int, 2>{});
+    else if (some == 1) products(std::integral_constant<int, 1>{});
+    else products(std::integral_constant<int, 0>{});
     // 32 x 32 fragments: row = lane % 32, four columns by register and lane / 32
     unroll<2>([&](auto I) {
         f32x4 v[8];
