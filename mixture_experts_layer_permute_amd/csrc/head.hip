@@ -129,6 +129,7 @@ constexpr int kXcdRun = 32;             // neighbouring tiles on one XCD
 constexpr int kRound = 256;             // compute units
 constexpr int kMaxParts = 32;           // of a tile
 constexpr int kMaxSlots = 768;          // rest tiles times parts
+constexpr long kScoreSlots = 128;       // the scores' tiles times parts, where they are split
 
 // Parts of each of R rest tiles whose reduction has nj stages of 64 steps: the
 // fewest stage times over the rounds they take, with `ends` of them for a tile's
@@ -315,7 +316,8 @@ struct HeadGemm {
     int terms;               // reduction rows of a piece's row (dyn 2)
     const int32_t* count;
     int p0, piece;
-    const int32_t* plan;     // parts of a rest tile (NULL: 1)
+    const int32_t* plan;     // parts of a rest tile (NULL: split)
+    int split;               // of every tile of a product with fewer than 256, known to the host
     float* part;             // [slot][BM][BN]
 };
 
@@ -344,7 +346,7 @@ __device__ __forceinline__ HeadTile head_tile(const HeadGemm<T>& p, int block) {
     const int n = p.dyn ? piece_rows(p.count, p.p0, p.piece, p.piece) : 0;
     const int M = p.dyn == 1 ? n : p.M, K = p.dyn == 2 ? n * p.terms : p.K;
     const int nM = (M + BM - 1) / BM, nN = (p.N + BN - 1) / BN, tiles = nM * nN;
-    const int S = p.plan ? *p.plan : 1;
+    const int S = p.plan ? *p.plan : p.split;
     const int full = S > 1 ? tiles / kRound * kRound : tiles;
     int L = xcd_logical(block, kXcdRun);
     t.slot = -1;
@@ -537,6 +539,15 @@ struct EpiScores {
         }
         if (in && Lanes::first()) stat[at] = make_float2(m, sum);
     }
+};
+
+// Scores whose product was split: only parts are stored.
+struct EpiParts {
+    static constexpr bool kSplits = true;
+    typedef int Ask;
+    __device__ __forceinline__ int ask(const HeadTile&, int) const { return 0; }
+    template <class Lanes>
+    __device__ __forceinline__ void row(const HeadTile&, int, int, const f32x4 (&)[8], int) const {}
 };
 
 template <typename T>
@@ -1162,6 +1173,69 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadGemm<T> gx, EpiRows
     else head_join_body<BM, BM>(gw, ew, b - nx);
 }
 
+// The scores of a product that was split: their parts added in order, then what
+// EpiScores does.  8 columns a thread, the W columns of a statistic in W / 8 lanes.
+template <int BM, int W, typename T>
+__global__ __launch_bounds__(1024) void head_scores_join_kernel(HeadGemm<T> p, EpiScores es) {
+    constexpr int PER = BM * BM / 8192;               // blocks of a tile
+    const int n = piece_rows(p.count, p.p0, p.piece, p.piece);
+    const int nM = (n + BM - 1) / BM, nN = (p.N + BM - 1) / BM, R = nM * nN;
+    const int tile = blockIdx.x / PER;
+    if (tile >= R) return;
+    int m0, n0;
+    head_origin<BM, BM>(tile, nM, nN, m0, n0);
+    const int e = ((blockIdx.x % PER) * 1024 + threadIdx.x) * 8;
+    const long r = m0 + e / BM;
+    const int c = n0 + e % BM, left = es.V - c;
+    const bool in = r < n;                            // (all lanes stay, for the exchanges)
+    float v[8] = {};
+    const float* q = p.part + (long)tile * (BM * BM) + e;
+    for (int k = 0; k < p.split; ++k) {
+        const float* a = q + (long)k * R * (BM * BM);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (in && left > 4 * h) {                 // quads that were stored
+                const f32x4 b = *reinterpret_cast<const f32x4*>(a + 4 * h);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) v[4 * h + u] += b[u];
+            }
+    }
+    const int y = in && es.labels ? es.labels[r] - c : -1;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        if (u == y && u < left) es.zl[r] = v[u];
+    if (es.Z && in && c < es.ldz) st8(es.Z + r * es.ldz + c, v);
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        v[u] = u < left ? v[u] : -INFINITY;
+        m = fmaxf(m, v[u]);
+    }
+#pragma unroll
+    for (int k = 1; k < W / 8; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
+    const float ref = m == -INFINITY ? 0.0f : m, m2 = ref * kLog2e, mt = ref * es.l2t;
+    float x[8], s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        x[u] = fmaf(v[u], kLog2e, -m2);
+        s += exp2_hw(x[u]);
+        if (es.tstat) t += exp2_hw(fmaf(v[u], es.l2t, -mt));
+    }
+    if (W == 128 && es.code && in && c < es.ldz)
+        *reinterpret_cast<u32x4_t*>(es.code + r * es.ldz + c) =
+            u32x4_t{code_pair(x[0], x[1]), code_pair(x[2], x[3]), code_pair(x[4], x[5]),
+                    code_pair(x[6], x[7])};
+#pragma unroll
+    for (int k = 1; k < W / 8; k *= 2) {
+        s += __shfl_xor(s, k);
+        if (es.tstat) t += __shfl_xor(t, k);
+    }
+    if (!in || (threadIdx.x & (W / 8 - 1))) return;
+    const long at = (long)(c / W) * es.sp + r * es.sr;
+    es.stat[at] = make_float2(m, s);
+    if (es.tstat) es.tstat[at] = t;
+}
+
 // --------------------------------------------------------- normalisers
 
 // The normaliser of a row in units of log2: 2^(a + b) = sum_v e^z, a = the maximum
@@ -1529,6 +1603,28 @@ inline long head_slots(long tiles, long K, bool f32) {
     return parts > 1 ? std::min((long)kMaxSlots, std::min(tiles, (long)kRound - 1) * parts) : 0;
 }
 
+// Parts of the scores' tiles: few tiles with a long reduction would leave most
+// compute units idle.  A stage takes 1.2 us, the parts' way through memory and the
+// second launch about 12 (scores, one part / split: fp32 12 tokens, d 3712, 587
+// entries 145 us / 29; 500, 1536, 2000 120 / 74; bf16 12, 3968, 2151 82 / 28; 1000, 2048,
+// 2000 55 / 43; 16, 1536, 16000 40 / 30).
+inline int head_score_split(long rows, int d, int V, bool f32) {
+    const int bm = f32 ? 128 : 256, stages = cdiv(d, f32 ? 32 : 64);
+    const long tiles = (long)cdiv(rows, bm) * cdiv(V, bm);
+    if (tiles == 0 || tiles > kScoreSlots / 2 || stages < 24) return 1;
+    return (int)std::min(kScoreSlots / tiles, (long)stages / 8);
+}
+// Their slots, for any number of rows up to `rows`.
+inline long head_score_slots(long rows, int d, int V, bool f32) {
+    const int bm = f32 ? 128 : 256;
+    long most = 0;
+    for (long k = 1; k <= std::min((long)cdiv(rows, bm), kScoreSlots / 2); ++k) {
+        const int s = head_score_split(k * bm, d, V, f32);
+        if (s > 1) most = std::max(most, k * cdiv(V, bm) * s);
+    }
+    return most;
+}
+
 HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int piece) {
     HeadPlan p;
     const size_t b = dt == MOE_BF16 ? 2 : 4;
@@ -1585,7 +1681,9 @@ HeadPlan head_layout(int T, int d, int V, int K, moe_dtype dt, int grad, int pie
     const long sx = head_slots(cdiv(piece, bm) * cols, V, dt == MOE_F32);
     const long sw = head_slots(cdiv(V, bm) * cols, gmax, dt == MOE_F32);
     p.slots_dx = sx > 0, p.slots_dw = sw > 0;
-    p.part_dx = take(grad ? (size_t)sx * bm * bm * 4 : 0);
+    // (the scores' parts are done with before the gradients' come)
+    const long ss = head_score_slots(rmax, d, V, dt == MOE_F32);
+    p.part_dx = take((size_t)std::max(grad ? sx : 0l, ss) * bm * bm * 4);
     p.part_dw = take(grad ? (size_t)sw * bm * bm * 4 : 0);
     p.acc = take(grad && p.pieces > 1 ? (size_t)V * d * 4 : 0);
     p.total = o;
@@ -1632,7 +1730,8 @@ struct HeadCall {
 template <int BM, typename T>
 int head_grid(const HeadGemm<T>& g, long m) {
     const long tiles = (long)cdiv(m, BM) * cdiv(g.N, BM);
-    const long blocks = g.plan ? std::max(tiles, tiles / kRound * kRound + kMaxSlots) : tiles;
+    const long blocks = g.plan ? std::max(tiles, tiles / kRound * kRound + kMaxSlots)
+                               : tiles * g.split;
     const long pad = NXCD * kXcdRun;
     return (int)((blocks + pad - 1) / pad * pad);
 }
@@ -1643,12 +1742,14 @@ int head_join_grid(const HeadGemm<T>& g, long m) {
     return g.plan ? (int)(rest * (BM * BM / 8192)) : 0;
 }
 
-void head_scores(const HeadGemm<bf16_t>& g, long m, const EpiScores& e, hipStream_t s) {
-    MOE_LAUNCH("head_scores", s, head_product_kernel<KMAJ, KMAJ, EpiScores>
+template <class Epi>
+void head_scores(const HeadGemm<bf16_t>& g, long m, const Epi& e, hipStream_t s) {
+    MOE_LAUNCH("head_scores", s, head_product_kernel<KMAJ, KMAJ, Epi>
                <<<head_grid<256>(g, m), 256, 0, s>>>(g, e));
 }
-void head_scores(const HeadGemm<float>& g, long m, const EpiScores& e, hipStream_t s) {
-    MOE_LAUNCH("head_scores", s, head_product_f32_kernel<KMAJ, KMAJ, EpiScores>
+template <class Epi>
+void head_scores(const HeadGemm<float>& g, long m, const Epi& e, hipStream_t s) {
+    MOE_LAUNCH("head_scores", s, head_product_f32_kernel<KMAJ, KMAJ, Epi>
                <<<head_grid<FBM>(g, m), 256, 0, s>>>(g, e));
 }
 
@@ -1713,13 +1814,22 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
             g.A = p.direct ? static_cast<const T*>(c.x) : xc + (long)q0 * ldx;
             g.lda = p.direct ? c.d : ldx, g.B = static_cast<const T*>(c.Wv), g.ldb = c.d;
             g.M = sn, g.N = c.V, g.K = c.d, g.dyn = 1, g.terms = 1, g.p0 = s0, g.piece = sn;
-            g.plan = nullptr, g.part = nullptr;
+            g.plan = nullptr, g.part = reinterpret_cast<float*>(ws + p.part_dx);
+            g.split = head_score_split(sn, c.d, c.V, sizeof(T) == 4);
             // statistics by row for head_dz, by part for head_lse; the label's score
             // comes from z where that is kept
             const EpiScores es = {c.V, stat, tstat, store ? 1 : (long)p.sub, store ? p.parts : 1, l2t,
                                   teacher ? nullptr : p.direct ? c.labels : clab + s0, zl, Z, code,
                                   p.ldz};
-            head_scores(g, sn, es, s);
+            if (g.split == 1) {
+                head_scores(g, sn, es, s);
+            } else {
+                head_scores(g, sn, EpiParts{}, s);
+                const int blocks = cdiv(sn, BM) * cdiv(c.V, BM) * (BM * BM / 8192);
+                MOE_LAUNCH("head_scores_join", s,
+                           head_scores_join_kernel<BM, (sizeof(T) == 2 ? 128 : 64), T>
+                           <<<blocks, 1024, 0, s>>>(g, es));
+            }
             if (!store) {
                 MOE_LAUNCH("head_lse", s, head_lse_kernel<<<cdiv(sn, 16), 1024, 0, s>>>(
                                stat, p.parts, p.sub, zl, c.labels, c.V, p.direct ? nullptr : rows,
@@ -1747,6 +1857,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
         }
         if (!c.grad) continue;
         HeadGemm<T> gx = g, gw = g;
+        gx.split = gw.split = 1;
         gx.p0 = gw.p0 = p0, gx.piece = gw.piece = p.piece;
         gx.A = gw.A = G, gx.lda = ldg, gw.lda = p.ldz;
         gx.B = static_cast<const T*>(c.Wv), gx.ldb = c.d;

@@ -403,3 +403,15 @@ def test_gradient_past_32_bit_offsets():
     val, tol = (t[-64:] * (T // base) for t in ref["dWv"])
     assert bool(((got["dWv"][-64:].double() - val).abs() <= 1.05 * tol + T * 2.0 ** -23 * val.abs()
                  .max()).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V,K", [(12, 3712, 587, 0), (1, 4096, 1, 0), (270, 1600, 1003, 5),
+                                     (130, 1536, 128, 0), (30, 2112, 668, 67), (9, 768, 3000, 2)])
+def test_split_scores(T, d, V, K, dt):
+    """Few tiles with a long reduction: the scores' product in parts."""
+    banner("head split scores", T, d, V, K, dt)
+    x, Wv, labels, weight, teacher = inputs(T, d, V, dt, masked=0.2, K=K, seed=T)
+    ref = reference(x, Wv, labels, weight, teacher, 2.0, dt)
+    check(run(x, Wv, labels, None, teacher, 2.0, grad=False), ref, "forward")
+    check(run(x, Wv, labels, weight, teacher, 2.0), ref, "gradient")
