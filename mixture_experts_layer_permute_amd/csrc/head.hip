@@ -766,13 +766,17 @@ struct HeadOperand {
     // wlds: the unit's LDS address + 1 KB times the wave, in a scalar register
     template <int I>
     __device__ __forceinline__ void load(i32x4_t rs, uint32_t wlds) const {
-        // one wait state between writing m0 and the load that reads it
+        // One wait state between writing m0 and the load that reads it.  A vector
+        // instruction that writes a scalar register (the descriptor may come out of
+        // v_readfirstlane) stands five wait states before a load that reads it, and
+        // the compiler does not count them into inline assembly: the first load of a
+        // unit, the nearest to its descriptor, waits for all five itself.
         asm volatile(
             "s_add_u32 m0, %0, %1\n\t"
-            "s_nop 0\n\t"
+            "s_nop %4\n\t"
             "buffer_load_dwordx4 %2, %3, 0 offen lds"
             :
-            : "s"(wlds), "n"(NW * I * 1024), "v"(off[I]), "s"(rs)
+            : "s"(wlds), "n"(NW * I * 1024), "v"(off[I]), "s"(rs), "n"(I == 0 ? 3 : 0)
             : "memory", "m0", "scc");
     }
     // Fragment I (rows 16 I on of the wave's) of the 32 steps S of the unit at
