@@ -75,8 +75,10 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // the compiler does not tie every later LDS read to its completion; callers
 // wait on vmcnt themselves (stage_barrier) before reading the stage.
 __device__ __forceinline__ void lds_dma16(i32x4_t rs, uint32_t voff, uint32_t lds) {
+    // (one wait state between writing m0 and the load that reads it)
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
         :
         : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)

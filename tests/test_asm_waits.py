@@ -36,6 +36,11 @@ def test_a_descriptor_is_there_when_a_load_reads_it(found, src):
     assert short(found, src, ("sgpr",)) == []
 
 
+@pytest.mark.parametrize("src", SOURCES)
+def test_m0_is_there_when_a_load_into_lds_reads_it(found, src):
+    assert short(found, src, ("m0",)) == []
+
+
 def test_matrix_instructions_keep_their_distance_over_a_loops_end_too(found):
     inline = sum(i.inline and i.mfma for b, _ in found["head.hip"].values()
                  for ins, _ in b for i in ins)
