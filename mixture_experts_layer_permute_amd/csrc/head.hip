@@ -1259,7 +1259,11 @@ __device__ __forceinline__ float norm_p(Norm2 n, float z, float l2) {
 
 // A part's factor relative to the maximum mx: 2^(m' - mx'), m' as in the sums; a
 // part without a column (m = -inf) adds its sum as it is: 0, or the NaN of a score.
+// Both products are rounded by themselves: fused with the difference one of them
+// would not be, and the factor of the part that holds the maximum not 1 but off by
+// the rounding of m L, once for every merge (lse up to 127: 2.3e-5).
 __device__ __forceinline__ float part_factor(float m, float mx, float l2) {
+#pragma clang fp contract(off)
     return m == -INFINITY ? 1.0f : exp2_hw(m * l2 - mx * l2);
 }
 
