@@ -111,16 +111,22 @@ __device__ __forceinline__ void unroll(F&& f) {
 // ------------------------------------------------------- tokens with a loss
 
 __device__ __forceinline__ bool in_vocab(int v, int V) { return (unsigned)v < (unsigned)V; }
+// Whether a teacher's slot counts: its entry is one, its score not -infinity (a NaN
+// counts, and shows in the results).
+__device__ __forceinline__ bool slot_on(const int32_t* tidx, const float* tlogit, long at, int V) {
+    return in_vocab(tidx[at], V) && !(tlogit[at] == -INFINITY);
+}
 
 // act[t]: whether token t has a label or a teacher's slot (one wave a token).
 __global__ __launch_bounds__(256) void head_active_kernel(const int32_t* __restrict__ labels,
                                                           const int32_t* __restrict__ tidx,
+                                                          const float* __restrict__ tlogit,
                                                           int T, int K, int V,
                                                           int32_t* __restrict__ act) {
     const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (t >= T) return;
     bool on = labels && in_vocab(labels[t], V);
-    for (int j = lane; j < K && !on; j += 64) on = in_vocab(tidx[(long)t * K + j], V);
+    for (int j = lane; j < K && !on; j += 64) on = slot_on(tidx, tlogit, (long)t * K + j, V);
     const bool any = __ballot(on) != 0;
     if (lane == 0) act[t] = any ? 1 : -1;
 }
@@ -161,11 +167,12 @@ struct HeadTokens {
     const int32_t* act;      // labels (limit V) or flags (limit 2), or NULL
     int limit;
     const int32_t* tidx;     // or NULL
+    const float* tlogit;
     int K, V, T;
     __device__ __forceinline__ bool has_loss(int t) const {
         bool on = act && in_vocab(act[t], limit);
         if (tidx)
-            for (int j = 0; j < K; ++j) on |= in_vocab(tidx[(long)t * K + j], V);
+            for (int j = 0; j < K && !on; ++j) on = slot_on(tidx, tlogit, (long)t * K + j, V);
         return on;
     }
 };
@@ -1460,23 +1467,22 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
     float wkd = 0.0f;
     if (p.tidx) {
         float hi = -INFINITY;
+        bool some = false;
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
             const int j = lane + 64 * u;
             idx[u] = -1;
             q[u] = -INFINITY;
-            if (j < p.K) {
-                const int v = p.tidx[(long)t * p.K + j];
-                if (in_vocab(v, p.V)) {
-                    idx[u] = v;
-                    q[u] = p.tlogit[(long)t * p.K + j] * p.inv_tau;
-                    hi = fmaxf(hi, q[u]);
-                }
+            if (j < p.K && slot_on(p.tidx, p.tlogit, (long)t * p.K + j, p.V)) {
+                some = true;
+                idx[u] = p.tidx[(long)t * p.K + j];
+                q[u] = p.tlogit[(long)t * p.K + j] * p.inv_tau;
+                hi = fmaxf(hi, q[u]);
             }
         }
         hi = wave_max(hi);
-        const bool any = hi > -INFINITY;
-        const float ref = any ? hi : 0.0f;
+        const bool any = __ballot(some) != 0;
+        const float ref = hi > -INFINITY ? hi : 0.0f;      // (NaNs alone: they show)
         float tot = 0.0f;
         float lq[PL];
 #pragma unroll
@@ -1783,7 +1789,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
     HeadGemm<T> g;
     g.count = p.direct ? nullptr : count;
     if (!p.direct) {
-        HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.K, c.V, c.T};
+        HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.tlogit, c.K, c.V, c.T};
         const HeadParts hp = {plan, plan ? p.pieces : 0, p.piece, c.d, c.V, BM, p.terms};
         const HeadStart st = {rows, clab, count, {c.loss, c.lse, c.kd}, hp};
         u32x4_t* dx0 = c.grad ? static_cast<u32x4_t*>(c.dx) : nullptr;
@@ -1791,7 +1797,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
         if (teacher && (long)c.T * c.K > 16384) {
             int32_t* a = reinterpret_cast<int32_t*>(ws + p.act);
             MOE_LAUNCH("head_active", s, head_active_kernel<<<cdiv(c.T, 4), 256, 0, s>>>(
-                           c.labels, c.tidx, c.T, c.K, c.V, a));
+                           c.labels, c.tidx, c.tlogit, c.T, c.K, c.V, a));
             tk.act = a, tk.limit = 2, tk.tidx = nullptr;
         }
         if (c.T <= kStartTokens && p.pieces == 1) {
@@ -1807,7 +1813,7 @@ moe_status head_run(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t 
         const int p0 = i * p.piece, bound = std::min(p.piece, c.T - p0);
         if (!p.direct && (c.T > kStartTokens || p.pieces > 1)) {
             u32x4_t* dx0 = c.grad && i == 0 ? static_cast<u32x4_t*>(c.dx) : nullptr;
-            HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.K, c.V, c.T};
+            HeadTokens tk = {c.labels, c.V, teacher ? c.tidx : nullptr, c.tlogit, c.K, c.V, c.T};
             if (teacher && (long)c.T * c.K > 16384) {
                 tk.act = reinterpret_cast<int32_t*>(ws + p.act);
                 tk.limit = 2, tk.tidx = nullptr;
