@@ -1476,7 +1476,7 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
             if (j < p.K && slot_on(p.tidx, p.tlogit, (long)t * p.K + j, p.V)) {
                 some = true;
                 idx[u] = p.tidx[(long)t * p.K + j];
-                q[u] = p.tlogit[(long)t * p.K + j] * p.inv_tau;
+                q[u] = p.tlogit[(long)t * p.K + j];
                 hi = fmaxf(hi, q[u]);
             }
         }
@@ -1485,9 +1485,11 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
         const float ref = hi > -INFINITY ? hi : 0.0f;      // (NaNs alone: they show)
         float tot = 0.0f;
         float lq[PL];
+        // the difference first: rounded, s / tau would be off by 2^-24 of itself, which at
+        // a low temperature is much in q (1e-3 for a score of 16 at 0.001)
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
-            lq[u] = q[u] - ref;
+            lq[u] = (q[u] - ref) * p.inv_tau;
             q[u] = expf(lq[u]);               // 0 for a slot left out
             tot += q[u];
         }

@@ -141,3 +141,35 @@ def test_low_temperatures(V, tau):
     dz = tau * (logp.exp() - hot)
     tol = tau * (logp.exp() * (e + 4 * u) + 4 * u * hot)
     assert off(res["dWv"].t(), dz, tol) is None
+
+
+@pytest.mark.parametrize("tau", [0.001, 0.01, 0.05, 0.3])
+@pytest.mark.parametrize("K", [2, 12, 100])
+def test_low_temperatures_of_the_teacher(K, tau):
+    """Several slots in fp32.  A slot's ln q has 4 u times its difference from the largest
+    (the difference, the constant 1 / tau, their product) and 24 u of the exponential,
+    the sum of K in a wave, the quotient and the logarithm; q has that and the sum's."""
+    V, far = 400, 15.0
+    banner("head low tau, slots", K, tau)
+    g = torch.Generator().manual_seed(K)
+    z = torch.linspace(1.0, 60.0, D)[:, None] - tau * far * torch.rand(D, V, generator=g)
+    Wv, x = given(z, "f32"), pick(D, "f32")
+    idx = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(D)])
+    score = torch.linspace(-40.0, 16.0, D)[:, None] - tau * far * torch.rand(D, K, generator=g)
+    logp = torch.log_softmax(z.double() / tau, 1)
+    span = z.double().max(1, keepdim=True).values / tau - z.double() / tau
+    ep = sum_error(V, "f32") + u * (8 + 4 * span.max(1, keepdim=True).values + 4 * logp.abs())
+    logq = torch.log_softmax(score.double() / tau, 1)
+    q = logq.exp()
+    wide = (score.double().max(1, keepdim=True).values - score.double()) / tau
+    eq = u * (24 + 4 * wide + 4 * wide.max(1, keepdim=True).values)
+    res = M.moe_head_distill_grad(x, Wv, (idx.to(torch.int32).cuda(), score.cuda()), tau)
+    lp = logp.gather(1, idx)
+    kd = (q * (logq - lp)).sum(1)
+    tol = (q * (eq * (1 + (logq - lp).abs()) + ep.gather(1, idx)
+                + 4 * u * (logq.abs() + lp.abs()))).sum(1)
+    assert off(res["kd"], tau ** 2 * kd, tau ** 2 * tol) is None
+    p, qs = logp.exp(), torch.zeros(D, V, dtype=torch.float64).scatter_(1, idx, q)
+    eqs = torch.zeros(D, V, dtype=torch.float64).scatter_(1, idx, q * eq)
+    tol = tau * (p * ep + eqs + 4 * u * (p + qs))
+    assert off(res["dWv"].t(), tau * (p - qs), tol) is None
