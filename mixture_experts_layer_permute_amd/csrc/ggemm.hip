@@ -1652,7 +1652,7 @@ __global__ __launch_bounds__(256) void lds_probe_kernel(const bf16_t* src, uint3
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t o = ((gw * 8 + j + (uint32_t)it * 8) * 1024 + lane * 16) & win_mask;
-                lds_dma16(rs, o, ldm + j * 1024);
+                lds_dma16(j == 0, rs, o, ldm + j * 1024);
             }
         }
         constexpr int NR = (MODE & 8) != 0 ? 3 : 1;

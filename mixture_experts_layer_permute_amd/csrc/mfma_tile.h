@@ -74,15 +74,23 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // l's bytes at voff land at lds + 16*l.  Issued from inline assembly so that
 // the compiler does not tie every later LDS read to its completion; callers
 // wait on vmcnt themselves (stage_barrier) before reading the stage.
+// The compiler counts no wait states into inline assembly: one between writing
+// m0 and the load that reads it, and five between a vector instruction that
+// writes a scalar register (v_readfirstlane, in rsrc_words) and a load that reads
+// it, which the first load behind a descriptor (FIRST) waits for itself.
+template <bool FIRST>
 __device__ __forceinline__ void lds_dma16(i32x4_t rs, uint32_t voff, uint32_t lds) {
-    // (one wait state between writing m0 and the load that reads it)
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
-        "s_nop 0\n\t"
+        "s_nop %3\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds"
         :
-        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs), "n"(FIRST ? 3 : 0)
         : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma16(bool first, i32x4_t rs, uint32_t voff, uint32_t lds) {
+    if (first) lds_dma16<true>(rs, voff, lds);      // (a constant in an unrolled loop)
+    else lds_dma16<false>(rs, voff, lds);
 }
 
 template <int ROWS, int LAY, int NT, int BK>
@@ -199,7 +207,7 @@ struct DmaOperand {
             const long k = k0 + (w + NW * i) * RB + lane / NC;
             const uint32_t o = ((uint32_t)rows[i] * (uint32_t)(ld * 2) + off[i]) |
                                ((uint32_t)(k >= k_lim) << 31);
-            lds_dma16(rs, o, lds0 + NW * i * 1024);
+            lds_dma16(i == 0, rs, o, lds0 + NW * i * 1024);
         }
     }
 
@@ -216,7 +224,7 @@ struct DmaOperand {
         const i32x4_t rs = rsrc_words(base, nbytes);
         const uint32_t lds0 = lds_addr(stage) + (uint32_t)((threadIdx.x >> 6) * 1024);
 #pragma unroll
-        for (int i = 0; i < NLOAD; ++i) lds_dma16(rs, off[i], lds0 + NW * i * 1024);
+        for (int i = 0; i < NLOAD; ++i) lds_dma16(i == 0, rs, off[i], lds0 + NW * i * 1024);
     }
 };
 

@@ -25,6 +25,16 @@ def found(tmp_path_factory):
     return {s: {n: (b, scan(b)) for n, b in functions(a, r"_ZN3moe\w+")} for s, a in asm.items()}
 
 
+@pytest.fixture(scope="module")
+def found_debug(tmp_path_factory):
+    if not os.path.exists(build.hipcc()):
+        pytest.skip("no hipcc")
+    d = str(tmp_path_factory.mktemp("waits_debug"))
+    with ThreadPoolExecutor(len(SOURCES)) as ex:
+        asm = dict(zip(SOURCES, ex.map(lambda s: device_asm(s, True, d), SOURCES)))
+    return {s: {n: (b, scan(b)) for n, b in functions(a, r"_ZN3moe\w+")} for s, a in asm.items()}
+
+
 def short(found, src, rules):
     return [(n, x) for n, (_, f) in found[src].items() for x in f if x[0] in rules]
 
@@ -39,6 +49,12 @@ def test_a_descriptor_is_there_when_a_load_reads_it(found, src):
 @pytest.mark.parametrize("src", SOURCES)
 def test_m0_is_there_when_a_load_into_lds_reads_it(found, src):
     assert short(found, src, ("m0",)) == []
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_the_debug_build_waits_too(found_debug, src):
+    """Its checks move the registers around."""
+    assert short(found_debug, src, ("sgpr", "m0", "mfma in", "mfma out")) == []
 
 
 def test_matrix_instructions_keep_their_distance_over_a_loops_end_too(found):
