@@ -409,11 +409,14 @@ __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2
 // scores: writing them 1.65 GB to 0.82, the pass that reads them 466 us to 330).  What lies 64
 // or more below (2^-64 of that maximum) counts as 64 below.  The label's own score and the
 // statistics stay fp32.
-// The coding is the hardware's conversion of [0, 1] to 0 .. 65535, clamped and rounded.
+// The coding is the hardware's conversion of [0, 1] to 0 .. 65535, clamped and rounded,
+// of what z L lies below m L itself: x, relative to m' = m L rounded, less rho = m L - m',
+// which is as large as a step of the code for scores above 4000.
 constexpr float kCodeRange = 64.0f, kCodeStep = 64.0f / 65535.0f;
-__device__ __forceinline__ uint32_t code_pair(float lo, float hi) {      // log2, <= 0
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(
-                                            lo * (-1.0f / kCodeRange), hi * (-1.0f / kCodeRange)));
+__device__ __forceinline__ uint32_t code_pair(float lo, float hi, float rho) {
+    constexpr float k = -1.0f / kCodeRange;
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_u16(fmaf(lo, k, -k * rho),
+                                                                       fmaf(hi, k, -k * rho)));
 }
 
 // (fmaxf would first turn signalling NaNs into quiet ones, an instruction each)
@@ -515,7 +518,7 @@ struct EpiScores {
         for (int q = 1; q < 8; ++q) m = max3(max3(m, v[q][0], v[q][1]), v[q][2], v[q][3]);
         m = Lanes::max(m);
         const float ref = m == -INFINITY ? 0.0f : m;   // no column here, or none finite
-        const float m2 = ref * kLog2e;
+        const float m2 = ref * kLog2e, rho = fmaf(ref, kLog2e, -m2);
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t w[8][2];
 #pragma unroll
@@ -529,7 +532,7 @@ struct EpiScores {
             for (int u = 0; u < 4; ++u) s[u] += e[u];
             if (kCodes)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) w[q][u] = code_pair(x[2 * u], x[2 * u + 1]);
+                for (int u = 0; u < 2; ++u) w[q][u] = code_pair(x[2 * u], x[2 * u + 1], rho);
         }
         if (kCodes && code) store_pairs<EDGE>(code + r * ldz + col, in, room, w);
         const float sum = Lanes::sum((s[0] + s[1]) + (s[2] + s[3]));
@@ -1225,6 +1228,7 @@ __global__ __launch_bounds__(1024) void head_scores_join_kernel(HeadGemm<T> p, E
 #pragma unroll
     for (int k = 1; k < W / 8; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
     const float ref = m == -INFINITY ? 0.0f : m, m2 = ref * kLog2e, mt = ref * es.l2t;
+    const float rho = fmaf(ref, kLog2e, -m2);
     float x[8], s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -1234,8 +1238,8 @@ __global__ __launch_bounds__(1024) void head_scores_join_kernel(HeadGemm<T> p, E
     }
     if (W == 128 && es.code && in && c < es.ldz)
         *reinterpret_cast<u32x4_t*>(es.code + r * es.ldz + c) =
-            u32x4_t{code_pair(x[0], x[1]), code_pair(x[2], x[3]), code_pair(x[4], x[5]),
-                    code_pair(x[6], x[7])};
+            u32x4_t{code_pair(x[0], x[1], rho), code_pair(x[2], x[3], rho),
+                    code_pair(x[4], x[5], rho), code_pair(x[6], x[7], rho)};
 #pragma unroll
     for (int k = 1; k < W / 8; k *= 2) {
         s += __shfl_xor(s, k);
@@ -1414,10 +1418,9 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
         if (p.lse) p.lse[t] = label >= 0 ? l : 0.0f;
     }
     if constexpr (CODED) {
-        // every row has a label; dz = w 2^(m' - step * code - log2 of the sum), m' the part's
+        // every row has a label; dz = w 2^(m L - step * code - log2 of the sum), m the part's
         bf16_t* g = static_cast<bf16_t*>(p.G) + (long)r * p.ldg;
         const uint16_t* cr = p.code + (long)r * p.ldz;
-        const float norm = nm.a + nm.b;
         constexpr int U = 4;                  // units of 512 in flight
         for (int c = c0 + lane * 8; c < c1; c += 512 * U) {
             u32x4_t w[U];
@@ -1433,7 +1436,7 @@ __global__ __launch_bounds__(256) void head_dz_kernel(HeadDz p) {
             for (int u = 0; u < U; ++u) {
                 const int cu = c + 512 * u;
                 if (cu >= c1) break;
-                const float b = top[u] * kLog2e - norm;
+                const float b = fmaf(top[u], kLog2e, -nm.a) - nm.b;
                 u32x4_t o, o2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

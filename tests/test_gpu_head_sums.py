@@ -173,3 +173,26 @@ def test_low_temperatures_of_the_teacher(K, tau):
     eqs = torch.zeros(D, V, dtype=torch.float64).scatter_(1, idx, q * eq)
     tol = tau * (p * ep + eqs + 4 * u * (p + qs))
     assert off(res["dWv"].t(), tau * (p - qs), tol) is None
+
+
+@pytest.mark.parametrize("V", [600, 3000])
+def test_gradients_of_very_high_scores(V):
+    """bf16, 64 equal scores of 4000 to 64000 and all others far below (2^-64 of the
+    largest at most, where the 16 bits end): dz of those is
+    1/64, as dWv shows it (x picks).  1/64 has no rounding in bf16, and half a step is
+    2^-9 of it (below it: 2^-10), so that it comes out exactly if the scores' 16 bits
+    (3.4e-4) and what else the exponent is off by stay below that; an exponent that
+    is rounded at the size of the score times log2(e) does not."""
+    banner("head very high scores", V)
+    g = torch.Generator().manual_seed(V)
+    top = torch.linspace(4000.0, 64000.0, D).to(torch.bfloat16).float()
+    z = (top[:, None] * 0.9).expand(D, V).clone()
+    hot = torch.stack([torch.randperm(V, generator=g)[:64] for _ in range(D)])
+    z = z.scatter_(1, hot, top[:, None].expand(D, 64)).to(torch.bfloat16).float()
+    Wv, x = given(z, "bf16"), pick(D, "bf16")
+    labels = hot[:, 0].to(torch.int32).cuda()
+    res = M.moe_head_xent_grad(x, Wv, labels)
+    want = torch.zeros(D, V).scatter_(1, hot, torch.full((D, 64), 1.0 / 64))
+    want.scatter_(1, hot[:, :1], torch.full((D, 1), 1.0 / 64 - 1.0))     # 63/64: 6 bits
+    bad = (~((res["dWv"].t().float().cpu() - want).abs() <= 2.0 ** -64)).nonzero()
+    assert len(bad) == 0, (len(bad), bad[0], float(res["dWv"][bad[0][1], bad[0][0]]))
