@@ -432,9 +432,10 @@ moe_status moe_clip_grads(const void *const *grads, void *const *out,
  *   dx = dz Wv, dWv = dz^T x
  * The scores are never kept whole: the loss alone keeps a maximum and a sum per
  * 128 (fp32: 64) of them, the gradient dz for a piece of tokens, as many as the
- * workspace holds, and the scores of a part of it.  A token whose label lies outside [0,V) (padding, a prompt)
- * has no loss: loss, lse and its row of dx are 0, it adds nothing to dWv, and
- * its row of x is not read.
+ * workspace holds, and the scores of a part of it.  A token whose label lies outside
+ * [0,V) (padding, a prompt) has no loss: loss, lse and its row of dx are 0, it adds
+ * nothing to dWv, and what its row of x holds (NaN, say) reaches no result; the row is
+ * not read, but by a loss alone of up to 256 tokens.
  *   x [T,d] dt, Wv [V,d] dt (row v scores entry v, the layout of an embedding
  *   table, which it may be), labels [T] int32, weight [T] float or NULL (all
  *   ones; the mean over n tokens is 1/n each), loss [T] float, lse [T] float or

@@ -406,7 +406,7 @@ __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2
 // to 2^-9), a score is kept in 16 bits, as how far below the largest of its 128
 // columns it lies, in steps of 64 / 65535 of log2: exp(z) comes back within 2^-11 ln 2 =
 // 3.4e-4, a sixth of that rounding, at half the bytes of fp32 (8192 x 50257
-// scores: writing them 1.65 GB to 0.82, the pass that reads them 466 us to 330).  What lies 64
+// scores: writing them 1.65 GB to 0.82, the pass that reads them 466 us to 298).  What lies 64
 // or more below (2^-64 of that maximum) counts as 64 below.  The label's own score and the
 // statistics stay fp32.
 // The coding is the hardware's conversion of [0, 1] to 0 .. 65535, clamped and rounded,
@@ -958,9 +958,10 @@ __device__ __forceinline__ void head_product_body(const HeadGemm<bf16_t>& p, con
     });
 }
 
-// The scores: 8192 x 50257 from d 1024 900 us with 16-bit scores stored (935
-// TFLOP/s; 16 stages and a 10 us epilogue a tile, pipes busy 42%), 620 for the loss
-// alone; 16 tokens, d 4096, 128000 entries 236 us (Wv at 4.5 TB/s).
+// The scores, on two cards: 8192 x 50257 from d 1024 900 and 935 us with 16-bit scores
+// stored (935 and 900 TFLOP/s; 16 stages and a 10 us epilogue a tile, pipes busy 42%), a
+// tenth masked and the loss alone 620 and 645; 16 tokens, d 4096, 128000 entries 228-236
+// us (Wv at 4.6 TB/s).
 template <int ALAY, int BLAY, class Epi>
 __global__ __launch_bounds__(256, 1) void head_product_kernel(HeadGemm<bf16_t> p, Epi epi) {
     __shared__ __attribute__((aligned(UNIT))) uint8_t ringbuf[kRingBytes];
@@ -1126,8 +1127,9 @@ __global__ __launch_bounds__(256, 2) void head_product_f32_kernel(HeadGemm<float
 }
 
 // Bound by the matrix pipes and the power they draw: 68% of their cycles busy at
-// 1.9 GHz; 8192 tokens, d 1024, 50257 entries 1200 us (1405 TFLOP/s), 16384, 4096,
-// 128000 23.7 ms (1450); fp32 1999, 1088, 8191 650 us (104).
+// 1.9 GHz; on two cards 8192 tokens, d 1024, 50257 entries 1200 and 1267 us (1405 and
+// 1331 TFLOP/s), 16384, 4096, 128000 23.7 and 24.8 ms (1450 and 1384); fp32 1999, 1088,
+// 8191 618-650 us (104-110).
 // Both gradients' products in one launch: blocks 0 .. nx - 1 make dx = dz Wv, the
 // others dWv = dz^T x, so that the second fills the rounds that the first leaves.
 __global__ __launch_bounds__(256, 1) void head_grads_kernel(HeadGemm<bf16_t> gx,
@@ -1378,8 +1380,8 @@ struct HeadDz {
     int grad;
 };
 
-// Bound by HBM: 8192 x 50257 in bf16 from coded scores 290 us (1.65 GB, 5.7 TB/s), with
-// a teacher from fp32 ones 520 us (2.5 GB, 4.8 TB/s; two exponentials an entry).
+// Bound by HBM: 8192 x 50257 in bf16 from coded scores 298 us (1.65 GB, 5.5 TB/s), with
+// a teacher from fp32 ones 533 us (2.5 GB, 4.7 TB/s; two exponentials an entry).
 // One wave a row, or a segment of one when the rows are few.  The dz of the label
 // and the teacher's slots are written behind the others (an entry named twice by
 // its first slot, with the slots' q added in order).
@@ -1623,7 +1625,7 @@ inline long head_slots(long tiles, long K, bool f32) {
 }
 
 // Parts of the scores' tiles: few tiles with a long reduction would leave most
-// compute units idle.  A stage takes 1.2 us, the parts' way through memory and the
+// compute units idle.  A stage takes 1.2 us (fp32: 1.7), the parts' way through memory and the
 // second launch about 12 (scores, one part / split: fp32 12 tokens, d 3712, 587
 // entries 145 us / 29; 500, 1536, 2000 120 / 74; bf16 12, 3968, 2151 82 / 28; 1000, 2048,
 // 2000 55 / 43; 16, 1536, 16000 40 / 30).

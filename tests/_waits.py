@@ -96,41 +96,44 @@ def blocks(body):
     return res
 
 
-def step(state, i, found):
-    """The distances behind instruction i; those too short on the way go to `found`.
-    state: (kind of writer, register) -> (wait states since, inline, line, passes)."""
+def walk(ins, entry, found=None):
+    """Through a block's instructions from the distances at its entry to those at its
+    end; those too short on the way go to `found`.  A distance: (kind of writer,
+    register) -> (wait states since, inline, line, wait of a matrix instruction)."""
+    now = 0
+    state = {k: (-w[0],) + w[1:] for k, w in entry.items()}
+
     def near(kind, r, rule, least):
         w = state.get((kind, r))
-        if found is None or w is None or not (w[1] or i.inline):
+        if w is None or not (w[1] or i.inline) or now - w[0] >= FAR:
             return
-        least = w[3] if least is None else least
-        found.least[rule] = min(found.least.get(rule, FAR), w[0])
-        if w[0] < least:
-            found.append((rule, w[0], least, w[2], i.line))
-    if i.vmem:
-        for r in i.reads:
-            if r[0] in ("s", "vcc", "m0"):
-                near("valu", r, "sgpr", SGPR_TO_VMEM)
-    if i.lds_load:
-        near("salu", ("m0", 0), "m0", M0_TO_LDS_LOAD)
-    if i.mfma:
-        for r in i.reads:
-            near("valu", r, "mfma in", VALU_TO_MFMA)
-    elif i.valu or i.vmem or i.op.startswith("ds_"):
-        for r in i.reads + i.writes:
-            near("mfma", r, "mfma out", None)
-    for k in list(state):
-        d = state[k][0] + i.states
-        if d < FAR:
-            state[k] = (d,) + state[k][1:]
-        else:
-            del state[k]
-    kind = "valu" if i.valu else "mfma" if i.mfma else "salu" if i.op.startswith("s_") else None
-    for r in i.writes:
-        for other in ("valu", "salu", "mfma"):
-            state.pop((other, r), None)
-        if kind:
-            state[(kind, r)] = (0, i.inline, i.line, i.wait)
+        d, least = now - w[0], w[3] if least is None else least
+        found.least[rule] = min(found.least.get(rule, FAR), d)
+        if d < least:
+            found.append((rule, d, least, w[2], i.line))
+
+    for i in ins:
+        if found is not None:
+            if i.vmem:
+                for r in i.reads:
+                    if r[0] in ("s", "vcc", "m0"):
+                        near("valu", r, "sgpr", SGPR_TO_VMEM)
+            if i.lds_load:
+                near("salu", ("m0", 0), "m0", M0_TO_LDS_LOAD)
+            if i.mfma:
+                for r in i.reads:
+                    near("valu", r, "mfma in", VALU_TO_MFMA)
+            elif i.valu or i.vmem or i.op.startswith("ds_"):
+                for r in i.reads + i.writes:
+                    near("mfma", r, "mfma out", None)
+        now += i.states
+        kind = "valu" if i.valu else "mfma" if i.mfma else "salu" if i.op.startswith("s_") else None
+        for r in i.writes:
+            for other in ("valu", "salu", "mfma"):
+                state.pop((other, r), None)
+            if kind:
+                state[(kind, r)] = (now, i.inline, i.line, i.wait)
+    return {k: (now - w[0],) + w[1:] for k, w in state.items() if now - w[0] < FAR}
 
 
 class Found(list):
@@ -147,26 +150,18 @@ def scan(blks):
     todo = [0]
     while todo:
         n = todo.pop()
-        state = dict(entry[n])
-        for i in blks[n][0]:
-            step(state, i, None)
+        state = walk(blks[n][0], entry[n])
         for a in blks[n][1]:
             if entry[a] is None:
                 entry[a] = dict(state)
                 todo.append(a)
                 continue
-            changed = False
-            for k, w in state.items():
-                if k not in entry[a] or w[0] < entry[a][k][0]:
-                    entry[a][k] = w
-                    changed = True
-            if changed:
+            nearer = {k: w for k, w in state.items() if k not in entry[a] or w[0] < entry[a][k][0]}
+            if nearer:
+                entry[a].update(nearer)
                 todo.append(a)
     found = Found()
-    for n, (ins, _) in enumerate(blks):
-        if entry[n] is None:
-            continue
-        state = dict(entry[n])
-        for i in ins:
-            step(state, i, found)
+    for (ins, _), state in zip(blks, entry):
+        if state is not None:
+            walk(ins, state, found)
     return found

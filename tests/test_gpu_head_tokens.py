@@ -34,6 +34,20 @@ def test_a_token_whose_slots_score_minus_infinity_is_left_out(T):
         check(M.moe_head_distill(dirty, Wv, teacher[:2], 1.5, lab), ref)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 100, 256])
+def test_the_loss_alone_of_few_tokens_passes_over_nan_rows(T, dt):
+    """Up to 256 tokens every row is scored, those without a label too: nothing of
+    them reaches another row."""
+    d, V = 192, 701
+    banner("head NaN rows", T, dt)
+    x, Wv, labels, _, _ = inputs(T, d, V, dt, seed=T)
+    labels[::3] = -1
+    want = reference(x, Wv, labels, dt=dt)
+    x[::3] = float("nan")
+    check(M.moe_head_xent(x, Wv, labels), want)
+
+
 @pytest.mark.parametrize("K", [1, 70])
 def test_a_teachers_nan_shows(K):
     """In the token that has it, whether its other slots have scores or not, and in
